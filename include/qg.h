@@ -448,6 +448,86 @@ qg_status qg_sample(const float* logits, int B, int V, const int32_t* past, int 
                     int32_t* out, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged K/V cache (no counterpart on the pages: what several users' decodes
+ * need beside the contiguous cache of qg_decode_attention)
+ *
+ * A pool of pages of page_size tokens for one layer; page_table row b lists
+ * sequence b's pages in order, so token t of sequence b is row
+ * t % page_size of page page_table[b][t / page_size]. Pages hold bf16
+ * values, or int8 codes with one fp32 scale per (page, head, block of
+ * QG_KV_BLOCK tokens), K and V each: value = code * scale.
+ *
+ * Packed rows: the calls below take the rows of all sequences one after
+ * another, T rows in all; sequence b owns rows row_start[b] ..
+ * row_start[b+1] - 1 (n_b of them, 0 allowed). kv_len[b] counts its cached
+ * tokens with these rows included: its i-th row is token kv_len[b] - n_b + i.
+ * row_start NULL means one row each (T = B). Rows outside every sequence (a
+ * padded batch) are neither read nor written. Row starts and lengths are
+ * read on the device; row starts must not decrease and are clamped to
+ * [0, T].
+ * ---------------------------------------------------------------------- */
+#define QG_KV_BLOCK 16
+typedef enum qg_kv_dtype { QG_KV_BF16 = 0, QG_KV_INT8 = 1 } qg_kv_dtype;
+
+typedef struct qg_paged_kv {
+  void* k_pages;    /* device [num_pages][kv_heads][page_size][head_dim] */
+  void* v_pages;    /* as k_pages */
+  float* k_scales;  /* device fp32 [num_pages][kv_heads][page_size/16], int8 only (4-byte align) */
+  float* v_scales;  /* as k_scales */
+  int num_pages, page_size, kv_heads, head_dim;
+  qg_kv_dtype dtype;
+} qg_paged_kv;
+
+/* Per-head RMSNorm and NeoX rotation of q and k, and the append of k and v
+ * to a paged cache, in one launch.
+ *
+ * q and k rows: x_i <- x_i / sqrt(mean(x^2) + eps) * w_i per head when the
+ * norm weight is given, then qg_rope_neox's rotation at the row's token
+ * index. The rotated q goes to q_out; k, and v as it is, to the cache.
+ * bf16 pages: rounded to nearest even.
+ * int8 pages, for each block of 16 tokens that gets rows: let o be the first
+ * such row's place in the block (0..15) and s_old the block's scale if
+ * o > 0, else 0. The new scale is s = max(s_old, max|x| / 127) over the new
+ * rows' values of that head. The rows before o are brought to it, code <-
+ * rint(code * (s_old / s)) (half a step of s at most per change), and the
+ * new rows get code = clamp(rint(x / s), -127, 127) (0 where s is 0). Rows
+ * after the new ones stay as they are. A NaN or infinite value, or a NaN
+ * s_old, makes s NaN, and with it every value of the block until a call
+ * writes the block from its first row again.
+ *
+ * page_table device int32 [B][max_pages]; only entries of tokens that get
+ *            rows are read. A page outside [0, num_pages): its K/V rows are
+ *            dropped (q_out is written).
+ * kv_len     device int32 [B]. Outside [n_b, max_pages * page_size]: nothing
+ *            of the sequence is written, q_out included.
+ * row_start  device int32 [B+1], or NULL (see above).
+ * q, k, v    device, of x_dtype; row r at r * q_ld (k_ld, v_ld) elements,
+ *            its heads one after another. q NULL with H = 0: k and v alone.
+ * q_norm, k_norm device bf16 [head_dim] or NULL (2-byte alignment).
+ * rotary_dim in [0, head_dim], a multiple of head_dim / 16; 0: no rotation.
+ * q_out      device [T][H * head_dim] of q_out_dtype; may be q itself when
+ *            the types match and q_ld = H * head_dim.
+ * Pages that get rows must not be shared by two sequences of the call.
+ * Angles are formed in float64 and reduced there; sine and cosine are fp32.
+ * q, k, v rows must start on 16 bytes; B, T, H >= 0, max_pages >= 0. */
+qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
+                             const int32_t* kv_len, const int32_t* row_start, const void* q,
+                             long long q_ld, const void* k, long long k_ld, const void* v,
+                             long long v_ld, qg_dtype x_dtype, const uint16_t* q_norm,
+                             const uint16_t* k_norm, float eps, double theta, int rotary_dim,
+                             void* q_out, qg_dtype q_out_dtype, int B, int T, int H,
+                             void* stream);
+
+/* Cached rows back as values: packed row i of sequence b is its token
+ * first[b] + i (first NULL: 0). k_out, v_out device [T][kv_heads * head_dim]
+ * of out_dtype (either may be NULL). A token index outside
+ * [0, max_pages * page_size) or a page outside [0, num_pages) gives NaN.
+ * row_start as above, NULL: one row each. */
+qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
+                             const int32_t* first, const int32_t* row_start, void* k_out,
+                             void* v_out, qg_dtype out_dtype, int B, int T, void* stream);
+
+/* ------------------------------------------------------------------------
  * Code predictor  [MK: makima src/tts/qwen3/code_predictor.rs,
  * CodePredictor::predict and CodePredictorLayer::forward]
  *

@@ -882,3 +882,84 @@ def prefix_forward(cfg, weights, token_ids):
         x = x + gemv_affine8(*lw["down"], hmid)
     xn = round_bf16(rmsnorm(x, weights["final_norm"], eps))
     return gemv_affine8(ew, es, eb, xn)
+
+
+# ---------------------------------------------------------------------------
+# Serving operators (no counterpart on the pages; the definitions are those
+# of include/qg.h): the int8 block of a paged cache, attention of several
+# rows over cached keys, filtered sampling.
+# ---------------------------------------------------------------------------
+
+KV_BLOCK = 16
+
+
+def kv_block_append(codes, s_old, o, x):
+    """Append rows ``x [n, D]`` (float64) at place ``o`` of an int8 block
+    ``codes [16, D]`` with scale ``s_old``: (codes after, scale after). The
+    scale is max(s_old, max|x| / 127), without s_old when o = 0; rows before
+    o are requantised to it, rows after the new ones stay. Non-finite values
+    or a NaN s_old give a NaN scale (codes of the written rows are then
+    unspecified: 0 here)."""
+    codes = np.array(codes, dtype=np.int64)
+    x = np.asarray(x, dtype=np.float64)
+    n = x.shape[0]
+    s_old = float(s_old) if o > 0 else 0.0
+    if not np.isfinite(x).all() or math.isnan(s_old):
+        codes[:o + n] = 0
+        return codes, math.nan
+    s = max(s_old, float(np.abs(x).max(initial=0.0)) / 127.0)
+    if s > 0.0:
+        codes[:o] = np.rint(codes[:o] * (s_old / s))
+        codes[o:o + n] = np.clip(np.rint(x / s), -127, 127)
+    else:
+        codes[:o + n] = 0
+    return codes, s
+
+
+def rows_attention(q, k, v, H, Hkv, D, scale=None):
+    """Causal attention of a sequence's last n rows over its L cached tokens
+    (theirs included): q ``[n, H*D]``, k and v ``[Hkv, L, D]``; row i sees
+    tokens 0 .. L - n + i. One ``decode_attention`` per row."""
+    n, L = q.shape[0], k.shape[1]
+    return np.stack([decode_attention(q[i], k, v, L - n + i + 1, H, Hkv, D, scale)
+                     for i in range(n)]) if n else np.zeros((0, H * D))
+
+
+def sample_filtered(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, kept, log-probability) of one row, in float64, by sorting: the
+    candidates are the values that are not NaN and above -inf, by value
+    descending, equal values by index; weights exp((l - max) / temperature)
+    (1 for +inf when the maximum is +inf, 0 for the rest then). Kept: the
+    first top_k (0 or less: all), of these while the weight before a
+    candidate is below top_p times theirs (1 or more: all; the first always),
+    and weights of at least min_p (above 1: as 1). The token is the first kept candidate whose
+    running weight reaches u times the kept weight. A temperature of 0 or
+    less keeps the first alone. No candidate: (0, 0, nan)."""
+    l = np.asarray(logits, dtype=np.float64)
+    idx = np.flatnonzero(~np.isnan(l) & (l > -np.inf))
+    if idx.size == 0:
+        return 0, 0, math.nan
+    order = idx[np.lexsort((idx, -l[idx]))]
+    top = l[order[0]]
+    if not temperature > 0:
+        return int(order[0]), 1, 0.0
+    if np.isinf(top):
+        w = (l[order] == top).astype(np.float64)
+    else:
+        w = np.exp((l[order] - top) / float(temperature))
+    kept = order.size
+    if top_k > 0:
+        kept = min(kept, int(top_k))
+    if top_p < 1:
+        run = np.cumsum(w[:kept])
+        before = run - w[:kept]
+        before[1:] = run[:-1]
+        inside = before < float(top_p) * run[-1]
+        inside[0] = True
+        kept = int(inside.sum())
+    if min_p > 0:
+        kept = int((w[:kept] >= min(1.0, float(min_p))).sum())
+    run = np.cumsum(w[:kept])
+    target = min(max(float(u), 0.0), 1.0) * run[-1]
+    j = min(int((run < target).sum()), kept - 1)
+    return int(order[j]), kept, math.log(w[j] / run[-1]) if w[j] > 0 else -math.inf

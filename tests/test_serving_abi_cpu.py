@@ -1,0 +1,101 @@
+"""Refusals of the serving entry points before any launch (no GPU needed):
+each names the argument at fault."""
+import ctypes
+
+import pytest
+import torch
+
+import weight_only_quantized_03_b200 as qg
+
+FAKE = 0x7F0000000000  # aligned, never dereferenced
+
+
+def _status(name, *args):
+    st = getattr(qg.lib, name)(*args)
+    return st, qg.last_error()
+
+
+def _kv(**kw):
+    f = dict(k_pages=FAKE, v_pages=FAKE, k_scales=FAKE, v_scales=FAKE, num_pages=10, page_size=64,
+             kv_heads=2, head_dim=128, dtype=qg.QG_KV_INT8)
+    f.update(kw)
+    return qg.qg_paged_kv(**f)
+
+
+def _append(kv=None, **kw):
+    a = dict(table=FAKE, max_pages=4, kv_len=FAKE, row_start=None, q=FAKE, q_ld=512, k=FAKE,
+             k_ld=256, v=FAKE, v_ld=256, xdt=qg.QG_F32, qn=None, kn=None, eps=1e-6, theta=1e6,
+             rd=128, qo=FAKE, qdt=qg.QG_BF16, B=2, T=2, H=4)
+    a.update(kw)
+    ref = ctypes.byref(kv if kv is not None else _kv())
+    return _status("qg_paged_kv_append", ref, *a.values(), None)
+
+
+def test_pool_refusals_name_the_field():
+    U, I, M = qg.QG_ERR_UNSUPPORTED_SHAPE, qg.QG_ERR_INVALID_ARGUMENT, qg.QG_ERR_MISALIGNED
+    for kv, code, word in ((_kv(head_dim=96), U, "head_dim=96"), (_kv(page_size=24), U, "page_size=24"),
+                           (_kv(page_size=0), U, "page_size=0"), (_kv(kv_heads=0), U, "kv_heads=0"),
+                           (_kv(dtype=3), I, "dtype=3"), (_kv(num_pages=-1), U, "num_pages=-1"),
+                           (_kv(k_pages=None), I, "k_pages"), (_kv(v_pages=FAKE + 8), M, "v_pages"),
+                           (_kv(k_scales=None), I, "k_scales"), (_kv(v_scales=FAKE + 2), M, "scales")):
+        st, msg = _append(kv)
+        assert st == code and word in msg, (st, msg)
+        st, msg = _status("qg_paged_kv_gather", ctypes.byref(kv), FAKE, 4, FAKE, None, FAKE, FAKE,
+                          qg.QG_F32, 2, 2, None)
+        assert st == code and word in msg, (st, msg)
+    assert _status("qg_paged_kv_append", None, *([0] * 0), FAKE, 4, FAKE, None, None, 0, FAKE, 256,
+                   FAKE, 256, 0, None, None, 1e-6, 1e6, 0, None, 0, 1, 1, 0, None)[0] == I
+    st, msg = _append(max_pages=1 << 28)
+    assert st == U and "max_pages" in msg
+
+
+def test_append_refusals():
+    U, I, M = qg.QG_ERR_UNSUPPORTED_SHAPE, qg.QG_ERR_INVALID_ARGUMENT, qg.QG_ERR_MISALIGNED
+    for kw, code, word in ((dict(T=3), U, "row_start"), (dict(B=-1), U, "B=-1"),
+                           (dict(xdt=5), I, "x_dtype=5"), (dict(qdt=5), I, "q_out_dtype=5"),
+                           (dict(rd=130), U, "rotary_dim=130"), (dict(rd=12), U, "rotary_dim=12"),
+                           (dict(theta=0.0), I, "theta"), (dict(table=None), I, "page_table"),
+                           (dict(kv_len=None), I, "kv_len"), (dict(k=None), I, "k or v"),
+                           (dict(q=None), I, "q"), (dict(qo=None), I, "q_out"),
+                           (dict(k_ld=128), U, "k_ld=128"), (dict(v_ld=258), M, "k or v"),
+                           (dict(k=FAKE + 8), M, "k or v"), (dict(q_ld=514), M, "q or q_out"),
+                           (dict(qo=FAKE + 4), M, "q_out"), (dict(row_start=FAKE + 2), M, "row_start")):
+        st, msg = _append(**kw)
+        assert st == code and word in msg, (kw, st, msg)
+    # empty work launches nothing
+    assert _append(B=0, T=0, k=None)[0] == qg.QG_OK
+    assert _append(row_start=FAKE, T=0)[0] == qg.QG_OK
+
+
+def test_gather_refusals():
+    ref = ctypes.byref(_kv())
+    g = lambda *a: _status("qg_paged_kv_gather", ref, *a, None)
+    assert g(FAKE, 4, FAKE, None, FAKE, FAKE, qg.QG_F32, 2, 3)[0] == qg.QG_ERR_UNSUPPORTED_SHAPE
+    assert g(FAKE, 4, FAKE, None, FAKE, FAKE, 9, 2, 2)[0] == qg.QG_ERR_INVALID_ARGUMENT
+    assert g(None, 4, FAKE, None, FAKE, FAKE, 0, 2, 2)[0] == qg.QG_ERR_INVALID_ARGUMENT
+    assert g(FAKE, 4, FAKE, None, FAKE + 8, None, 0, 2, 2)[0] == qg.QG_ERR_MISALIGNED
+    assert g(FAKE, 4, FAKE, None, None, None, 0, 2, 2)[0] == qg.QG_OK
+
+
+def test_python_refusals():
+    """The binding refuses host tensors, layouts and types that the C side
+    could not see."""
+    pages = lambda dt: torch.zeros((2, 1, 16, 64), dtype=dt)
+    with pytest.raises(TypeError):
+        qg.PagedKV(pages(torch.float16), pages(torch.float16))
+    with pytest.raises(ValueError, match="k_scales"):
+        qg.PagedKV(pages(torch.int8), pages(torch.int8))
+    with pytest.raises(ValueError, match="v_scales"):
+        qg.PagedKV(pages(torch.int8), pages(torch.int8), torch.zeros(2, 1, 1), torch.zeros(2, 1, 2))
+    with pytest.raises(ValueError, match="contiguous"):
+        t = torch.zeros((2, 16, 1, 64), dtype=torch.bfloat16).transpose(1, 2).expand(2, 3, 16, 64)
+        qg.PagedKV(t, t)
+    with pytest.raises(ValueError, match="one type"):
+        qg.PagedKV(pages(torch.bfloat16), pages(torch.int8))
+    with pytest.raises(ValueError, match="unit stride"):
+        qg._rows_of("k", torch.zeros(64, 4).t(), 64)
+    assert qg._rows_of("k", torch.zeros(4, 96)[:, 32:], 64) == 96
+    with pytest.raises(ValueError, match="int32"):
+        qg._int32(kv_len=torch.zeros(3))
+    with pytest.raises(ValueError, match="cpu"):
+        qg._on_device(0, k=torch.zeros(3))

@@ -35,12 +35,16 @@ QG_ERR_CUDA = 5
 QG_ERR_TIMEOUT = 6
 QG_F32 = 0
 QG_BF16 = 1
+QG_KV_BF16 = 0
+QG_KV_INT8 = 1
+QG_KV_BLOCK = 16
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _d = ctypes.c_double
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 class QGError(RuntimeError):
@@ -77,6 +81,12 @@ class qg_whisper_layer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("ln1_g", "ln1_b", "q", "q_b", "k", "v", "v_b", "o", "o_b", "ln2_g", "ln2_b",
                  "fc1", "fc1_b", "fc2", "fc2_b")]
+
+
+class qg_paged_kv(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scales", _vp), ("v_scales", _vp),
+                ("num_pages", _i), ("page_size", _i), ("kv_heads", _i), ("head_dim", _i),
+                ("dtype", _i)]
 
 
 class qg_code_predictor_weights(ctypes.Structure):
@@ -145,6 +155,9 @@ _SIGS = {
     "qg_token_logprob": (_i, [_vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "qg_sample_workspace_size": (_sz, [_i, _i, _i]),
     "qg_sample": (_i, [_vp, _i, _i, _vp, _i, _f, _f, _i, _vp, _vp, _vp, _sz, _vp]),
+    "qg_paged_kv_append": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp,
+                                _f, _d, _i, _vp, _i, _i, _i, _i, _vp]),
+    "qg_paged_kv_gather": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
     "qg_step_graphs_enable": (None, [_i]),
     "qg_step_graphs_clear": (None, []),
     "qg_argmax_workspace_size": (_sz, [_i, _i]),
@@ -367,6 +380,144 @@ def qg_dequant_affine8_g64(w, scales, biases, out, stream=None):
 def qg_dequant_q4_0(blocks, out, stream=None):
     _call("qg_dequant_q4_0", _p(blocks), _p(out), blocks.shape[0], blocks.shape[1] // 18 * 32,
           _stream(stream))
+
+
+# ------------------------------------------------------------ paged cache ----
+
+def _on_device(dev, **tensors):
+    """Every given tensor lives on CUDA device ``dev`` (an index)."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+
+
+def _int32(**tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+
+
+def _rows_of(name, t, width):
+    """Row stride (elements) of [rows, width] whose rows may lie apart."""
+    if t.dim() != 2 or t.shape[1] != width or (t.shape[0] and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, {width}] with unit stride along a row, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+class PagedKV:
+    """A pool of K/V pages of one layer (``qg_paged_kv``): ``k_pages`` and
+    ``v_pages`` [num_pages, kv_heads, page_size, head_dim], bfloat16, or int8
+    with fp32 ``k_scales`` and ``v_scales`` [num_pages, kv_heads,
+    page_size / 16]. The tensors are borrowed and kept alive."""
+
+    def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+            raise ValueError("k_pages and v_pages must be [num_pages, kv_heads, page_size, "
+                             "head_dim] of one type")
+        if k_pages.dtype not in (torch.bfloat16, torch.int8):
+            raise TypeError(f"pages must be bfloat16 or int8, not {k_pages.dtype}")
+        P, Hkv, size, D = k_pages.shape
+        int8 = k_pages.dtype == torch.int8
+        for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if (s is not None) != int8:
+                raise ValueError(f"{name} goes with int8 pages only, and they need it")
+            if int8 and (s.dtype != torch.float32 or s.shape != (P, Hkv, size // QG_KV_BLOCK)
+                         or not s.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous fp32 "
+                                 f"[{P}, {Hkv}, {size // QG_KV_BLOCK}]")
+        if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+            raise ValueError("k_pages and v_pages must be contiguous")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = (k_pages, v_pages, k_scales,
+                                                                    v_scales)
+        self.kv_heads, self.page_size, self.head_dim = Hkv, size, D
+        self.c_kv = qg_paged_kv(_p(k_pages), _p(v_pages), _p(k_scales), _p(v_scales), P, size, Hkv,
+                                D, QG_KV_INT8 if int8 else QG_KV_BF16)
+        self._ref = ctypes.byref(self.c_kv)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype=torch.int8, device="cuda"):
+        """A pool of new pages (contents not initialised)."""
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        pages = [torch.empty(shape, dtype=dtype, device=device) for _ in range(2)]
+        if dtype == torch.int8:
+            pages += [torch.empty(shape[:2] + (page_size // QG_KV_BLOCK,), device=device)
+                      for _ in range(2)]
+        return cls(*pages)
+
+    def _batch(self, page_table, lens, row_start, T, dev):
+        """B, after checking the batch's index tensors."""
+        _on_device(dev, k_pages=self.k_pages, v_pages=self.v_pages, k_scales=self.k_scales,
+                   v_scales=self.v_scales, page_table=page_table, row_start=row_start)
+        _int32(page_table=page_table, row_start=row_start)
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [B, max_pages]")
+        B = page_table.shape[0]
+        if lens is not None:
+            _on_device(dev, kv_len=lens)
+            _int32(kv_len=lens)
+            if lens.numel() != B:
+                raise ValueError(f"{lens.numel()} lengths for {B} sequences")
+        if row_start is not None and row_start.numel() != B + 1:
+            raise ValueError(f"row_start must have {B + 1} entries")
+        if row_start is None and T != B:
+            raise ValueError(f"{T} rows of {B} sequences need row_start")
+        return B
+
+
+def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_out=None,
+                       q_norm=None, k_norm=None, eps=1e-6, theta=1e6, rotary_dim=None,
+                       stream=None):
+    """Norm (optional) and rotate q [T, H*D] and k [T, Hkv*D], append k and v
+    to the pages of ``kv`` (a PagedKV) and write the rotated q to q_out
+    [T, H*D] (fp32 or bf16; q itself if the types match). Rows of q, k and v
+    (fp32 or bf16, one type) may lie apart, as slices of one projection do.
+    page_table int32 [B, max_pages]; kv_len int32 [B] counts the new rows;
+    row_start int32 [B+1], or None for one row per sequence. ``rotary_dim``
+    None: the whole head."""
+    dev = torch.cuda.current_device()
+    D, W, T = kv.head_dim, kv.kv_heads * kv.head_dim, k.shape[0]
+    _on_device(dev, q=q, k=k, v=v, q_out=q_out, q_norm=q_norm, k_norm=k_norm)
+    B = kv._batch(page_table, kv_len, row_start, T, dev)
+    if kv_len is None:
+        raise ValueError("kv_len is needed")
+    k_ld, v_ld = _rows_of("k", k, W), _rows_of("v", v, W)
+    if v.shape[0] != T or v.dtype != k.dtype:
+        raise ValueError("v must have k's rows and type")
+    H, q_ld, qdt = 0, 0, QG_BF16
+    if q is not None:
+        if q.dim() != 2 or q.shape[0] != T or q.dtype != k.dtype or q.shape[1] % D:
+            raise ValueError(f"q must be [{T}, H * {D}] of k's type")
+        H, q_ld = q.shape[1] // D, _rows_of("q", q, q.shape[1])
+        if q_out is None or q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous with q's shape")
+        qdt = _dt(q_out)
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None and (w.numel() != D or w.element_size() != 2 or not w.is_contiguous()):
+            raise ValueError(f"{name} must be {D} bf16 values")
+    _call("qg_paged_kv_append", kv._ref, _p(page_table), page_table.shape[1], _p(kv_len),
+          _p(row_start), _p(q), q_ld, _p(k), k_ld, _p(v), v_ld, _dt(k), _p(q_norm), _p(k_norm),
+          eps, theta, D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
+          _stream(stream))
+
+
+def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None, stream=None):
+    """Cached rows as values: packed row i of sequence b is its token
+    first[b] + i (first int32 [B] or None: from 0; row_start int32 [B+1] or
+    None: one row each). k_out, v_out contiguous [T, Hkv*D], fp32 or bf16."""
+    dev = torch.cuda.current_device()
+    W = kv.kv_heads * kv.head_dim
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        return
+    _on_device(dev, k_out=k_out, v_out=v_out)
+    T = outs[0].shape[0]
+    B = kv._batch(page_table, first, row_start, T, dev)
+    for t in outs:
+        if t.shape != (T, W) or t.dtype != outs[0].dtype or not t.is_contiguous():
+            raise ValueError(f"k_out and v_out must be contiguous [{T}, {W}] of one type")
+    _call("qg_paged_kv_gather", kv._ref, _p(page_table), page_table.shape[1], _p(first),
+          _p(row_start), _p(k_out), _p(v_out), _dt(outs[0]), B, T, _stream(stream))
 
 
 # ---------------------------------------------------------- decode step ----

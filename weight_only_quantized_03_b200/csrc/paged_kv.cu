@@ -1,0 +1,573 @@
+// Appending to a paged K/V cache with the per-head RMSNorm and the NeoX
+// rotation applied on the way, and reading cached rows back as values
+// (include/qg.h, "Paged K/V cache", states both).
+//
+// Append. A CTA owns one block of 16 tokens of one sequence, the unit that
+// shares a scale of an int8 page: whoever writes a row of it has to see all
+// its new rows (for their maximum) and may have to bring the block's earlier
+// rows to a larger scale. Its warps take (q, K or V; head) items: a lane
+// holds D/32 neighbouring values of each of the block's rows in registers,
+// so the norm's sum, the rotation's partner (D/2 away: another lane) and the
+// block's maximum are warp shuffles, and each value is read once and written
+// once. The (cos, sin) pairs of the block's tokens are formed once per CTA
+// in shared memory and serve all heads.
+//
+// The mapping of CTAs to (sequence, block) needs no host knowledge of the
+// lengths: n rows touch at most n/16 + 2 blocks, so slot ranges
+// [row_start[b]/16 + 2b, row_start[b+1]/16 + 2(b+1)) are wide enough for
+// every sequence and do not overlap.
+#include "paged_kv.cuh"
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+namespace qg {
+namespace pk {
+
+constexpr int kWarps = 8;
+constexpr int kMaxHalf = 128;  // rotated pairs of the widest head
+
+struct AppendParams {
+  uint8_t* kp;
+  uint8_t* vp;
+  float* ks;
+  float* vs;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* row_start;
+  const uint8_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  long long q_ld, k_ld, v_ld;
+  const uint16_t* qn;
+  const uint16_t* kn;
+  void* qo;
+  int q_bf16;
+  float eps;
+  int half;  // rotated pairs
+  int B, T, H, Hkv, page_size, max_pages, num_pages;
+  double turns[kMaxHalf];  // angle of pair i at position 1, in units of pi
+};
+
+// EPL consecutive values of a row, fp32 or bf16, as fp32.
+template <int EPL, bool XF32>
+__device__ __forceinline__ void load_vals(const uint8_t* p, float (&x)[EPL]) {
+  if constexpr (XF32) {
+    if constexpr (EPL == 2) {
+      const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
+      x[0] = t.x;
+      x[1] = t.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) {
+        const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + j / 4);
+        x[j] = t.x;
+        x[j + 1] = t.y;
+        x[j + 2] = t.z;
+        x[j + 3] = t.w;
+      }
+    }
+  } else {
+    uint32_t w[EPL / 2];
+    if constexpr (EPL == 2) {
+      w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (EPL == 4) {
+      const uint2 t = __ldcg(reinterpret_cast<const uint2*>(p));
+      w[0] = t.x;
+      w[1] = t.y;
+    } else {
+      const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
+      w[0] = t.x;
+      w[1] = t.y;
+      w[2] = t.z;
+      w[3] = t.w;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL / 2; ++j) {
+      x[2 * j] = bf16_lo(w[j]);
+      x[2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+
+template <int EPL>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float (&x)[EPL]) {
+  uint32_t w[EPL / 2];
+#pragma unroll
+  for (int j = 0; j < EPL / 2; ++j)
+    w[j] = (uint32_t)f32_to_bf16_bits(x[2 * j]) | ((uint32_t)f32_to_bf16_bits(x[2 * j + 1]) << 16);
+  if constexpr (EPL == 2)
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+  else if constexpr (EPL == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int EPL>
+__device__ __forceinline__ void store_f32(float* p, const float (&x)[EPL]) {
+  if constexpr (EPL == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4)
+      *reinterpret_cast<float4*>(p + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+  }
+}
+
+// EPL int8 codes as packed words (the last half unused for EPL = 2).
+template <int EPL>
+__device__ __forceinline__ void load_codes(const uint8_t* p, int (&c)[EPL]) {
+  uint32_t w[2] = {0, 0};
+  if constexpr (EPL == 2)
+    w[0] = __ldcg(reinterpret_cast<const uint16_t*>(p));
+  else if constexpr (EPL == 4)
+    w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
+  else {
+    const uint2 t = __ldcg(reinterpret_cast<const uint2*>(p));
+    w[0] = t.x;
+    w[1] = t.y;
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) c[j] = (int)(int8_t)(w[j >> 2] >> (8 * (j & 3)));
+}
+
+template <int EPL>
+__device__ __forceinline__ void store_codes(uint8_t* p, const int (&c)[EPL]) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) w[j >> 2] |= (uint32_t)(uint8_t)c[j] << (8 * (j & 3));
+  if constexpr (EPL == 2)
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+  else if constexpr (EPL == 4)
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// RMSNorm of one head's row across the warp (as qg_rmsnorm_perhead).
+template <int D>
+__device__ __forceinline__ void norm_row(float (&x)[D / 32], const float (&w)[D / 32], float eps) {
+  constexpr int EPL = D / 32;
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) ss = fmaf(x[j], x[j], ss);
+  const float inv = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) x[j] = x[j] * inv * w[j];
+}
+
+// Rotation of one head's row: dim d < half pairs with d + half, which the
+// lane `half / EPL` further holds at the same place (half is a multiple of
+// EPL). cs: the row's (cos, sin).
+template <int D>
+__device__ __forceinline__ void rotate_row(float (&x)[D / 32], const float2* cs, int half,
+                                           int lane) {
+  constexpr int EPL = D / 32;
+  const int hl = half / EPL;  // lanes per half
+  const bool lo = lane < hl, hi = !lo && lane < 2 * hl;
+  const int src = lo ? lane + hl : hi ? lane - hl : lane;
+  const int i0 = (lo ? lane : hi ? lane - hl : 0) * EPL;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const float other = __shfl_sync(0xffffffffu, x[j], src);
+    if (lo || hi) {
+      const float2 t = cs[i0 + j];
+      x[j] = lo ? x[j] * t.x - other * t.y : x[j] * t.x + other * t.y;
+    }
+  }
+}
+
+template <int D, bool I8, bool XF32>
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendParams P) {
+  constexpr int EPL = D / 32;
+  __shared__ float2 cs[kBlock * D / 2];
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+
+  // the sequence whose slot range holds this CTA's slot
+  const int u = blockIdx.x;
+  int b = u;
+  if (P.row_start) {
+    if (tid == 0) s_b = -1;
+    __syncthreads();
+    for (int i = tid; i < P.B; i += kWarps * 32) {
+      const int lo = row_begin(P.row_start, i, P.T) / kBlock + 2 * i;
+      const int hi = row_begin(P.row_start, i + 1, P.T) / kBlock + 2 * (i + 1);
+      if (lo <= u && u < hi) s_b = i;
+    }
+    __syncthreads();
+    b = s_b;
+    if (b < 0) return;
+  }
+  const int r0 = row_begin(P.row_start, b, P.T), n = row_begin(P.row_start, b + 1, P.T) - r0;
+  const int len = __ldcg(P.kv_len + b);
+  if (n < 1 || len < n || len > P.max_pages * P.page_size) return;
+  const int p0 = len - n;
+  const int first = (p0 / kBlock + (P.row_start ? u - (r0 / kBlock + 2 * b) : 0)) * kBlock;
+  if (first >= len) return;
+  const int lo = max(p0, first), hi = min(len, first + kBlock);
+  const int nr = hi - lo, o = lo - first;  // new rows, and rows of the block before them
+  const long long row = r0 + (lo - p0);
+  const int page = __ldcg(P.table + (long long)b * P.max_pages + first / P.page_size);
+  const bool in_pool = page >= 0 && page < P.num_pages;
+
+  // (cos, sin) of the new rows: the angle pos * theta^(-2i/rd) in units of
+  // pi and its reduction to [-1, 1] in float64 (positions in the millions
+  // keep the full fp32 accuracy), sincospi in fp32: within 2^-22 of the
+  // exact values, at a fraction of the cost of a float64 sincos.
+  for (int i = tid; i < nr * P.half; i += kWarps * 32) {
+    const int r = i / P.half, f = i % P.half;
+    const double t = (double)(lo + r) * P.turns[f];
+    float sn, cn;
+    sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn, &cn);
+    cs[i] = make_float2(cn, sn);
+  }
+  __syncthreads();
+
+  constexpr int XB = XF32 ? 4 : 2;
+  const int items = 2 * P.Hkv + P.H;
+  for (int it = blockIdx.y * kWarps + warp; it < items; it += gridDim.y * kWarps) {
+    const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
+    const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
+    const uint16_t* wp = isk ? P.kn : isv ? nullptr : P.qn;
+    float nw[EPL];  // the norm weights of the lane's values
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) nw[j] = wp ? bf16_bits_to_f32(__ldcg(wp + lane * EPL + j)) : 1.f;
+    if (!isk && !isv) {  // a query head
+      const uint8_t* src = P.q + (row * P.q_ld + h * D + lane * EPL) * XB;
+      for (int r = 0; r < nr; r += 4) {
+        float x[4][EPL];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r + e < nr) load_vals<EPL, XF32>(src + (r + e) * P.q_ld * XB, x[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (r + e >= nr) break;
+          if (P.qn) norm_row<D>(x[e], nw, P.eps);
+          if (P.half) rotate_row<D>(x[e], cs + (r + e) * P.half, P.half, lane);
+          __syncwarp();  // q_out may be q: every lane has its values
+          const long long at = (row + r + e) * P.H * D + h * D + lane * EPL;
+          if (P.q_bf16)
+            store_bf16<EPL>(reinterpret_cast<uint16_t*>(P.qo) + at, x[e]);
+          else
+            store_f32<EPL>(reinterpret_cast<float*>(P.qo) + at, x[e]);
+        }
+      }
+      continue;
+    }
+    if (!in_pool) continue;
+    const uint8_t* src = isk ? P.k + (row * P.k_ld + h * D + lane * EPL) * XB
+                             : P.v + (row * P.v_ld + h * D + lane * EPL) * XB;
+    const long long ld = (isk ? P.k_ld : P.v_ld) * XB;
+    // the block's first row in the pool
+    const long long at =
+        (((long long)page * P.Hkv + h) * P.page_size + first % P.page_size) * D + lane * EPL;
+    uint8_t* dst = (isk ? P.kp : P.vp) + at * (I8 ? 1 : 2);
+    if constexpr (!I8) {
+      for (int r = 0; r < nr; r += 4) {
+        float x[4][EPL];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r + e < nr) load_vals<EPL, XF32>(src + (r + e) * ld, x[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (r + e >= nr) break;
+          if (isk && P.kn) norm_row<D>(x[e], nw, P.eps);
+          if (isk && P.half) rotate_row<D>(x[e], cs + (r + e) * P.half, P.half, lane);
+          store_bf16<EPL>(reinterpret_cast<uint16_t*>(dst) + (o + r + e) * D, x[e]);
+        }
+      }
+    } else {
+      float* sp = (isk ? P.ks : P.vs) + ((long long)page * P.Hkv + h) * (P.page_size / kBlock) +
+                  (first % P.page_size) / kBlock;
+      const float s_old = o > 0 ? __ldcg(sp) : 0.f;
+      float x[kBlock][EPL];
+#pragma unroll
+      for (int r = 0; r < kBlock; ++r)
+        if (r < nr) load_vals<EPL, XF32>(src + r * ld, x[r]);
+      float top = 0.f;
+      bool bad = s_old != s_old;
+#pragma unroll
+      for (int r = 0; r < kBlock; ++r) {
+        if (r >= nr) break;
+        if (isk && P.kn) norm_row<D>(x[r], nw, P.eps);
+        if (isk && P.half) rotate_row<D>(x[r], cs + r * P.half, P.half, lane);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          top = fmaxf(top, fabsf(x[r][j]));
+          bad |= !(fabsf(x[r][j]) <= FLT_MAX);
+        }
+      }
+      const bool nan = __any_sync(0xffffffffu, bad);
+      const float s = nan ? __int_as_float(0x7FC00000) : fmaxf(s_old, warp_max(top) / 127.0f);
+      if (o > 0 && s != s_old) {  // the block's earlier rows to the new scale
+        const float ratio = s_old / s;
+        for (int r = 0; r < o; ++r) {
+          int c[EPL];
+          load_codes<EPL>(dst + r * D, c);
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) c[j] = __float2int_rn((float)c[j] * ratio);
+          store_codes<EPL>(dst + r * D, c);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kBlock; ++r) {
+        if (r >= nr) break;
+        int c[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const float t = s > 0.f ? x[r][j] / s : 0.f;  // (false for a NaN scale)
+          c[j] = min(127, max(-127, __float2int_rn(t)));
+        }
+        store_codes<EPL>(dst + (o + r) * D, c);
+      }
+      __syncwarp();  // every lane has read s_old
+      if (lane == 0) *sp = s;
+    }
+  }
+}
+
+struct GatherParams {
+  const uint8_t* kp;
+  const uint8_t* vp;
+  const float* ks;
+  const float* vs;
+  const int32_t* table;
+  const int32_t* first;
+  const int32_t* row_start;
+  void* ko;
+  void* vo;
+  int out_bf16;
+  int B, T, Hkv, page_size, max_pages, num_pages;
+};
+
+// One warp per (row, head), K and V.
+template <int D, bool I8>
+__global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams P) {
+  constexpr int EPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int row = (int)(w / P.Hkv), h = (int)(w % P.Hkv);
+  if (row >= P.T) return;
+  int b = row;
+  if (P.row_start) {  // the last sequence that starts at or before the row and holds it
+    b = -1;
+    for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < P.B && row_begin(P.row_start, i, P.T) <= row &&
+                      row < row_begin(P.row_start, i + 1, P.T);
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (m) b = i0 + __ffs(m) - 1;
+    }
+    if (b < 0) return;
+  }
+  const long long t =
+      (long long)(P.first ? __ldcg(P.first + b) : 0) + (row - row_begin(P.row_start, b, P.T));
+  int page = -1;
+  if (t >= 0 && t < (long long)P.max_pages * P.page_size)
+    page = __ldcg(P.table + (long long)b * P.max_pages + t / P.page_size);
+  const bool ok = page >= 0 && page < P.num_pages;
+  const int off = ok ? (int)(t % P.page_size) : 0;
+  const long long at = (((long long)(ok ? page : 0) * P.Hkv + h) * P.page_size + off) * D + lane * EPL;
+  const long long sat =
+      ((long long)(ok ? page : 0) * P.Hkv + h) * (P.page_size / kBlock) + off / kBlock;
+  const long long to = ((long long)row * P.Hkv + h) * D + lane * EPL;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    void* out = which ? P.vo : P.ko;
+    if (!out) continue;
+    const uint8_t* pages = which ? P.vp : P.kp;
+    float x[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[j] = __int_as_float(0x7FC00000);
+    if (ok) {
+      if constexpr (I8) {
+        int c[EPL];
+        load_codes<EPL>(pages + at, c);
+        const float s = __ldcg((which ? P.vs : P.ks) + sat);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) x[j] = (float)c[j] * s;
+      } else {
+        load_vals<EPL, false>(pages + at * 2, x);
+      }
+    }
+    if (P.out_bf16)
+      store_bf16<EPL>(reinterpret_cast<uint16_t*>(out) + to, x);
+    else
+      store_f32<EPL>(reinterpret_cast<float*>(out) + to, x);
+  }
+}
+
+template <int D, bool I8>
+cudaError_t launch_append(const AppendParams& P, bool xf32, dim3 grid, cudaStream_t st) {
+  if (xf32)
+    return launch_pdl(append_kernel<D, I8, true>, grid, dim3(kWarps * 32), 0, st, true, P);
+  return launch_pdl(append_kernel<D, I8, false>, grid, dim3(kWarps * 32), 0, st, true, P);
+}
+
+template <int D>
+cudaError_t launch_append(const AppendParams& P, bool i8, bool xf32, dim3 grid, cudaStream_t st) {
+  return i8 ? launch_append<D, true>(P, xf32, grid, st) : launch_append<D, false>(P, xf32, grid, st);
+}
+
+template <int D>
+cudaError_t launch_gather(const GatherParams& P, bool i8, dim3 grid, cudaStream_t st) {
+  if (i8) return launch_pdl(gather_kernel<D, true>, grid, dim3(kWarps * 32), 0, st, true, P);
+  return launch_pdl(gather_kernel<D, false>, grid, dim3(kWarps * 32), 0, st, true, P);
+}
+
+}  // namespace pk
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* page_table,
+                                        int max_pages, const int32_t* kv_len,
+                                        const int32_t* row_start, const void* q, long long q_ld,
+                                        const void* k, long long k_ld, const void* v,
+                                        long long v_ld, qg_dtype x_dtype, const uint16_t* q_norm,
+                                        const uint16_t* k_norm, float eps, double theta,
+                                        int rotary_dim, void* q_out, qg_dtype q_out_dtype, int B,
+                                        int T, int H, void* stream) {
+  clear_error();
+  const char* who = "qg_paged_kv_append";
+  if (qg_status s = pk::check_pool(who, kv, max_pages)) return s;
+  const int D = kv->head_dim, Hkv = kv->kv_heads;
+  QG_REQUIRE(B >= 0 && T >= 0 && H >= 0 && H <= 8192, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: B=%d T=%d H=%d", who, B, T, H);
+  QG_REQUIRE(B <= (1 << 24) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE, "%s: B=%d T=%d too large",
+             who, B, T);
+  QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d rows without row_start must be B=%d", who, T, B);
+  QG_REQUIRE((x_dtype == QG_F32 || x_dtype == QG_BF16) &&
+                 (q_out_dtype == QG_F32 || q_out_dtype == QG_BF16),
+             QG_ERR_INVALID_ARGUMENT, "%s: x_dtype=%d q_out_dtype=%d", who, (int)x_dtype,
+             (int)q_out_dtype);
+  QG_REQUIRE(rotary_dim >= 0 && rotary_dim <= D && rotary_dim % (D / 16) == 0,
+             QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: rotary_dim=%d must be a multiple of %d in [0, head_dim=%d]", who, rotary_dim,
+             D / 16, D);
+  QG_REQUIRE(rotary_dim == 0 || theta > 0.0, QG_ERR_INVALID_ARGUMENT, "%s: theta=%g must be > 0",
+             who, theta);
+  if (B == 0 || T == 0) return QG_OK;
+  if (qg_status s = pk::check_pool_pointers(who, kv)) return s;
+  QG_REQUIRE(page_table && kv_len && k && v, QG_ERR_INVALID_ARGUMENT,
+             "%s: null page_table, kv_len, k or v", who);
+  QG_REQUIRE(H == 0 || (q && q_out), QG_ERR_INVALID_ARGUMENT, "%s: null q or q_out with H=%d", who,
+             H);
+  const int xb = x_dtype == QG_F32 ? 4 : 2;
+  QG_REQUIRE(k_ld >= (long long)Hkv * D && v_ld >= (long long)Hkv * D &&
+                 (H == 0 || q_ld >= (long long)H * D),
+             QG_ERR_UNSUPPORTED_SHAPE, "%s: q_ld=%lld k_ld=%lld v_ld=%lld shorter than a row", who,
+             q_ld, k_ld, v_ld);
+  QG_REQUIRE(k_ld < (1LL << 40) && v_ld < (1LL << 40) && (H == 0 || q_ld < (1LL << 40)),
+             QG_ERR_UNSUPPORTED_SHAPE, "%s: row stride too large", who);
+  QG_REQUIRE(aligned(k, 16) && aligned(v, 16) && k_ld * xb % 16 == 0 && v_ld * xb % 16 == 0,
+             QG_ERR_MISALIGNED, "%s: rows of k or v do not start on 16 bytes", who);
+  QG_REQUIRE(H == 0 || (aligned(q, 16) && aligned(q_out, 16) && q_ld * xb % 16 == 0),
+             QG_ERR_MISALIGNED, "%s: rows of q or q_out do not start on 16 bytes", who);
+  QG_REQUIRE(aligned(page_table, 4) && aligned(kv_len, 4) && aligned(row_start, 4) &&
+                 aligned(q_norm, 2) && aligned(k_norm, 2),
+             QG_ERR_MISALIGNED, "%s: page_table, kv_len, row_start or a norm weight misaligned",
+             who);
+  pk::AppendParams P = {};
+  P.kp = reinterpret_cast<uint8_t*>(kv->k_pages);
+  P.vp = reinterpret_cast<uint8_t*>(kv->v_pages);
+  P.ks = kv->k_scales;
+  P.vs = kv->v_scales;
+  P.table = page_table;
+  P.kv_len = kv_len;
+  P.row_start = row_start;
+  P.q = reinterpret_cast<const uint8_t*>(q);
+  P.k = reinterpret_cast<const uint8_t*>(k);
+  P.v = reinterpret_cast<const uint8_t*>(v);
+  P.q_ld = q_ld;
+  P.k_ld = k_ld;
+  P.v_ld = v_ld;
+  P.qn = q_norm;
+  P.kn = k_norm;
+  P.qo = q_out;
+  P.q_bf16 = q_out_dtype == QG_BF16;
+  P.eps = eps;
+  P.half = rotary_dim / 2;
+  P.B = B;
+  P.T = T;
+  P.H = H;
+  P.Hkv = Hkv;
+  P.page_size = kv->page_size;
+  P.max_pages = max_pages;
+  P.num_pages = kv->num_pages;
+  for (int i = 0; i < P.half; ++i)
+    P.turns[i] = pow(theta, -2.0 * i / rotary_dim) / 3.14159265358979323846;
+  const int slots = row_start ? T / pk::kBlock + 2 * B : B;
+  // heads spread over CTAs until the grid fills the GPU twice or each warp
+  // has one item
+  const int most = (2 * Hkv + H + pk::kWarps - 1) / pk::kWarps;
+  const int ny = std::max(1, std::min(most, 2 * num_sms() / std::max(slots, 1)));
+  const dim3 grid(slots, ny);
+  const bool i8 = kv->dtype == QG_KV_INT8, xf32 = x_dtype == QG_F32;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (D == 64)
+    pk::launch_append<64>(P, i8, xf32, grid, st);
+  else if (D == 128)
+    pk::launch_append<128>(P, i8, xf32, grid, st);
+  else
+    pk::launch_append<256>(P, i8, xf32, grid, st);
+  return check_launch(who);
+}
+
+extern "C" qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table,
+                                        int max_pages, const int32_t* first,
+                                        const int32_t* row_start, void* k_out, void* v_out,
+                                        qg_dtype out_dtype, int B, int T, void* stream) {
+  clear_error();
+  const char* who = "qg_paged_kv_gather";
+  if (qg_status s = pk::check_pool(who, kv, max_pages)) return s;
+  QG_REQUIRE(B >= 0 && T >= 0 && B <= (1 << 24) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: B=%d T=%d", who, B, T);
+  QG_REQUIRE((long long)T * kv->kv_heads < (1LL << 33), QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d x kv_heads=%d too large", who, T, kv->kv_heads);
+  QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d rows without row_start must be B=%d", who, T, B);
+  QG_REQUIRE(out_dtype == QG_F32 || out_dtype == QG_BF16, QG_ERR_INVALID_ARGUMENT,
+             "%s: out_dtype=%d", who, (int)out_dtype);
+  if (B == 0 || T == 0 || (!k_out && !v_out)) return QG_OK;
+  if (qg_status s = pk::check_pool_pointers(who, kv)) return s;
+  QG_REQUIRE(page_table, QG_ERR_INVALID_ARGUMENT, "%s: null page_table", who);
+  QG_REQUIRE(aligned(k_out, 16) && aligned(v_out, 16), QG_ERR_MISALIGNED,
+             "%s: k_out or v_out not 16-byte aligned", who);
+  QG_REQUIRE(aligned(page_table, 4) && aligned(first, 4) && aligned(row_start, 4),
+             QG_ERR_MISALIGNED, "%s: page_table, first or row_start misaligned", who);
+  pk::GatherParams P = {};
+  P.kp = reinterpret_cast<const uint8_t*>(kv->k_pages);
+  P.vp = reinterpret_cast<const uint8_t*>(kv->v_pages);
+  P.ks = kv->k_scales;
+  P.vs = kv->v_scales;
+  P.table = page_table;
+  P.first = first;
+  P.row_start = row_start;
+  P.ko = k_out;
+  P.vo = v_out;
+  P.out_bf16 = out_dtype == QG_BF16;
+  P.B = B;
+  P.T = T;
+  P.Hkv = kv->kv_heads;
+  P.page_size = kv->page_size;
+  P.max_pages = max_pages;
+  P.num_pages = kv->num_pages;
+  const long long warps = (long long)T * kv->kv_heads;
+  const dim3 grid((unsigned)((warps + pk::kWarps - 1) / pk::kWarps));
+  const bool i8 = kv->dtype == QG_KV_INT8;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (kv->head_dim == 64)
+    pk::launch_gather<64>(P, i8, grid, st);
+  else if (kv->head_dim == 128)
+    pk::launch_gather<128>(P, i8, grid, st);
+  else
+    pk::launch_gather<256>(P, i8, grid, st);
+  return check_launch(who);
+}
