@@ -527,6 +527,33 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
                              const int32_t* first, const int32_t* row_start, void* k_out,
                              void* v_out, qg_dtype out_dtype, int B, int T, void* stream);
 
+/* Softmax attention over a paged cache, the rows of several sequences at
+ * once (a decode: one row each; a few draft tokens; prompts):
+ *   out[r][h] = sum_{t <= p} softmax_t(scale q[r][h] . k[t][g]) v[t][g],
+ *   g = h / (H / kv_heads), p = kv_len[b] - n_b + (r - row_start[b]):
+ * each row sees the cached tokens up to its own, which qg_paged_kv_append
+ * has written before.
+ * q          device [T][H * head_dim] of q_dtype.
+ * out        device [T][H * head_dim] of out_dtype.
+ * kv_len     device int32 [B]. Outside [n_b, max_pages * page_size], and 0:
+ *            zero rows (nothing is read). A page outside [0, num_pages)
+ *            gives NaN to the rows that see its tokens. Tokens past
+ *            kv_len are never used, whatever the page holds there.
+ * ws         >= qg_paged_attention_workspace_size(head_dim) bytes, 256-byte
+ *            aligned; contents need not be initialised. One workspace
+ *            serves calls that run one after another (one stream), not
+ *            calls that may overlap.
+ * Precision: bf16 q and out: operands of the tensor cores are exact (codes,
+ * bf16 values, q) but for the softmax weights (fp16 with int8 pages, bf16
+ * with bf16 pages); sums, maxima and scales in fp32. With an fp32 q or out,
+ * q and the weights are carried in several 16-bit terms (22 bits or more).
+ * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0. */
+size_t qg_paged_attention_workspace_size(int head_dim);
+qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
+                             const int32_t* kv_len, const int32_t* row_start, const void* q,
+                             qg_dtype q_dtype, void* out, qg_dtype out_dtype, int B, int T, int H,
+                             float scale, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Code predictor  [MK: makima src/tts/qwen3/code_predictor.rs,
  * CodePredictor::predict and CodePredictorLayer::forward]

@@ -99,3 +99,33 @@ def test_python_refusals():
         qg._int32(kv_len=torch.zeros(3))
     with pytest.raises(ValueError, match="cpu"):
         qg._on_device(0, k=torch.zeros(3))
+
+
+def _attend(kv=None, **kw):
+    need = qg.lib.qg_paged_attention_workspace_size(128)
+    a = dict(table=FAKE, max_pages=4, kv_len=FAKE, row_start=None, q=FAKE, qdt=qg.QG_BF16, out=FAKE,
+             odt=qg.QG_BF16, B=2, T=2, H=4, scale=0.1, ws=FAKE, ws_bytes=need)
+    a.update(kw)
+    return _status("qg_paged_attention", ctypes.byref(kv if kv is not None else _kv()),
+                   *a.values(), None)
+
+
+def test_attention_refusals():
+    U, I, M = qg.QG_ERR_UNSUPPORTED_SHAPE, qg.QG_ERR_INVALID_ARGUMENT, qg.QG_ERR_MISALIGNED
+    need = qg.lib.qg_paged_attention_workspace_size(128)
+    assert need > 0 and qg.lib.qg_paged_attention_workspace_size(0) == 0
+    for kw, code, word in ((dict(T=3), U, "row_start"), (dict(H=5), U, "H=5"), (dict(H=0), U, "H=0"),
+                           (dict(B=1 << 17, T=1 << 17), U, "too large"),
+                           (dict(row_start=FAKE, T=1 << 29), U, "too large"),
+                           (dict(qdt=4), I, "q_dtype=4"), (dict(odt=4), I, "out_dtype=4"),
+                           (dict(scale=0.0), I, "scale"), (dict(scale=float("nan")), I, "scale"),
+                           (dict(scale=float("inf")), I, "scale"), (dict(q=None), I, "q or out"),
+                           (dict(out=FAKE + 8), M, "out"), (dict(kv_len=FAKE + 1), M, "kv_len"),
+                           (dict(ws_bytes=need - 1), qg.QG_ERR_WORKSPACE_TOO_SMALL, str(need)),
+                           (dict(ws=None), qg.QG_ERR_WORKSPACE_TOO_SMALL, str(need)),
+                           (dict(ws=FAKE + 16), M, "ws")):
+        st, msg = _attend(**kw)
+        assert st == code and word in msg, (kw, st, msg)
+    st, msg = _attend(_kv(num_pages=1 << 29))
+    assert st == U and "too large" in msg
+    assert _attend(B=0, T=0, q=None)[0] == qg.QG_OK

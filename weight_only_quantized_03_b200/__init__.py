@@ -158,6 +158,9 @@ _SIGS = {
     "qg_paged_kv_append": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _vp,
                                 _f, _d, _i, _vp, _i, _i, _i, _i, _vp]),
     "qg_paged_kv_gather": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "qg_paged_attention_workspace_size": (_sz, [_i]),
+    "qg_paged_attention": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _sz,
+                                _vp]),
     "qg_step_graphs_enable": (None, [_i]),
     "qg_step_graphs_clear": (None, []),
     "qg_argmax_workspace_size": (_sz, [_i, _i]),
@@ -518,6 +521,30 @@ def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None,
             raise ValueError(f"k_out and v_out must be contiguous [{T}, {W}] of one type")
     _call("qg_paged_kv_gather", kv._ref, _p(page_table), page_table.shape[1], _p(first),
           _p(row_start), _p(k_out), _p(v_out), _dt(outs[0]), B, T, _stream(stream))
+
+
+def qg_paged_attention_workspace_size(head_dim):
+    return int(lib.qg_paged_attention_workspace_size(head_dim))
+
+
+def qg_paged_attention(kv, page_table, kv_len, q, out, H, scale, ws, row_start=None, stream=None):
+    """out [T, H*D] (fp32 or bf16) = causal softmax attention of the rows q
+    [T, H*D] (fp32 or bf16) over their sequences' cached tokens in the pages
+    of ``kv`` (a PagedKV). page_table int32 [B, max_pages]; kv_len int32 [B]
+    counts the rows' own tokens; row_start int32 [B+1], or None for one row
+    per sequence; ws of qg_paged_attention_workspace_size(D) bytes."""
+    dev = torch.cuda.current_device()
+    T = q.shape[0]
+    _on_device(dev, q=q, out=out, ws=ws)
+    B = kv._batch(page_table, kv_len, row_start, T, dev)
+    if kv_len is None:
+        raise ValueError("kv_len is needed")
+    if q.shape != (T, H * kv.head_dim) or out.shape != q.shape or \
+            not (q.is_contiguous() and out.is_contiguous()):
+        raise ValueError(f"q and out must be contiguous [T, {H} * {kv.head_dim}]")
+    _call("qg_paged_attention", kv._ref, _p(page_table), page_table.shape[1], _p(kv_len),
+          _p(row_start), _p(q), _dt(q), _p(out), _dt(out), B, T, H, scale, _p(ws),
+          ws.numel() * ws.element_size(), _stream(stream))
 
 
 # ---------------------------------------------------------- decode step ----

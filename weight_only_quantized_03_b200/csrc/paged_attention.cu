@@ -1,0 +1,988 @@
+// Softmax attention over a paged K/V cache (include/qg.h, qg_paged_attention):
+//
+//   out[r][h] = sum_{t <= p(r)} softmax_t(scale q[r][h] . k[t][h/G]) v[t][h/G],
+//   p(r) = kv_len[b] - n_b + (r - row_start[b]).
+//
+// What bounds it. A cached token of one KV head is 2 D codes (or bf16
+// values) and meets G query heads of each row: 2 G flops a byte for a single
+// row, so a decode is bound by reading the cache once. Long prompts are
+// bound by the tensor cores.
+//
+// The tile. The unit is a block of 16 tokens, which never straddles a page
+// and has one K and one V scale. Its "columns" are (row, head) pairs of one
+// KV head. Scores are computed transposed, S^T = K Q^T, and the output as
+// O^T = V^T P^T, with mma.sync m16n8k16: the 16 tokens (then 16 dims) are the
+// M side and 8 columns the N side, so a decode's few query heads waste
+// little, and the K and V operands go from global memory to registers in the
+// order the fragments want: the contraction's order is free, so a lane takes
+// 16 neighbouring bytes of two K rows, and 1/8 of the dims of four V rows,
+// in whole 16-byte loads, with no shared memory and no barrier between them.
+// P^T goes from the accumulator's layout to the operand's by movmatrix.
+//
+// int8 codes are exact in fp16 (1024 + q by a byte permute, minus 1152), so
+// they are multiplied as they are; the K scale multiplies the scores, the V
+// scale the weights. q is multiplied by a power of two before its rounding
+// to fp16 (largest value in [2^13, 2^14)): bf16 q is exact down to 2^-28 of the
+// largest, fp32 q takes two fp16 terms (22 bits). Weights times V's scale
+// are brought into fp16's range by a running power of two r >= |scale| and
+// 2^11: they keep 11 bits down to 2^-25 of the largest, where bf16 would
+// keep 8. bf16 pages: bf16 operands, fp32 q and weights in three bf16 terms.
+// With a bf16 output the weights take one term, with an fp32 output two
+// (int8 pages) or three (bf16 pages); the denominator sums them unrounded.
+//
+// The softmax is online per column in fp32, with a lazy maximum: the
+// reference only moves (and the accumulators are only rescaled) when a score
+// passes it by 2^kMargin, one vote per tile instead of the shuffles of a
+// maximum.
+//
+// Work split (kernel "split", decodes and short prompts). All (sequence, KV
+// head, column tile) items' key chunks form one line that is cut into equal
+// pieces, one per CTA, from the lengths on the device: ragged batches are
+// balanced, and the grid never depends on them. A CTA's 8 warps take a
+// piece's tiles in turn and merge in shared memory. An item inside one piece
+// is written out; the others' parts go to the workspace and a second small
+// launch merges them in order (results do not depend on scheduling).
+// Kernel "whole" (long prompts): a warp takes 32 columns over all their keys.
+#include <cuda_fp16.h>
+
+#include "mma_sync.cuh"
+#include "paged_kv.cuh"
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+namespace qg {
+namespace pa {
+
+using pk::kBlock;
+using pk::row_begin;
+
+constexpr int kWarps = 8;            // split kernel
+constexpr int kChunk = kWarps * kBlock;
+constexpr int kWholeWarps = 4;       // whole kernel
+constexpr int kWholeNT = 4;
+constexpr int kMergeThreads = 128;
+constexpr float kMargin = 4.f;       // log2 of how far a weight may pass 1
+
+struct Params {
+  const void* q;
+  void* out;
+  const uint8_t* kp;
+  const uint8_t* vp;
+  const float* ks;
+  const float* vs;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* row_start;
+  float* part;  // [2 * pieces][NC * (D + 2)]
+  int q_bf16, out_bf16;
+  int B, T, H, Hkv, G, bpp, max_pages, num_pages;  // bpp: blocks of 16 tokens per page
+  int pieces;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <bool I8>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (I8)
+    mma_f16(c, a0, a1, a2, a3, b0, b1);
+  else
+    mm::mma_bf16(c, a0, a1, a2, a3, b0, b1);
+}
+// (lo, hi) rounded to the operand type; lo and hi become the rests.
+template <bool I8>
+__device__ __forceinline__ uint32_t take16(float& lo, float& hi) {
+  if constexpr (I8) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    const float2 f = __half22float2(h);
+    lo -= f.x;
+    hi -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    lo -= __bfloat162float(h.x);
+    hi -= __bfloat162float(h.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+__device__ __forceinline__ uint4 ldcg16(const uint8_t* p) {
+  return __ldcg(reinterpret_cast<const uint4*>(p));
+}
+
+// One (sequence, KV head, column tile) item.
+struct Item {
+  int b, h, ct;   // sequence, KV head, column tile
+  int r0, n;      // the sequence's first packed row and rows
+  int len;        // cached tokens, 0 for a length out of range
+};
+
+__device__ __forceinline__ void set_seq(const Params& P, Item& it, int b) {
+  it.b = b;
+  it.r0 = row_begin(P.row_start, b, P.T);
+  it.n = max(0, row_begin(P.row_start, b + 1, P.T) - it.r0);
+  const int len = __ldcg(P.kv_len + b);
+  it.len = len >= it.n && (long long)len <= (long long)P.max_pages * P.bpp * kBlock ? len : 0;
+}
+
+// Visible tokens of column c of the item's sequence. Columns past the last
+// one (their q is zero, nothing is stored for them) see everything, so that
+// they do not make a tile partly masked.
+__device__ __forceinline__ int visible(const Params& P, const Item& it, int c) {
+  const int i = c / P.G;
+  return i < it.n ? it.len - it.n + i + 1 : 0x7FFFFFFF;
+}
+
+__device__ __forceinline__ float load_q(const Params& P, const Item& it, int c, int d, int D) {
+  const int i = c / P.G;
+  if (i >= it.n) return 0.f;
+  const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D + d;
+  return P.q_bf16 ? bf16_bits_to_f32(__ldcg(reinterpret_cast<const uint16_t*>(P.q) + at))
+                  : __ldcg(reinterpret_cast<const float*>(P.q) + at);
+}
+
+// Where element (column n, dim d) of Q lies in the fragments' order
+// [k step][column tile][term][lane][4] of 16-bit values: a lane's 16 bytes
+// of a K row are neighbouring dims, four per k step.
+template <bool I8, int NT, int QS>
+__device__ __forceinline__ int q_at(int n, int d, int term) {
+  constexpr int PL = I8 ? 16 : 8;  // dims of a lane's 16 bytes
+  const int t = d % (4 * PL) / PL, ks = d / (4 * PL) * (PL / 4) + d % PL / 4;
+  return (((ks * NT + n / 8) * QS + term) * 32 + (n % 8) * 4 + t) * 4 + d % 4;
+}
+
+// Stores four neighbouring values of one column, split into QS terms.
+template <bool I8, int NT, int QS>
+__device__ __forceinline__ void put_q(uint16_t* sq, int n, int d, float (&x)[4]) {
+#pragma unroll
+  for (int s = 0; s < QS; ++s) {
+    uint2 w;
+    w.x = take16<I8>(x[0], x[1]);
+    w.y = take16<I8>(x[2], x[3]);
+    *reinterpret_cast<uint2*>(sq + q_at<I8, NT, QS>(n, d, s)) = w;
+  }
+}
+
+// 2^e that brings the largest |q| into [2^13, 2^14) (int8 pages).
+__device__ __forceinline__ float q_unit(float top) {
+  const int ex = (__float_as_int(top) >> 23) & 255;  // 0: zero or subnormal, 255: not finite
+  if (ex == 0 || ex == 255) return 1.f;
+  return __int_as_float(min(254, max(1, 127 + 13 - (ex - 127))) << 23);
+}
+
+// A warp's running state over the columns of its item.
+template <int D, int NT>
+struct State {
+  float m[NT][2], l[NT][2];   // columns 8 nt + 2 t (+ 1): reference, this lane's weights
+  float o[D / 16][NT][4];     // dims g D/8 + 2 i (+ 1), columns 2 t (+ 1)
+  float r;                    // unit of o: the V scales seen are at most r
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      m[j][0] = m[j][1] = -FLT_MAX;
+      l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+    }
+    r = FLT_MIN;
+  }
+};
+
+// A warp's walk over tiles first, first + step, ... < end of one sequence
+// and KV head: page lookups 32 tiles at a time, K and V one tile ahead.
+template <int D, bool I8, int NT, int QS, int PS>
+struct Walk {
+  static constexpr int ES = I8 ? 1 : 2;
+  static constexpr int KC = D * ES / 64;        // 16-byte pieces of a lane per K row
+  static constexpr int VB = D * ES / 8;         // bytes of a lane per V row
+  static constexpr int VC = (VB + 15) / 16;
+  const Params& P;
+  const int lane, g, t;
+  int lim[NT][2];     // visible tokens of the lane's columns
+  int min_lim, len;   // of all the item's columns; cached tokens
+  float qf;           // scale_log2 / 2^e
+  const uint16_t* sq;
+  uint4 kr[2][KC];
+  uint4 vr[4][VC];
+  float ks, vs;
+  int blocks;         // lane i: block index in the pool of tile base + i step, -1: bad page
+
+  __device__ __forceinline__ Walk(const Params& P_, int lane_)
+      : P(P_), lane(lane_), g(lane_ >> 2), t(lane_ & 3) {}
+
+  __device__ __forceinline__ void lookup(const Item& it, int tile, int step, int end) {
+    const long long at = (long long)tile + (long long)lane * step;
+    blocks = -1;
+    if (at < end) {
+      const int pi = (int)at / P.bpp;
+      const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
+      if (page >= 0 && page < P.num_pages)
+        blocks = (page * P.Hkv + it.h) * P.bpp + ((int)at - pi * P.bpp);
+    }
+  }
+
+  __device__ __forceinline__ void load_k(int blk) {
+    const bool ok = blk >= 0;
+    const uint8_t* p = P.kp + (long long)(ok ? blk : 0) * (kBlock * D * ES) + g * (D * ES) + t * 16;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      kr[0][c] = ok ? ldcg16(p + c * 64) : make_uint4(0, 0, 0, 0);
+      kr[1][c] = ok ? ldcg16(p + 8 * D * ES + c * 64) : make_uint4(0, 0, 0, 0);
+    }
+    // a bad page: NaN scores for whoever sees its tokens
+    ks = !ok ? __int_as_float(0x7FC00000) : I8 ? __ldcg(P.ks + blk) : 1.f;
+  }
+
+  // Rows at or past the sequence's end hold anything: zero (0 * NaN).
+  __device__ __forceinline__ void load_v(int blk, int tile) {
+    const bool ok = blk >= 0;
+    const int left = I8 ? kBlock : len - tile * kBlock;
+    const uint8_t* p = P.vp + (long long)(ok ? blk : 0) * (kBlock * D * ES) + g * VB;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+      const uint8_t* pi = p + key * (D * ES);
+      const bool in = ok && key < left;
+      if constexpr (VB >= 16) {
+#pragma unroll
+        for (int c = 0; c < VC; ++c) vr[i][c] = in ? ldcg16(pi + c * 16) : make_uint4(0, 0, 0, 0);
+      } else {
+        const uint2 w = in ? __ldcg(reinterpret_cast<const uint2*>(pi)) : make_uint2(0, 0);
+        vr[i][0] = make_uint4(w.x, w.y, 0, 0);
+      }
+    }
+    vs = I8 && ok ? __ldcg(P.vs + blk) : 1.f;
+  }
+
+  static __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  }
+
+  __device__ __forceinline__ void scores(float (&s)[NT][4]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+#pragma unroll
+      for (int u = 0; u < (I8 ? 4 : 2); ++u) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (I8) {
+          const uint32_t lo = word(kr[0][c], u) ^ 0x80808080u, hi = word(kr[1][c], u) ^ 0x80808080u;
+          a0 = codes01(lo);
+          a1 = codes01(hi);
+          a2 = codes23(lo);
+          a3 = codes23(hi);
+        } else {
+          a0 = word(kr[0][c], 2 * u);
+          a1 = word(kr[1][c], 2 * u);
+          a2 = word(kr[0][c], 2 * u + 1);
+          a3 = word(kr[1][c], 2 * u + 1);
+        }
+        const int step = c * (I8 ? 4 : 2) + u;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int e = 0; e < QS; ++e) {
+            const uint2 b = *reinterpret_cast<const uint2*>(
+                sq + (((step * NT + j) * QS + e) * 32 + lane) * 4);
+            mma<I8>(s[j], a0, a1, a2, a3, b.x, b.y);
+          }
+        }
+      }
+    }
+  }
+
+  // bf16 pages, a tile that some columns see in part, with V values that are
+  // not finite: 0 * NaN must not reach the columns that do not see them, so
+  // the products are formed one by one (never taken with finite values).
+  static __device__ __forceinline__ void accumulate_seen(State<D, NT>& S, const float (&p)[NT][4],
+                                                      const uint4 (&vr)[4][VC], int lane) {
+    const int t = lane & 3;
+#pragma unroll 1
+    for (int key = 0; key < kBlock; ++key) {
+      const int slot = (key & 1) + 2 * (key >> 3), src = (lane & ~3) | ((key & 7) >> 1);
+      float w[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[j][e] = __shfl_sync(0xffffffffu, key < 8 ? p[j][e] : p[j][2 + e], (key & 7) * 4 + t);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t mine = slot == 0   ? word(vr[0][i / 4], i % 4)
+                              : slot == 1 ? word(vr[1][i / 4], i % 4)
+                              : slot == 2 ? word(vr[2][i / 4], i % 4)
+                                          : word(vr[3][i / 4], i % 4);
+        const uint32_t x = __shfl_sync(0xffffffffu, mine, src);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (w[j][e] != 0.f) {
+              S.o[i][j][e] = fmaf(w[j][e], bf16_lo(x), S.o[i][j][e]);
+              S.o[i][j][2 + e] = fmaf(w[j][e], bf16_hi(x), S.o[i][j][2 + e]);
+            }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void weigh(State<D, NT>& S, float (&p)[NT][4], bool part) {
+    if constexpr (!I8) {
+      if (part) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = word(vr[i][c], e);
+              odd |= (x & 0x7F800000u) == 0x7F800000u || (x & 0x7F80u) == 0x7F80u;
+            }
+        if (__any_sync(0xffffffffu, odd)) {
+          accumulate_seen(S, p, vr, lane);
+          return;
+        }
+      }
+    }
+    uint32_t b[NT][PS][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < PS; ++e) {
+        b[j][e][0] = transpose8x8(take16<I8>(p[j][0], p[j][1]));
+        b[j][e][1] = transpose8x8(take16<I8>(p[j][2], p[j][3]));
+      }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t a0, a1, a2, a3;
+      if constexpr (I8) {
+        // dims 2 i and 2 i + 1 of the lane's: bytes of word i / 2
+        const int c = i / 8, e = i / 2 % 4;
+        const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+        const uint32_t lo =
+            __byte_perm(word(vr[0][c], e), word(vr[1][c], e), sel) ^ 0x80808080u;
+        const uint32_t hi =
+            __byte_perm(word(vr[2][c], e), word(vr[3][c], e), sel) ^ 0x80808080u;
+        a0 = codes01(lo);
+        a1 = codes23(lo);
+        a2 = codes01(hi);
+        a3 = codes23(hi);
+      } else {
+        const int c = i / 4, e = i % 4;
+        a0 = __byte_perm(word(vr[0][c], e), word(vr[1][c], e), 0x5410u);
+        a1 = __byte_perm(word(vr[0][c], e), word(vr[1][c], e), 0x7632u);
+        a2 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x5410u);
+        a3 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x7632u);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < PS; ++e) mma<I8>(S.o[i][j], a0, a1, a2, a3, b[j][e][0], b[j][e][1]);
+    }
+  }
+
+  __device__ __forceinline__ void run(State<D, NT>& S, const Item& it, int first, int step,
+                                      int end) {
+    if (first >= end) return;
+    int at = 0;  // tile `first + at * step` of the current batch of lookups
+    int tile = first;
+    lookup(it, tile, step, end);
+    int blk = __shfl_sync(0xffffffffu, blocks, 0);
+    load_k(blk);
+    load_v(blk, tile);
+    for (;;) {
+      const bool more = end - tile > step;
+      if (more && ++at == 32) {
+        at = 0;
+        lookup(it, tile + step, step, end);
+      }
+      const int next = __shfl_sync(0xffffffffu, blocks, at);
+      float p[NT][4];
+      scores(p);
+      const float f = qf * ks;
+      if (more) load_k(next);
+      // scores in log2 units, masked
+      const int key0 = tile * kBlock + g;
+      const bool part = tile * kBlock + kBlock > min_lim;
+      bool over = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[j][e] *= f;
+          if (part && key0 + 8 * (e >> 1) >= lim[j][e & 1]) p[j][e] = -INFINITY;
+          over |= p[j][e] > S.m[j][e & 1] + kMargin;
+        }
+      const bool wider = I8 && fabsf(vs) > S.r && fabsf(vs) <= FLT_MAX;  // the same in all lanes
+      if (__any_sync(0xffffffffu, over) || wider) {
+        float down = 1.f;
+        if (wider) {
+          const int ex = min(254, ((__float_as_int(vs) >> 23) & 255) + 1);
+          const float r = __int_as_float(ex << 23);
+          down = S.r / r;
+          S.r = r;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float a[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(p[j][e], p[j][2 + e]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, S.m[j][e]);
+            a[e] = ex2(S.m[j][e] - x);
+            S.m[j][e] = x;
+            S.l[j][e] *= a[e];
+          }
+          a[0] *= down;
+          a[1] *= down;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            S.o[i][j][0] *= a[0];
+            S.o[i][j][1] *= a[1];
+            S.o[i][j][2] *= a[0];
+            S.o[i][j][3] *= a[1];
+          }
+        }
+      }
+      const float wv = I8 ? vs * (1.f / S.r) * 2048.f : 1.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = ex2(p[j][e] - S.m[j][e & 1]);
+          S.l[j][e & 1] += x;
+          // a token that the column does not see keeps weight 0 whatever the
+          // block's scale is
+          if constexpr (I8) p[j][e] = part && p[j][e] == -INFINITY ? 0.f : x * wv;
+          else p[j][e] = x;
+        }
+      weigh(S, p, part);
+      if (!more) break;
+      tile += step;
+      load_v(next, tile);
+    }
+  }
+};
+
+// The unit of the accumulators of a state (2^11: the weights' own).
+template <bool I8>
+__device__ __forceinline__ float o_unit(float r) {
+  return I8 ? r * (1.f / 2048.f) : 1.f;
+}
+
+// Sets up a walk over the item's column tile: q into shared memory by the
+// `nthr` threads that call this (id `id` of them), limits per lane.
+template <int D, bool I8, int NT, int QS>
+__device__ __forceinline__ float stage_q(const Params& P, const Item& it, uint16_t* sq, int id,
+                                         int nthr, float top) {
+  const float unit = I8 ? q_unit(top) : 1.f;
+  for (int i = id; i < NT * 8 * D / 4; i += nthr) {
+    const int n = i / (D / 4), d = i % (D / 4) * 4;
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = load_q(P, it, it.ct * NT * 8 + n, d + e, D) * unit;
+    put_q<I8, NT, QS>(sq, n, d, x);
+  }
+  return P.scale_log2 / unit;
+}
+
+template <int D, int NT>
+__device__ __forceinline__ float q_top(const Params& P, const Item& it, int id, int nthr) {
+  float top = 0.f;
+  for (int i = id; i < NT * 8 * D; i += nthr)
+    top = fmaxf(top, fabsf(load_q(P, it, it.ct * NT * 8 + i / D, i % D, D)));
+  return warp_max(top);
+}
+
+template <class W>
+__device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w, int NT) {
+  int lo = 0x7FFFFFFF;
+  for (int j = 0; j < NT; ++j)
+    for (int e = 0; e < 2; ++e) {
+      w.lim[j][e] = visible(P, it, it.ct * NT * 8 + j * 8 + 2 * w.t + e);
+      lo = min(lo, w.lim[j][e]);
+    }
+  lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  w.min_lim = min(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
+  w.len = it.len;
+}
+
+__device__ __forceinline__ void store_out(const Params& P, const Item& it, int c, int d, int D,
+                                          float x) {
+  const int i = c / P.G;
+  if (i >= it.n) return;
+  const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D + d;
+  if (P.out_bf16)
+    reinterpret_cast<uint16_t*>(P.out)[at] = f32_to_bf16_bits(x);
+  else
+    reinterpret_cast<float*>(P.out)[at] = x;
+}
+
+// ------------------------------------------------------------ split kernel --
+
+// Chunks of sequence b's items (at least one, so that empty ones are
+// written) and the item count.
+struct SeqWork {
+  int tiles, chunks;
+  __device__ __forceinline__ long long total(int Hkv) const {
+    return (long long)tiles * Hkv * chunks;
+  }
+};
+__device__ __forceinline__ SeqWork seq_work(const Params& P, int b, int NC) {
+  Item it;
+  set_seq(P, it, b);
+  SeqWork w;
+  w.tiles = (int)(((long long)it.n * P.G + NC - 1) / NC);
+  w.chunks = max(1, (it.len + kChunk - 1) / kChunk);
+  return w;
+}
+
+// Exclusive prefix over the calling block's NTHR threads of v; *total gets
+// the sum. `buf` holds NTHR / 32 values.
+template <int NTHR>
+__device__ __forceinline__ long long block_prefix(long long v, long long* buf, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) buf[warp] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int i = 0; i < NTHR / 32; ++i) {
+    if (i < warp) before += buf[i];
+    sum += buf[i];
+  }
+  __syncthreads();
+  *total = sum;
+  return before + x - v;
+}
+
+// First chunk of piece c of N chunks in `pieces`.
+__device__ __forceinline__ long long piece_begin(long long N, int c, int pieces) {
+  return N * c / pieces;
+}
+
+template <int D, bool I8, int NT, int QS, int PS>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 && D <= 128 ? 2 : 1)
+split_kernel(const __grid_constant__ Params P) {
+  constexpr int NC = NT * 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);            // [kWarps][NC][D]
+  float* sm = so + kWarps * NC * D;                      // [kWarps][NC]
+  float* sl = sm + kWarps * NC;                          // [kWarps][NC]
+  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * NC);  // fragments of q
+  __shared__ long long buf[kWarps], s_rest;
+  __shared__ int s_b;
+  __shared__ float s_top[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+
+  // the line of all chunks, sequence after sequence; this CTA's piece of it
+  const int per = (P.B + kWarps * 32 - 1) / (kWarps * 32);
+  long long mine = 0, N;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
+  }
+  const long long before = block_prefix<kWarps * 32>(mine, buf, &N);
+  long long pos = piece_begin(N, blockIdx.x, P.pieces);
+  const long long stop = piece_begin(N, blockIdx.x + 1, P.pieces);
+  if (pos >= stop) return;
+  if (pos >= before && pos < before + mine) {
+    long long rest = pos - before;
+    int b = tid * per;
+    for (;; ++b) {
+      const long long w = seq_work(P, b, NC).total(P.Hkv);
+      if (rest < w) break;
+      rest -= w;
+    }
+    s_b = b;
+    s_rest = rest;
+  }
+  __syncthreads();
+  Item it;
+  set_seq(P, it, s_b);
+  SeqWork w = seq_work(P, s_b, NC);
+  int unit = (int)(s_rest / w.chunks);   // (head, column tile) of the sequence
+  int c0 = (int)(s_rest % w.chunks);     // first chunk of the item in this piece
+
+  Walk<D, I8, NT, QS, PS> walk(P, lane);
+  walk.sq = sq;
+  State<D, NT> S;
+  while (pos < stop) {
+    it.h = unit / w.tiles;
+    it.ct = unit % w.tiles;
+    const int c1 = (int)min((long long)w.chunks, c0 + (stop - pos));
+    // q of the item's columns
+    float top = 0.f;
+    if (I8) {
+      top = q_top<D, NT>(P, it, tid, kWarps * 32);
+      if (lane == 0) s_top[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, s_top[i]);
+    }
+    walk.qf = stage_q<D, I8, NT, QS>(P, it, sq, tid, kWarps * 32, top);
+    set_limits(P, it, walk, NT);
+    __syncthreads();
+    S.clear();
+    const int end = min(c1 * kWarps, (it.len + kBlock - 1) / kBlock);
+    walk.run(S, it, c0 * kWarps + warp, kWarps, end);
+    // the warps' states to shared memory: weights summed over the lanes that
+    // share a column, outputs in plain units
+    const float u = o_unit<I8>(S.r);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = S.l[j][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int n = j * 8 + 2 * walk.t + e;
+        if (walk.g == 0) {
+          sm[warp * NC + n] = S.m[j][e];
+          sl[warp * NC + n] = l;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(so + (warp * NC + n) * D + walk.g * (D / 8) + 2 * i) =
+              make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
+      }
+    }
+    __syncthreads();
+    const bool whole = c0 == 0 && c1 == w.chunks;
+    float* part = P.part + (long long)(2 * blockIdx.x + (c0 == 0)) * NC * (D + 2);
+    for (int i = tid; i < NC * D; i += kWarps * 32) {
+      const int n = i / D, d = i % D;
+      float M = sm[n];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) M = fmaxf(M, sm[k * NC + n]);
+      float L = 0.f, O = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float a = ex2(sm[k * NC + n] - M);
+        L = fmaf(a, sl[k * NC + n], L);
+        O = fmaf(a, so[(k * NC + n) * D + d], O);
+      }
+      if (whole) {
+        store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+      } else {
+        part[2 * NC + i] = O;
+        if (d == 0) {
+          part[n] = M;
+          part[NC + n] = L;
+        }
+      }
+    }
+    __syncthreads();
+    pos += c1 - c0;
+    c0 = 0;
+    if (pos < stop && ++unit == w.tiles * P.Hkv) {
+      unit = 0;
+      do {  // the next sequence with rows (one exists: chunks are left)
+        set_seq(P, it, it.b + 1);
+        w = seq_work(P, it.b, NC);
+      } while (w.tiles == 0);
+    }
+  }
+}
+
+// Items cut between pieces: one CTA per (sequence, head, column tile) slot.
+template <int D, int NT>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Params P) {
+  constexpr int NC = NT * 8;
+  __shared__ long long buf[kMergeThreads / 32], s_begin;
+  __shared__ int s_b;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  // sequence whose slot range holds this CTA's column tile
+  const int u = blockIdx.x;
+  if (tid == 0) s_b = -1;
+  const int per = (P.B + kMergeThreads - 1) / kMergeThreads;
+  long long mine = 0, N;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
+  }
+  long long before = block_prefix<kMergeThreads>(mine, buf, &N);
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b >= P.B) break;
+    const long long lo = (long long)row_begin(P.row_start, b, P.T) * P.G / NC + b;
+    const long long hi = (long long)row_begin(P.row_start, b + 1, P.T) * P.G / NC + b + 1;
+    if (lo <= u && u < hi) {
+      s_b = b;
+      s_begin = before;
+    }
+    before += seq_work(P, b, NC).total(P.Hkv);
+  }
+  __syncthreads();
+  if (s_b < 0) return;
+  Item it;
+  set_seq(P, it, s_b);
+  const SeqWork w = seq_work(P, s_b, NC);
+  it.ct = u - (int)((long long)it.r0 * P.G / NC + s_b);
+  it.h = blockIdx.y;
+  if (it.ct >= w.tiles) return;
+  const long long begin = s_begin + (long long)(it.h * w.tiles + it.ct) * w.chunks;
+  const long long last = begin + w.chunks - 1;
+  // the pieces that hold the item's first and last chunks
+  const int p0 = (int)(((begin + 1) * P.pieces - 1) / N);
+  const int p1 = (int)(((last + 1) * P.pieces - 1) / N);
+  if (p0 == p1) return;  // written by its piece
+  for (int i = tid; i < NC * D; i += kMergeThreads) {
+    const int n = i / D, d = i % D;
+    float M = -FLT_MAX, L = 0.f, O = 0.f;
+    for (int p = p0; p <= p1; ++p) {
+      if (piece_begin(N, p, P.pieces) == piece_begin(N, p + 1, P.pieces)) continue;  // empty
+      const float* part = P.part + (long long)(2 * p + (p == p0)) * NC * (D + 2);
+      const float m = __ldcg(part + n);
+      const float x = fmaxf(M, m);
+      const float a = ex2(M - x), c = ex2(m - x);
+      L = L * a + __ldcg(part + NC + n) * c;
+      O = O * a + __ldcg(part + 2 * NC + i) * c;
+      M = x;
+    }
+    store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+  }
+}
+
+// ------------------------------------------------------------ whole kernel --
+
+template <int D, bool I8, int QS, int PS>
+__global__ void __launch_bounds__(kWholeWarps * 32) whole_kernel(const __grid_constant__ Params P) {
+  constexpr int NT = kWholeNT, NC = NT * 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t* sq = reinterpret_cast<uint16_t*>(smem) + warp * (NC * D * QS);
+  pdl_wait();
+  // later column tiles see more keys: they go first
+  const long long u = (long long)(gridDim.x - 1 - blockIdx.x) * kWholeWarps + warp;
+  int b = -1;
+  for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
+    const int i = i0 + lane;
+    bool in = false;
+    if (i < P.B) {
+      const long long lo = (long long)row_begin(P.row_start, i, P.T) * P.G / NC + i;
+      const long long hi = (long long)row_begin(P.row_start, i + 1, P.T) * P.G / NC + i + 1;
+      in = lo <= u && u < hi;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (m) b = i0 + __ffs(m) - 1;
+  }
+  if (b < 0) return;
+  Item it;
+  set_seq(P, it, b);
+  it.ct = (int)(u - ((long long)it.r0 * P.G / NC + b));
+  it.h = blockIdx.y;
+  if ((long long)it.ct * NC >= (long long)it.n * P.G) return;
+  Walk<D, I8, NT, QS, PS> walk(P, lane);
+  walk.sq = sq;
+  const float top = I8 ? q_top<D, NT>(P, it, lane, 32) : 0.f;
+  walk.qf = stage_q<D, I8, NT, QS>(P, it, sq, lane, 32, top);
+  set_limits(P, it, walk, NT);
+  __syncwarp();
+  State<D, NT> S;
+  S.clear();
+  // keys of the tile's last row
+  const int last = min(it.n - 1, (it.ct * NC + NC - 1) / P.G);
+  const int keys = it.len ? it.len - it.n + last + 1 : 0;
+  walk.run(S, it, 0, 1, (keys + kBlock - 1) / kBlock);
+  const float un = o_unit<I8>(S.r);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = S.l[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const float a = l != 0.f ? un / l : 0.f;
+      const int c = it.ct * NC + j * 8 + 2 * walk.t + e, i = c / P.G;
+      if (i >= it.n) continue;
+      const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D +
+                           walk.g * (D / 8);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float x = S.o[k][j][e] * a, y = S.o[k][j][2 + e] * a;
+        if (P.out_bf16)
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(P.out) + at + 2 * k) =
+              mm::pack_bf16(x, y);
+        else
+          *reinterpret_cast<float2*>(reinterpret_cast<float*>(P.out) + at + 2 * k) =
+              make_float2(x, y);
+      }
+    }
+}
+
+// ---------------------------------------------------------------- launches --
+
+template <int D, bool I8, int NT, int QS, int PS>
+cudaError_t launch_split(const Params& P, cudaStream_t st) {
+  constexpr int NC = NT * 8;
+  const size_t smem = (size_t)kWarps * NC * (D + 2) * 4 + (size_t)NC * D * QS * 2;
+  ensure_smem((const void*)split_kernel<D, I8, NT, QS, PS>, (int)smem);
+  cudaError_t e = launch_pdl(split_kernel<D, I8, NT, QS, PS>, dim3(P.pieces), dim3(kWarps * 32),
+                             smem, st, true, P);
+  if (e != cudaSuccess || P.pieces == 1) return e;
+  const long long slots = (long long)P.T * P.G / NC + P.B;
+  return launch_pdl(merge_kernel<D, NT>, dim3((unsigned)slots, P.Hkv), dim3(kMergeThreads), 0, st,
+                    true, P);
+}
+
+template <int D, bool I8, int QS, int PS>
+cudaError_t launch_whole(const Params& P, cudaStream_t st) {
+  constexpr int NC = kWholeNT * 8;
+  const size_t smem = (size_t)kWholeWarps * NC * D * QS * 2;
+  ensure_smem((const void*)whole_kernel<D, I8, QS, PS>, (int)smem);
+  const long long slots = (long long)P.T * P.G / NC + P.B;
+  return launch_pdl(whole_kernel<D, I8, QS, PS>,
+                    dim3((unsigned)((slots + kWholeWarps - 1) / kWholeWarps), P.Hkv),
+                    dim3(kWholeWarps * 32), smem, st, true, P);
+}
+
+// How a call runs: columns per tile, pieces of the split kernel (0: the
+// whole kernel).
+struct Plan {
+  int nt, pieces;
+};
+inline Plan plan(int B, int T, int H, int Hkv, int D, long long cap, bool exact) {
+  const long long G = H / Hkv;
+  // a warp per 32 columns needs enough of them to fill the GPU
+  const long long warps = ((long long)T * G / 32 + B) * Hkv;
+  if (D <= 128 && !exact && T * G >= 16LL * B && warps >= 4LL * num_sms()) return {kWholeNT, 0};
+  const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
+  const long long items = ((long long)T * G / (8 * nt) + B) * Hkv;
+  const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
+  const long long most = (long long)num_sms() * (nt == 1 && D <= 128 ? 2 : 1);
+  return {nt, (int)std::max(1LL, std::min(most, items * chunks))};
+}
+
+template <int D, bool I8>
+cudaError_t launch(const Params& P, const Plan& p, bool exact, cudaStream_t st) {
+  constexpr int E = I8 ? 2 : 3;  // terms of fp32 q and weights
+  if (exact) return launch_split<D, I8, 1, E, E>(P, st);
+  if constexpr (D <= 128) {
+    if (p.pieces == 0) return launch_whole<D, I8, 1, 1>(P, st);
+    if (p.nt == 2) return launch_split<D, I8, 2, 1, 1>(P, st);
+  }
+  return launch_split<D, I8, 1, 1, 1>(P, st);
+}
+
+// The largest number of pieces times columns any call of the head size uses.
+inline size_t ws_bytes(int D) {
+  return (size_t)2 * num_sms() * 2 * 8 * (D + 2) * 4;
+}
+
+}  // namespace pa
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" size_t qg_paged_attention_workspace_size(int head_dim) {
+  if (head_dim <= 0 || head_dim > 256) return 0;
+  return pa::ws_bytes(head_dim);
+}
+
+extern "C" qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* page_table,
+                                        int max_pages, const int32_t* kv_len,
+                                        const int32_t* row_start, const void* q, qg_dtype q_dtype,
+                                        void* out, qg_dtype out_dtype, int B, int T, int H,
+                                        float scale, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* who = "qg_paged_attention";
+  if (qg_status s = pk::check_pool(who, kv, max_pages)) return s;
+  const int D = kv->head_dim, Hkv = kv->kv_heads;
+  QG_REQUIRE(B >= 0 && T >= 0 && H >= 1 && H <= 8192, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: B=%d T=%d H=%d", who, B, T, H);
+  QG_REQUIRE(H % Hkv == 0, QG_ERR_UNSUPPORTED_SHAPE, "%s: H=%d must be a multiple of kv_heads=%d",
+             who, H, Hkv);
+  QG_REQUIRE(B <= (1 << 16) && (long long)T * H <= (1LL << 30), QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: B=%d T=%d H=%d too large", who, B, T, H);
+  QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d rows without row_start must be B=%d", who, T, B);
+  QG_REQUIRE((q_dtype == QG_F32 || q_dtype == QG_BF16) &&
+                 (out_dtype == QG_F32 || out_dtype == QG_BF16),
+             QG_ERR_INVALID_ARGUMENT, "%s: q_dtype=%d out_dtype=%d", who, (int)q_dtype,
+             (int)out_dtype);
+  QG_REQUIRE(scale > 0.f && scale <= 3.402823466e38f, QG_ERR_INVALID_ARGUMENT,
+             "%s: scale must be positive and finite", who);
+  QG_REQUIRE((long long)kv->num_pages * Hkv * (kv->page_size / pk::kBlock) <= 0x7FFFFFFFLL,
+             QG_ERR_UNSUPPORTED_SHAPE, "%s: num_pages=%d: the pool is too large", who,
+             kv->num_pages);
+  if (B == 0 || T == 0) return QG_OK;
+  if (qg_status s = pk::check_pool_pointers(who, kv)) return s;
+  QG_REQUIRE(page_table && kv_len && q && out, QG_ERR_INVALID_ARGUMENT,
+             "%s: null page_table, kv_len, q or out", who);
+  QG_REQUIRE(aligned(q, 16) && aligned(out, 16), QG_ERR_MISALIGNED,
+             "%s: q or out not 16-byte aligned", who);
+  QG_REQUIRE(aligned(page_table, 4) && aligned(kv_len, 4) && aligned(row_start, 4),
+             QG_ERR_MISALIGNED, "%s: page_table, kv_len or row_start misaligned", who);
+  const size_t need = pa::ws_bytes(D);
+  QG_REQUIRE(ws && ws_bytes >= need, QG_ERR_WORKSPACE_TOO_SMALL,
+             "%s: workspace of %zu bytes given, %zu needed", who, ws_bytes, need);
+  QG_REQUIRE(aligned(ws, 256), QG_ERR_MISALIGNED, "%s: ws not 256-byte aligned", who);
+  const bool exact = q_dtype == QG_F32 || out_dtype == QG_F32;
+  const pa::Plan plan =
+      pa::plan(B, T, H, Hkv, D, (long long)max_pages * kv->page_size, exact);
+  pa::Params P = {};
+  P.q = q;
+  P.out = out;
+  P.kp = reinterpret_cast<const uint8_t*>(kv->k_pages);
+  P.vp = reinterpret_cast<const uint8_t*>(kv->v_pages);
+  P.ks = kv->k_scales;
+  P.vs = kv->v_scales;
+  P.table = page_table;
+  P.kv_len = kv_len;
+  P.row_start = row_start;
+  P.part = reinterpret_cast<float*>(ws);
+  P.q_bf16 = q_dtype == QG_BF16;
+  P.out_bf16 = out_dtype == QG_BF16;
+  P.B = B;
+  P.T = T;
+  P.H = H;
+  P.Hkv = Hkv;
+  P.G = H / Hkv;
+  P.bpp = kv->page_size / pk::kBlock;
+  P.max_pages = max_pages;
+  P.num_pages = kv->num_pages;
+  P.pieces = plan.pieces;
+  P.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  const bool i8 = kv->dtype == QG_KV_INT8;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (D == 64)
+    i8 ? pa::launch<64, true>(P, plan, exact, st) : pa::launch<64, false>(P, plan, exact, st);
+  else if (D == 128)
+    i8 ? pa::launch<128, true>(P, plan, exact, st) : pa::launch<128, false>(P, plan, exact, st);
+  else
+    i8 ? pa::launch<256, true>(P, plan, exact, st) : pa::launch<256, false>(P, plan, exact, st);
+  return check_launch(who);
+}
