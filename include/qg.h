@@ -555,6 +555,41 @@ qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* page_table, i
                              float scale, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Filtered sampling (no counterpart on the pages): temperature, top-k,
+ * top-p and min-p with parameters of each row's own, then a draw with a
+ * given uniform number. qg_sample has the page's repetition penalty and
+ * top-k with one setting for the batch.
+ *
+ * Candidates: the logits of a row that are not NaN and above -inf, in
+ * descending order, equal values (-0 and +0 among them) by index. Weights
+ * w = exp((l - max) / temperature); with a maximum of +inf, 1 for the
+ * infinite logits and 0 for the rest. Kept, in this order:
+ *   top-k: the first top_k candidates (0 or less: all);
+ *   top-p: of these, each before which less than top_p times their whole
+ *          weight lies (the first always; 1 or more, or NaN: all);
+ *   min-p: of these, those with w >= min_p (0 or less, or NaN: all; above 1
+ *          as 1).
+ * out[b] = the first kept candidate whose running weight reaches u[b] times
+ * the kept weight (u clamped to [0, 1]; NaN as 0). A temperature of 0 or
+ * less, or NaN, keeps the first candidate alone. A row without candidates
+ * gives out 0, kept 0, logprob NaN.
+ * logits   device fp32, row b at b * ld, ld >= V.
+ * temperature, top_p, min_p device fp32 [B] or NULL (1, 1, 0);
+ * top_k    device int32 [B] or NULL (0).   u device fp32 [B].
+ * out      device int32 [B].   kept device int32 [B] or NULL: how many
+ *          candidates were kept.   logprob device fp32 [B] or NULL: the log
+ *          of the drawn candidate's share of the kept weight.
+ * Weights and their sums are float64 and integers (rounded at 2^-44 of the
+ * largest weight, coarser past V = 2^18): the result does not depend on
+ * scheduling. One launch, no workspace. 1 <= V <= 2^22, B <= 65535; all
+ * pointers 4-byte aligned.
+ * ---------------------------------------------------------------------- */
+qg_status qg_sample_filtered(const float* logits, long long ld, int B, int V,
+                             const float* temperature, const int32_t* top_k, const float* top_p,
+                             const float* min_p, const float* u, int32_t* out, int32_t* kept,
+                             float* logprob, void* stream);
+
+/* ------------------------------------------------------------------------
  * Code predictor  [MK: makima src/tts/qwen3/code_predictor.rs,
  * CodePredictor::predict and CodePredictorLayer::forward]
  *

@@ -129,3 +129,22 @@ def test_attention_refusals():
     st, msg = _attend(_kv(num_pages=1 << 29))
     assert st == U and "too large" in msg
     assert _attend(B=0, T=0, q=None)[0] == qg.QG_OK
+
+
+def test_sample_filtered_refusals():
+    U, I, M = qg.QG_ERR_UNSUPPORTED_SHAPE, qg.QG_ERR_INVALID_ARGUMENT, qg.QG_ERR_MISALIGNED
+
+    def call(**kw):
+        a = dict(logits=FAKE, ld=1000, B=2, V=1000, t=None, k=None, p=None, m=None, u=FAKE, out=FAKE,
+                 kept=None, lp=None)
+        a.update(kw)
+        return _status("qg_sample_filtered", *a.values(), None)
+
+    for kw, code, word in ((dict(V=0), U, "V=0"), (dict(V=1 << 23, ld=1 << 23), U, "V="),
+                           (dict(ld=999), U, "ld=999"), (dict(B=-1), U, "B=-1"),
+                           (dict(B=70000), U, "B=70000"), (dict(logits=None), I, "logits"),
+                           (dict(u=None), I, "u"), (dict(out=None), I, "out"),
+                           (dict(t=FAKE + 2), M, "aligned"), (dict(logits=FAKE + 1), M, "aligned")):
+        st, msg = call(**kw)
+        assert st == code and word in msg, (kw, st, msg)
+    assert call(B=0, logits=None)[0] == qg.QG_OK

@@ -161,6 +161,7 @@ _SIGS = {
     "qg_paged_attention_workspace_size": (_sz, [_i]),
     "qg_paged_attention": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _sz,
                                 _vp]),
+    "qg_sample_filtered": (_i, [_vp, _ll, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "qg_step_graphs_enable": (None, [_i]),
     "qg_step_graphs_clear": (None, []),
     "qg_argmax_workspace_size": (_sz, [_i, _i]),
@@ -357,6 +358,30 @@ def qg_sample(logits, out, ws, past=None, penalty=1.0, temperature=1.0, top_k=0,
     P = 0 if past is None else past.shape[1]
     _call("qg_sample", _p(logits), B, V, _p(past), P, float(penalty), float(temperature),
           int(top_k), _p(r), _p(out), _p(ws), ws.numel() * ws.element_size(), _stream(stream))
+
+
+def qg_sample_filtered(logits, u, out, temperature=None, top_k=None, top_p=None, min_p=None,
+                       kept=None, logprob=None, stream=None):
+    """out[b] (int32 [B]): a token of logits[b] (fp32 [B, V], rows may lie
+    apart) drawn with the uniform number u[b] after temperature, top_k, top_p
+    and min_p, each a device tensor [B] (fp32; top_k int32) or None for off.
+    kept (int32) and logprob (fp32), when given, get the number of tokens
+    kept and the drawn one's log-probability among them."""
+    B, V = logits.shape
+    dev = torch.cuda.current_device()
+    _on_device(dev, logits=logits, u=u, out=out, temperature=temperature, top_k=top_k,
+               top_p=top_p, min_p=min_p, kept=kept, logprob=logprob)
+    if logits.dtype != torch.float32:
+        raise TypeError(f"logits must be float32, not {logits.dtype}")
+    ld = _rows_of("logits", logits, V)
+    for name, t, dt in (("u", u, torch.float32), ("out", out, torch.int32),
+                        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
+                        ("kept", kept, torch.int32), ("logprob", logprob, torch.float32)):
+        if t is not None and (t.dtype != dt or t.shape != (B,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dt} tensor of {B} values")
+    _call("qg_sample_filtered", _p(logits), ld, B, V, _p(temperature), _p(top_k), _p(top_p),
+          _p(min_p), _p(u), _p(out), _p(kept), _p(logprob), _stream(stream))
 
 
 def qg_decode_attention_static_scratch_capacity():
