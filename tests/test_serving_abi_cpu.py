@@ -96,9 +96,13 @@ def test_python_refusals():
         qg._rows_of("k", torch.zeros(64, 4).t(), 64)
     assert qg._rows_of("k", torch.zeros(4, 96)[:, 32:], 64) == 96
     with pytest.raises(ValueError, match="int32"):
-        qg._int32(kv_len=torch.zeros(3))
+        qg._check_index(-1, "kv_len", torch.zeros(3), 3)
+    with pytest.raises(ValueError, match="of 4 values"):
+        qg._check_index(-1, "kv_len", torch.zeros(3, dtype=torch.int32), 4)
     with pytest.raises(ValueError, match="cpu"):
-        qg._on_device(0, k=torch.zeros(3))
+        qg._check_index(0, "kv_len", torch.zeros(3, dtype=torch.int32), 3)
+    with pytest.raises(ValueError, match="cpu"):
+        qg._check_device(0, ("k", torch.zeros(3)))
 
 
 def _attend(kv=None, **kw):

@@ -197,6 +197,13 @@ def _stream(stream=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _raw_stream(stream, dev):
+    """``_stream`` without building a stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
 def _dt(t):
     if t.dtype == torch.float32:
         return QG_F32
@@ -369,19 +376,22 @@ def qg_sample_filtered(logits, u, out, temperature=None, top_k=None, top_p=None,
     kept and the drawn one's log-probability among them."""
     B, V = logits.shape
     dev = torch.cuda.current_device()
-    _on_device(dev, logits=logits, u=u, out=out, temperature=temperature, top_k=top_k,
-               top_p=top_p, min_p=min_p, kept=kept, logprob=logprob)
-    if logits.dtype != torch.float32:
+    if logits.dtype is not torch.float32:
         raise TypeError(f"logits must be float32, not {logits.dtype}")
     ld = _rows_of("logits", logits, V)
-    for name, t, dt in (("u", u, torch.float32), ("out", out, torch.int32),
-                        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
-                        ("kept", kept, torch.int32), ("logprob", logprob, torch.float32)):
-        if t is not None and (t.dtype != dt or t.shape != (B,) or not t.is_contiguous()):
+    f32, i32 = torch.float32, torch.int32
+    for name, t, dt in (("u", u, f32), ("out", out, i32), ("temperature", temperature, f32),
+                        ("top_k", top_k, i32), ("top_p", top_p, f32), ("min_p", min_p, f32),
+                        ("kept", kept, i32), ("logprob", logprob, f32), ("logits", logits, None)):
+        if t is None:
+            continue
+        if dt is not None and (t.dtype is not dt or t.shape != (B,) or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {dt} tensor of {B} values")
-    _call("qg_sample_filtered", _p(logits), ld, B, V, _p(temperature), _p(top_k), _p(top_p),
-          _p(min_p), _p(u), _p(out), _p(kept), _p(logprob), _stream(stream))
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+    _call("qg_sample_filtered", logits.data_ptr(), ld, B, V, _p(temperature), _p(top_k), _p(top_p),
+          _p(min_p), u.data_ptr(), out.data_ptr(), _p(kept), _p(logprob),
+          _raw_stream(stream, dev))
 
 
 def qg_decode_attention_static_scratch_capacity():
@@ -411,26 +421,33 @@ def qg_dequant_q4_0(blocks, out, stream=None):
 
 
 # ------------------------------------------------------------ paged cache ----
+# A serving loop makes these calls once a layer and token, so their checks
+# are written to cost little: plain loops, no keyword dictionaries.
 
-def _on_device(dev, **tensors):
-    """Every given tensor lives on CUDA device ``dev`` (an index)."""
-    for name, t in tensors.items():
+def _check_device(dev, *named):
+    """Every given tensor of the (name, tensor) pairs is on CUDA device ``dev``."""
+    for name, t in named:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
 
 
-def _int32(**tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
+def _check_index(dev, name, t, n):
+    """A contiguous int32 tensor of n values on device ``dev``."""
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
 
 
 def _rows_of(name, t, width):
     """Row stride (elements) of [rows, width] whose rows may lie apart."""
-    if t.dim() != 2 or t.shape[1] != width or (t.shape[0] and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, {width}] with unit stride along a row, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    shape = t.shape
+    if len(shape) == 2 and shape[1] == width:
+        ld, one = t.stride()
+        if one == 1 or shape[0] == 0:
+            return ld if shape[0] > 1 else max(ld, width)
+    raise ValueError(f"{name} must be [rows, {width}] with unit stride along a row, got "
+                     f"{tuple(shape)} with strides {t.stride()}")
 
 
 class PagedKV:
@@ -440,27 +457,30 @@ class PagedKV:
     page_size / 16]. The tensors are borrowed and kept alive."""
 
     def __init__(self, k_pages, v_pages, k_scales=None, v_scales=None):
-        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        shape, dtype = k_pages.shape, k_pages.dtype
+        if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
             raise ValueError("k_pages and v_pages must be [num_pages, kv_heads, page_size, "
                              "head_dim] of one type")
-        if k_pages.dtype not in (torch.bfloat16, torch.int8):
-            raise TypeError(f"pages must be bfloat16 or int8, not {k_pages.dtype}")
-        P, Hkv, size, D = k_pages.shape
-        int8 = k_pages.dtype == torch.int8
+        int8 = dtype is torch.int8
+        if not int8 and dtype is not torch.bfloat16:
+            raise TypeError(f"pages must be bfloat16 or int8, not {dtype}")
+        P, Hkv, size, D = shape
+        self.device_index = dev = k_pages.get_device()
         for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
             if (s is not None) != int8:
                 raise ValueError(f"{name} goes with int8 pages only, and they need it")
-            if int8 and (s.dtype != torch.float32 or s.shape != (P, Hkv, size // QG_KV_BLOCK)
-                         or not s.is_contiguous()):
+            if int8 and (s.dtype is not torch.float32 or s.shape != (P, Hkv, size // QG_KV_BLOCK)
+                         or not s.is_contiguous() or s.get_device() != dev):
                 raise ValueError(f"{name} must be contiguous fp32 "
-                                 f"[{P}, {Hkv}, {size // QG_KV_BLOCK}]")
-        if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
-            raise ValueError("k_pages and v_pages must be contiguous")
+                                 f"[{P}, {Hkv}, {size // QG_KV_BLOCK}] on the pages' device")
+        if not (k_pages.is_contiguous() and v_pages.is_contiguous()
+                and v_pages.get_device() == dev):
+            raise ValueError("k_pages and v_pages must be contiguous, on one device")
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = (k_pages, v_pages, k_scales,
                                                                     v_scales)
         self.kv_heads, self.page_size, self.head_dim = Hkv, size, D
-        self.c_kv = qg_paged_kv(_p(k_pages), _p(v_pages), _p(k_scales), _p(v_scales), P, size, Hkv,
-                                D, QG_KV_INT8 if int8 else QG_KV_BF16)
+        self.c_kv = qg_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), _p(k_scales),
+                                _p(v_scales), P, size, Hkv, D, QG_KV_INT8 if int8 else QG_KV_BF16)
         self._ref = ctypes.byref(self.c_kv)
 
     @classmethod
@@ -473,24 +493,23 @@ class PagedKV:
                       for _ in range(2)]
         return cls(*pages)
 
-    def _batch(self, page_table, lens, row_start, T, dev):
-        """B, after checking the batch's index tensors."""
-        _on_device(dev, k_pages=self.k_pages, v_pages=self.v_pages, k_scales=self.k_scales,
-                   v_scales=self.v_scales, page_table=page_table, row_start=row_start)
-        _int32(page_table=page_table, row_start=row_start)
-        if page_table.dim() != 2:
+    def _batch(self, page_table, lens, lens_name, row_start, T, dev):
+        """(B, max_pages), after checking the batch's index tensors."""
+        if self.device_index != dev:
+            raise ValueError(f"the pages are on device {self.device_index}, not on the current "
+                             f"device cuda:{dev}")
+        shape = page_table.shape
+        if len(shape) != 2:
             raise ValueError("page_table must be [B, max_pages]")
-        B = page_table.shape[0]
+        B, most = shape
+        _check_index(dev, "page_table", page_table, B * most)
         if lens is not None:
-            _on_device(dev, kv_len=lens)
-            _int32(kv_len=lens)
-            if lens.numel() != B:
-                raise ValueError(f"{lens.numel()} lengths for {B} sequences")
-        if row_start is not None and row_start.numel() != B + 1:
-            raise ValueError(f"row_start must have {B + 1} entries")
-        if row_start is None and T != B:
+            _check_index(dev, lens_name, lens, B)
+        if row_start is not None:
+            _check_index(dev, "row_start", row_start, B + 1)
+        elif T != B:
             raise ValueError(f"{T} rows of {B} sequences need row_start")
-        return B
+        return B, most
 
 
 def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_out=None,
@@ -504,48 +523,53 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
     row_start int32 [B+1], or None for one row per sequence. ``rotary_dim``
     None: the whole head."""
     dev = torch.cuda.current_device()
-    D, W, T = kv.head_dim, kv.kv_heads * kv.head_dim, k.shape[0]
-    _on_device(dev, q=q, k=k, v=v, q_out=q_out, q_norm=q_norm, k_norm=k_norm)
-    B = kv._batch(page_table, kv_len, row_start, T, dev)
+    D = kv.head_dim
+    W = kv.kv_heads * D
+    T, dt = k.shape[0], k.dtype
     if kv_len is None:
         raise ValueError("kv_len is needed")
+    B, most = kv._batch(page_table, kv_len, "kv_len", row_start, T, dev)
     k_ld, v_ld = _rows_of("k", k, W), _rows_of("v", v, W)
-    if v.shape[0] != T or v.dtype != k.dtype:
+    if v.shape[0] != T or v.dtype is not dt:
         raise ValueError("v must have k's rows and type")
     H, q_ld, qdt = 0, 0, QG_BF16
     if q is not None:
-        if q.dim() != 2 or q.shape[0] != T or q.dtype != k.dtype or q.shape[1] % D:
+        Q = q.shape[-1]
+        if q.shape[0] != T or q.dtype is not dt or Q % D:
             raise ValueError(f"q must be [{T}, H * {D}] of k's type")
-        H, q_ld = q.shape[1] // D, _rows_of("q", q, q.shape[1])
+        H, q_ld = Q // D, _rows_of("q", q, Q)
         if q_out is None or q_out.shape != q.shape or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous with q's shape")
         qdt = _dt(q_out)
+    _check_device(dev, ("k", k), ("v", v), ("q", q), ("q_out", q_out), ("q_norm", q_norm),
+                  ("k_norm", k_norm))
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
         if w is not None and (w.numel() != D or w.element_size() != 2 or not w.is_contiguous()):
             raise ValueError(f"{name} must be {D} bf16 values")
-    _call("qg_paged_kv_append", kv._ref, _p(page_table), page_table.shape[1], _p(kv_len),
-          _p(row_start), _p(q), q_ld, _p(k), k_ld, _p(v), v_ld, _dt(k), _p(q_norm), _p(k_norm),
-          eps, theta, D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
-          _stream(stream))
+    _call("qg_paged_kv_append", kv._ref, page_table.data_ptr(), most, kv_len.data_ptr(),
+          _p(row_start), _p(q), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, _dt(k), _p(q_norm),
+          _p(k_norm), eps, theta, D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
+          _raw_stream(stream, dev))
 
 
 def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None, stream=None):
     """Cached rows as values: packed row i of sequence b is its token
     first[b] + i (first int32 [B] or None: from 0; row_start int32 [B+1] or
     None: one row each). k_out, v_out contiguous [T, Hkv*D], fp32 or bf16."""
-    dev = torch.cuda.current_device()
-    W = kv.kv_heads * kv.head_dim
-    outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs:
+    one = k_out if k_out is not None else v_out
+    if one is None:
         return
-    _on_device(dev, k_out=k_out, v_out=v_out)
-    T = outs[0].shape[0]
-    B = kv._batch(page_table, first, row_start, T, dev)
-    for t in outs:
-        if t.shape != (T, W) or t.dtype != outs[0].dtype or not t.is_contiguous():
-            raise ValueError(f"k_out and v_out must be contiguous [{T}, {W}] of one type")
-    _call("qg_paged_kv_gather", kv._ref, _p(page_table), page_table.shape[1], _p(first),
-          _p(row_start), _p(k_out), _p(v_out), _dt(outs[0]), B, T, _stream(stream))
+    dev = torch.cuda.current_device()
+    T = one.shape[0]
+    B, most = kv._batch(page_table, first, "first", row_start, T, dev)
+    for t in (k_out, v_out):
+        if t is not None and (t.shape != (T, kv.kv_heads * kv.head_dim) or t.dtype is not one.dtype
+                              or not t.is_contiguous()):
+            raise ValueError(f"k_out and v_out must be contiguous [{T}, "
+                             f"{kv.kv_heads * kv.head_dim}] of one type")
+    _check_device(dev, ("k_out", k_out), ("v_out", v_out))
+    _call("qg_paged_kv_gather", kv._ref, page_table.data_ptr(), most, _p(first), _p(row_start),
+          _p(k_out), _p(v_out), _dt(one), B, T, _raw_stream(stream, dev))
 
 
 def qg_paged_attention_workspace_size(head_dim):
@@ -560,16 +584,16 @@ def qg_paged_attention(kv, page_table, kv_len, q, out, H, scale, ws, row_start=N
     per sequence; ws of qg_paged_attention_workspace_size(D) bytes."""
     dev = torch.cuda.current_device()
     T = q.shape[0]
-    _on_device(dev, q=q, out=out, ws=ws)
-    B = kv._batch(page_table, kv_len, row_start, T, dev)
     if kv_len is None:
         raise ValueError("kv_len is needed")
+    B, most = kv._batch(page_table, kv_len, "kv_len", row_start, T, dev)
     if q.shape != (T, H * kv.head_dim) or out.shape != q.shape or \
             not (q.is_contiguous() and out.is_contiguous()):
         raise ValueError(f"q and out must be contiguous [T, {H} * {kv.head_dim}]")
-    _call("qg_paged_attention", kv._ref, _p(page_table), page_table.shape[1], _p(kv_len),
-          _p(row_start), _p(q), _dt(q), _p(out), _dt(out), B, T, H, scale, _p(ws),
-          ws.numel() * ws.element_size(), _stream(stream))
+    _check_device(dev, ("q", q), ("out", out), ("ws", ws))
+    _call("qg_paged_attention", kv._ref, page_table.data_ptr(), most, kv_len.data_ptr(),
+          _p(row_start), q.data_ptr(), _dt(q), out.data_ptr(), _dt(out), B, T, H, scale,
+          ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev))
 
 
 # ---------------------------------------------------------- decode step ----

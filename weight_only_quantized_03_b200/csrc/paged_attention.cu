@@ -62,7 +62,8 @@ constexpr int kWarps = 8;            // split kernel
 constexpr int kChunk = kWarps * kBlock;
 constexpr int kWholeWarps = 4;       // whole kernel
 constexpr int kWholeNT = 4;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 512;
+constexpr int kMaxPieces = 320;      // of the split kernel (two CTAs on each of 148 SMs)
 constexpr float kMargin = 4.f;       // log2 of how far a weight may pass 1
 
 struct Params {
@@ -151,12 +152,34 @@ __device__ __forceinline__ int visible(const Params& P, const Item& it, int c) {
   return i < it.n ? it.len - it.n + i + 1 : 0x7FFFFFFF;
 }
 
-__device__ __forceinline__ float load_q(const Params& P, const Item& it, int c, int d, int D) {
+// The lane's D/32 neighbouring values of column c's query head.
+template <int D>
+__device__ __forceinline__ void load_q(const Params& P, const Item& it, int c, int lane,
+                                       float (&x)[D / 32]) {
+  constexpr int EPL = D / 32;
   const int i = c / P.G;
-  if (i >= it.n) return 0.f;
-  const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D + d;
-  return P.q_bf16 ? bf16_bits_to_f32(__ldcg(reinterpret_cast<const uint16_t*>(P.q) + at))
-                  : __ldcg(reinterpret_cast<const float*>(P.q) + at);
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) x[e] = 0.f;
+  if (i >= it.n) return;
+  const long long at =
+      ((long long)(it.r0 + i) * P.H + it.h * P.G + (c - i * P.G)) * D + lane * EPL;
+  if (P.q_bf16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(P.q) + at;
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2) {
+      const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(p + e));
+      x[e] = bf16_lo(w);
+      x[e + 1] = bf16_hi(w);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(P.q) + at;
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2) {
+      const float2 w = __ldcg(reinterpret_cast<const float2*>(p + e));
+      x[e] = w.x;
+      x[e + 1] = w.y;
+    }
+  }
 }
 
 // Where element (column n, dim d) of Q lies in the fragments' order
@@ -169,16 +192,15 @@ __device__ __forceinline__ int q_at(int n, int d, int term) {
   return (((ks * NT + n / 8) * QS + term) * 32 + (n % 8) * 4 + t) * 4 + d % 4;
 }
 
-// Stores four neighbouring values of one column, split into QS terms.
-template <bool I8, int NT, int QS>
-__device__ __forceinline__ void put_q(uint16_t* sq, int n, int d, float (&x)[4]) {
+// Stores a lane's neighbouring values of one column, split into QS terms.
+template <int D, bool I8, int NT, int QS>
+__device__ __forceinline__ void put_q(uint16_t* sq, int n, int lane, float (&x)[D / 32]) {
 #pragma unroll
-  for (int s = 0; s < QS; ++s) {
-    uint2 w;
-    w.x = take16<I8>(x[0], x[1]);
-    w.y = take16<I8>(x[2], x[3]);
-    *reinterpret_cast<uint2*>(sq + q_at<I8, NT, QS>(n, d, s)) = w;
-  }
+  for (int s = 0; s < QS; ++s)
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<uint32_t*>(sq + q_at<I8, NT, QS>(n, lane * (D / 32) + e, s)) =
+          take16<I8>(x[e], x[e + 1]);
 }
 
 // 2^e that brings the largest |q| into [2^13, 2^14) (int8 pages).
@@ -219,18 +241,19 @@ struct Walk {
   const int lane, g, t;
   int lim[NT][2];     // visible tokens of the lane's columns
   int min_lim, len;   // of all the item's columns; cached tokens
-  float qf;           // scale_log2 / 2^e
+  float qf[NT][2];    // scale_log2 / 2^e of the lane's columns
   const uint16_t* sq;
   uint4 kr[2][KC];
   uint4 vr[4][VC];
   float ks, vs;
   int blocks;         // lane i: block index in the pool of tile base + i step, -1: bad page
+  int tile, step, end;
 
   __device__ __forceinline__ Walk(const Params& P_, int lane_)
       : P(P_), lane(lane_), g(lane_ >> 2), t(lane_ & 3) {}
 
-  __device__ __forceinline__ void lookup(const Item& it, int tile, int step, int end) {
-    const long long at = (long long)tile + (long long)lane * step;
+  __device__ __forceinline__ void lookup(const Item& it, int first) {
+    const long long at = (long long)first + (long long)lane * step;
     blocks = -1;
     if (at < end) {
       const int pi = (int)at / P.bpp;
@@ -253,7 +276,7 @@ struct Walk {
   }
 
   // Rows at or past the sequence's end hold anything: zero (0 * NaN).
-  __device__ __forceinline__ void load_v(int blk, int tile) {
+  __device__ __forceinline__ void load_v(int blk) {
     const bool ok = blk >= 0;
     const int left = I8 ? kBlock : len - tile * kBlock;
     const uint8_t* p = P.vp + (long long)(ok ? blk : 0) * (kBlock * D * ES) + g * VB;
@@ -401,25 +424,36 @@ struct Walk {
     }
   }
 
-  __device__ __forceinline__ void run(State<D, NT>& S, const Item& it, int first, int step,
-                                      int end) {
-    if (first >= end) return;
-    int at = 0;  // tile `first + at * step` of the current batch of lookups
-    int tile = first;
-    lookup(it, tile, step, end);
-    int blk = __shfl_sync(0xffffffffu, blocks, 0);
+  // The walk's tiles; the first one's loads go out.
+  __device__ __forceinline__ void begin(const Item& it, int first, int step_, int end_) {
+    tile = first;
+    step = step_;
+    end = end_;
+    if (tile >= end) return;
+    lookup(it, tile);
+    const int blk = __shfl_sync(0xffffffffu, blocks, 0);
     load_k(blk);
-    load_v(blk, tile);
+    load_v(blk);
+  }
+
+  __device__ __forceinline__ void run(State<D, NT>& S, const Item& it) {
+    if (tile >= end) return;
+    int at = 0;  // the tile's place in the batch of lookups
     for (;;) {
       const bool more = end - tile > step;
       if (more && ++at == 32) {
         at = 0;
-        lookup(it, tile + step, step, end);
+        lookup(it, tile + step);
       }
       const int next = __shfl_sync(0xffffffffu, blocks, at);
       float p[NT][4];
       scores(p);
-      const float f = qf * ks;
+      float f[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        f[j][0] = qf[j][0] * ks;
+        f[j][1] = qf[j][1] * ks;
+      }
       if (more) load_k(next);
       // scores in log2 units, masked
       const int key0 = tile * kBlock + g;
@@ -429,7 +463,7 @@ struct Walk {
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[j][e] *= f;
+          p[j][e] *= f[j][e & 1];
           if (part && key0 + 8 * (e >> 1) >= lim[j][e & 1]) p[j][e] = -INFINITY;
           over |= p[j][e] > S.m[j][e & 1] + kMargin;
         }
@@ -482,7 +516,7 @@ struct Walk {
       weigh(S, p, part);
       if (!more) break;
       tile += step;
-      load_v(next, tile);
+      load_v(next);
     }
   }
 };
@@ -493,41 +527,41 @@ __device__ __forceinline__ float o_unit(float r) {
   return I8 ? r * (1.f / 2048.f) : 1.f;
 }
 
-// Sets up a walk over the item's column tile: q into shared memory by the
-// `nthr` threads that call this (id `id` of them), limits per lane.
+// q of the item's column tile into shared memory, a warp per column, with
+// the factor that turns a column's products into log2 units in sf.
 template <int D, bool I8, int NT, int QS>
-__device__ __forceinline__ float stage_q(const Params& P, const Item& it, uint16_t* sq, int id,
-                                         int nthr, float top) {
-  const float unit = I8 ? q_unit(top) : 1.f;
-  for (int i = id; i < NT * 8 * D / 4; i += nthr) {
-    const int n = i / (D / 4), d = i % (D / 4) * 4;
-    float x[4];
+__device__ __forceinline__ void stage_q(const Params& P, const Item& it, uint16_t* sq, float* sf,
+                                        int warp, int warps, int lane) {
+#pragma unroll 8
+  for (int n = warp; n < NT * 8; n += warps) {
+    float x[D / 32];
+    load_q<D>(P, it, it.ct * NT * 8 + n, lane, x);
+    float unit = 1.f;
+    if constexpr (I8) {
+      float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = load_q(P, it, it.ct * NT * 8 + n, d + e, D) * unit;
-    put_q<I8, NT, QS>(sq, n, d, x);
+      for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(x[e]));
+      unit = q_unit(warp_max(top));
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x[e] *= unit;
+    }
+    put_q<D, I8, NT, QS>(sq, n, lane, x);
+    if (lane == 0) sf[n] = P.scale_log2 / unit;
   }
-  return P.scale_log2 / unit;
 }
 
-template <int D, int NT>
-__device__ __forceinline__ float q_top(const Params& P, const Item& it, int id, int nthr) {
-  float top = 0.f;
-  for (int i = id; i < NT * 8 * D; i += nthr)
-    top = fmaxf(top, fabsf(load_q(P, it, it.ct * NT * 8 + i / D, i % D, D)));
-  return warp_max(top);
-}
-
-template <class W>
-__device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w, int NT) {
+template <int NT, class W>
+__device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w) {
   int lo = 0x7FFFFFFF;
+#pragma unroll
   for (int j = 0; j < NT; ++j)
+#pragma unroll
     for (int e = 0; e < 2; ++e) {
       w.lim[j][e] = visible(P, it, it.ct * NT * 8 + j * 8 + 2 * w.t + e);
       lo = min(lo, w.lim[j][e]);
     }
   lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
   w.min_lim = min(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
-  w.len = it.len;
 }
 
 __device__ __forceinline__ void store_out(const Params& P, const Item& it, int c, int d, int D,
@@ -584,9 +618,69 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* buf, l
   return before + x - v;
 }
 
-// First chunk of piece c of N chunks in `pieces`.
-__device__ __forceinline__ long long piece_begin(long long N, int c, int pieces) {
-  return N * c / pieces;
+// The line of N chunks cut into pieces: the first `rem` have q + 1 chunks,
+// the others q.
+struct Cut {
+  long long q;
+  int rem;
+  __device__ __forceinline__ Cut(long long N, int pieces) {
+    q = N >> 31 ? N / pieces : (long long)((unsigned)N / (unsigned)pieces);
+    rem = (int)(N - q * pieces);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return q * c + min(c, rem); }
+  __device__ __forceinline__ int piece_of(long long x) const {
+    const long long wide = (q + 1) * rem;
+    const long long y = x < wide ? x : x - wide, d = x < wide ? q + 1 : q;
+    const int i = y >> 31 ? (int)(y / d) : (int)((unsigned)y / (unsigned)d);
+    return x < wide ? i : rem + i;
+  }
+};
+
+// Sequence whose chunks hold place `pos` of the line, and the place within
+// them; *N gets the line's length. For up to 32 sequences every warp finds it
+// by itself (`pos_of` gets N).
+template <int NTHR, int NC, class F>
+__device__ __forceinline__ int find_seq(const Params& P, F pos_of, long long* N, long long* rest) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (P.B <= 32) {
+    const long long mine = lane < P.B ? seq_work(P, lane, NC).total(P.Hkv) : 0;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    *N = __shfl_sync(0xffffffffu, x, 31);
+    const long long pos = pos_of(*N);
+    const unsigned m = __ballot_sync(0xffffffffu, pos < x);
+    const int b = m ? __ffs(m) - 1 : 0;
+    *rest = pos - __shfl_sync(0xffffffffu, x - mine, b);
+    return b;
+  }
+  __shared__ long long buf[NTHR / 32], s_rest;
+  __shared__ int s_b;
+  const int per = (P.B + NTHR - 1) / NTHR;
+  long long mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
+  }
+  const long long before = block_prefix<NTHR>(mine, buf, N);
+  const long long pos = pos_of(*N);
+  if (pos >= before && pos < before + mine) {
+    long long r = pos - before;
+    int b = tid * per;
+    for (;; ++b) {
+      const long long w = seq_work(P, b, NC).total(P.Hkv);
+      if (r < w) break;
+      r -= w;
+    }
+    s_b = b;
+    s_rest = r;
+  }
+  __syncthreads();
+  *rest = s_rest;
+  return s_b;
 }
 
 template <int D, bool I8, int NT, int QS, int PS>
@@ -598,65 +692,52 @@ split_kernel(const __grid_constant__ Params P) {
   float* sm = so + kWarps * NC * D;                      // [kWarps][NC]
   float* sl = sm + kWarps * NC;                          // [kWarps][NC]
   uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * NC);  // fragments of q
-  __shared__ long long buf[kWarps], s_rest;
-  __shared__ int s_b;
-  __shared__ float s_top[kWarps];
+  __shared__ float sf[NC];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
+  pdl_trigger();  // the merge may find its items meanwhile
 
-  // the line of all chunks, sequence after sequence; this CTA's piece of it
-  const int per = (P.B + kWarps * 32 - 1) / (kWarps * 32);
-  long long mine = 0, N;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
-  }
-  const long long before = block_prefix<kWarps * 32>(mine, buf, &N);
-  long long pos = piece_begin(N, blockIdx.x, P.pieces);
-  const long long stop = piece_begin(N, blockIdx.x + 1, P.pieces);
+  long long N, pos = 0, stop = 0, rest;
+  const int b0 = find_seq<kWarps * 32, NC>(
+      P,
+      [&](long long n) {
+        const Cut cut(n, P.pieces);
+        pos = cut.begin(blockIdx.x);
+        stop = cut.begin(blockIdx.x + 1);
+        return pos;
+      },
+      &N, &rest);
   if (pos >= stop) return;
-  if (pos >= before && pos < before + mine) {
-    long long rest = pos - before;
-    int b = tid * per;
-    for (;; ++b) {
-      const long long w = seq_work(P, b, NC).total(P.Hkv);
-      if (rest < w) break;
-      rest -= w;
-    }
-    s_b = b;
-    s_rest = rest;
-  }
-  __syncthreads();
   Item it;
-  set_seq(P, it, s_b);
-  SeqWork w = seq_work(P, s_b, NC);
-  int unit = (int)(s_rest / w.chunks);   // (head, column tile) of the sequence
-  int c0 = (int)(s_rest % w.chunks);     // first chunk of the item in this piece
+  set_seq(P, it, b0);
+  SeqWork w = seq_work(P, b0, NC);
+  // (head, column tile) of the sequence, and the item's first chunk here
+  int unit = rest >> 31 ? (int)(rest / w.chunks) : (int)((unsigned)rest / (unsigned)w.chunks);
+  int c0 = (int)(rest - (long long)unit * w.chunks);
 
   Walk<D, I8, NT, QS, PS> walk(P, lane);
   walk.sq = sq;
   State<D, NT> S;
   while (pos < stop) {
     it.h = unit / w.tiles;
-    it.ct = unit % w.tiles;
+    it.ct = unit - it.h * w.tiles;
     const int c1 = (int)min((long long)w.chunks, c0 + (stop - pos));
-    // q of the item's columns
-    float top = 0.f;
-    if (I8) {
-      top = q_top<D, NT>(P, it, tid, kWarps * 32);
-      if (lane == 0) s_top[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, s_top[i]);
-    }
-    walk.qf = stage_q<D, I8, NT, QS>(P, it, sq, tid, kWarps * 32, top);
-    set_limits(P, it, walk, NT);
+    walk.len = it.len;
+    walk.begin(it, c0 * kWarps + warp, kWarps,
+               min(c1 * kWarps, (it.len + kBlock - 1) / kBlock));
+    stage_q<D, I8, NT, QS>(P, it, sq, sf, warp, kWarps, lane);
+    set_limits<NT>(P, it, walk);
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      walk.qf[j][0] = sf[j * 8 + 2 * walk.t];
+      walk.qf[j][1] = sf[j * 8 + 2 * walk.t + 1];
+    }
     S.clear();
-    const int end = min(c1 * kWarps, (it.len + kBlock - 1) / kBlock);
-    walk.run(S, it, c0 * kWarps + warp, kWarps, end);
+    walk.run(S, it);
     // the warps' states to shared memory: weights summed over the lanes that
     // share a column, outputs in plain units
+    const int cols = min(NC, it.n * P.G - it.ct * NC);  // of the tile, real ones
     const float u = o_unit<I8>(S.r);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -667,20 +748,22 @@ split_kernel(const __grid_constant__ Params P) {
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         const int n = j * 8 + 2 * walk.t + e;
-        if (walk.g == 0) {
-          sm[warp * NC + n] = S.m[j][e];
-          sl[warp * NC + n] = l;
-        }
+        if (n < cols) {
+          if (walk.g == 0) {
+            sm[warp * NC + n] = S.m[j][e];
+            sl[warp * NC + n] = l;
+          }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(so + (warp * NC + n) * D + walk.g * (D / 8) + 2 * i) =
-              make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
+          for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<float2*>(so + (warp * NC + n) * D + walk.g * (D / 8) + 2 * i) =
+                make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
+        }
       }
     }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == w.chunks;
     float* part = P.part + (long long)(2 * blockIdx.x + (c0 == 0)) * NC * (D + 2);
-    for (int i = tid; i < NC * D; i += kWarps * 32) {
+    for (int i = tid; i < cols * D; i += kWarps * 32) {
       const int n = i / D, d = i % D;
       float M = sm[n];
 #pragma unroll
@@ -702,47 +785,40 @@ split_kernel(const __grid_constant__ Params P) {
         }
       }
     }
-    __syncthreads();
     pos += c1 - c0;
     c0 = 0;
-    if (pos < stop && ++unit == w.tiles * P.Hkv) {
-      unit = 0;
-      do {  // the next sequence with rows (one exists: chunks are left)
-        set_seq(P, it, it.b + 1);
-        w = seq_work(P, it.b, NC);
-      } while (w.tiles == 0);
+    if (pos < stop) {
+      __syncthreads();  // shared memory is used again
+      if (++unit == w.tiles * P.Hkv) {
+        unit = 0;
+        do {  // the next sequence with rows (one exists: chunks are left)
+          set_seq(P, it, it.b + 1);
+          w = seq_work(P, it.b, NC);
+        } while (w.tiles == 0);
+      }
     }
   }
 }
 
-// Items cut between pieces: one CTA per (sequence, head, column tile) slot.
+// Items cut between pieces: one CTA per (column tile, head). A column tile's
+// slot: a sequence with x columns has at most x / NC + 1 tiles, so slot
+// ranges [begin G / NC + b, end G / NC + b + 1) do not overlap.
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Params P) {
   constexpr int NC = NT * 8;
-  __shared__ long long buf[kMergeThreads / 32], s_begin;
+  __shared__ float sw[NC][kMaxPieces];  // pieces' factors
+  __shared__ float acc[kMergeThreads];
   __shared__ int s_b;
-  const int tid = threadIdx.x;
-  pdl_wait();
-  // sequence whose slot range holds this CTA's column tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the split kernel's CTAs have passed their own wait, so what came before
+  // it on the stream is complete: lengths and row starts may be read)
   const int u = blockIdx.x;
   if (tid == 0) s_b = -1;
-  const int per = (P.B + kMergeThreads - 1) / kMergeThreads;
-  long long mine = 0, N;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
-  }
-  long long before = block_prefix<kMergeThreads>(mine, buf, &N);
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b >= P.B) break;
-    const long long lo = (long long)row_begin(P.row_start, b, P.T) * P.G / NC + b;
-    const long long hi = (long long)row_begin(P.row_start, b + 1, P.T) * P.G / NC + b + 1;
-    if (lo <= u && u < hi) {
-      s_b = b;
-      s_begin = before;
-    }
-    before += seq_work(P, b, NC).total(P.Hkv);
+  __syncthreads();
+  for (int i = tid; i < P.B; i += kMergeThreads) {
+    const long long lo = (long long)row_begin(P.row_start, i, P.T) * P.G / NC + i;
+    const long long hi = (long long)row_begin(P.row_start, i + 1, P.T) * P.G / NC + i + 1;
+    if (lo <= u && u < hi) s_b = i;
   }
   __syncthreads();
   if (s_b < 0) return;
@@ -752,26 +828,75 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   it.ct = u - (int)((long long)it.r0 * P.G / NC + s_b);
   it.h = blockIdx.y;
   if (it.ct >= w.tiles) return;
-  const long long begin = s_begin + (long long)(it.h * w.tiles + it.ct) * w.chunks;
-  const long long last = begin + w.chunks - 1;
-  // the pieces that hold the item's first and last chunks
-  const int p0 = (int)(((begin + 1) * P.pieces - 1) / N);
-  const int p1 = (int)(((last + 1) * P.pieces - 1) / N);
+  // chunks before the sequence, and the line's length
+  long long before = 0, N = 0;
+  for (int i = tid; i < P.B; i += kMergeThreads) {
+    const long long c = seq_work(P, i, NC).total(P.Hkv);
+    N += c;
+    before += i < s_b ? c : 0;
+  }
+  __shared__ long long r_n[kMergeThreads / 32], r_b[kMergeThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    N += __shfl_xor_sync(0xffffffffu, N, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    r_n[warp] = N;
+    r_b[warp] = before;
+  }
+  __syncthreads();
+  N = before = 0;
+#pragma unroll
+  for (int i = 0; i < kMergeThreads / 32; ++i) {
+    N += r_n[i];
+    before += r_b[i];
+  }
+  const long long begin = before + (long long)(it.h * w.tiles + it.ct) * w.chunks;
+  const Cut cut(N, P.pieces);
+  const int p0 = cut.piece_of(begin), p1 = cut.piece_of(begin + w.chunks - 1);
   if (p0 == p1) return;  // written by its piece
-  for (int i = tid; i < NC * D; i += kMergeThreads) {
-    const int n = i / D, d = i % D;
-    float M = -FLT_MAX, L = 0.f, O = 0.f;
-    for (int p = p0; p <= p1; ++p) {
-      if (piece_begin(N, p, P.pieces) == piece_begin(N, p + 1, P.pieces)) continue;  // empty
-      const float* part = P.part + (long long)(2 * p + (p == p0)) * NC * (D + 2);
-      const float m = __ldcg(part + n);
-      const float x = fmaxf(M, m);
-      const float a = ex2(M - x), c = ex2(m - x);
-      L = L * a + __ldcg(part + NC + n) * c;
-      O = O * a + __ldcg(part + 2 * NC + i) * c;
-      M = x;
+  pdl_wait();
+  const int np = p1 - p0 + 1, cols = min(NC, it.n * P.G - it.ct * NC);
+  // part of piece p0 + p: it begins the item in its second slot
+  auto part = [&](int p) {
+    return P.part + (long long)(2 * (p0 + p) + (p == 0)) * NC * (D + 2);
+  };
+  for (int n = warp; n < cols; n += kMergeThreads / 32) {
+    float M = -FLT_MAX, L = 0.f;
+    for (int p = lane; p < np; p += 32) {
+      const float m = __ldcg(part(p) + n);
+      sw[n][p] = m;
+      M = fmaxf(M, m);
     }
-    store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+    M = warp_max(M);
+    for (int p = lane; p < np; p += 32) {
+      const float a = ex2(sw[n][p] - M);
+      sw[n][p] = a;
+      L = fmaf(a, __ldcg(part(p) + NC + n), L);
+    }
+    L = warp_sum(L);
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    for (int p = lane; p < np; p += 32) sw[n][p] *= inv;
+  }
+  __syncthreads();
+  // few outputs: several groups of threads share the pieces
+  const int outs = cols * D, groups = max(1, min(np, kMergeThreads / outs));
+  const int width = groups == 1 ? kMergeThreads : outs, grp = tid / width;
+  for (int i = tid - grp * width; i < outs; i += width) {
+    const int n = i / D, d = i % D;
+    float O = 0.f;
+    if (grp < groups) {
+#pragma unroll 8
+      for (int p = grp; p < np; p += groups) O = fmaf(sw[n][p], __ldcg(part(p) + 2 * NC + i), O);
+    }
+    if (groups > 1) {
+      acc[tid] = O;
+      __syncthreads();
+      if (grp == 0)
+        for (int g = 1; g < groups; ++g) O += acc[g * width + i];
+    }
+    if (grp == 0) store_out(P, it, it.ct * NC + n, d, D, O);
   }
 }
 
@@ -783,7 +908,9 @@ __global__ void __launch_bounds__(kWholeWarps * 32) whole_kernel(const __grid_co
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* sq = reinterpret_cast<uint16_t*>(smem) + warp * (NC * D * QS);
+  __shared__ float sf[kWholeWarps][NC];
   pdl_wait();
+  pdl_trigger();
   // later column tiles see more keys: they go first
   const long long u = (long long)(gridDim.x - 1 - blockIdx.x) * kWholeWarps + warp;
   int b = -1;
@@ -806,16 +933,22 @@ __global__ void __launch_bounds__(kWholeWarps * 32) whole_kernel(const __grid_co
   if ((long long)it.ct * NC >= (long long)it.n * P.G) return;
   Walk<D, I8, NT, QS, PS> walk(P, lane);
   walk.sq = sq;
-  const float top = I8 ? q_top<D, NT>(P, it, lane, 32) : 0.f;
-  walk.qf = stage_q<D, I8, NT, QS>(P, it, sq, lane, 32, top);
-  set_limits(P, it, walk, NT);
-  __syncwarp();
-  State<D, NT> S;
-  S.clear();
+  walk.len = it.len;
   // keys of the tile's last row
   const int last = min(it.n - 1, (it.ct * NC + NC - 1) / P.G);
   const int keys = it.len ? it.len - it.n + last + 1 : 0;
-  walk.run(S, it, 0, 1, (keys + kBlock - 1) / kBlock);
+  walk.begin(it, 0, 1, (keys + kBlock - 1) / kBlock);
+  stage_q<D, I8, NT, QS>(P, it, sq, sf[warp], 0, 1, lane);
+  set_limits<NT>(P, it, walk);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    walk.qf[j][0] = sf[warp][j * 8 + 2 * walk.t];
+    walk.qf[j][1] = sf[warp][j * 8 + 2 * walk.t + 1];
+  }
+  State<D, NT> S;
+  S.clear();
+  walk.run(S, it);
   const float un = o_unit<I8>(S.r);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -882,7 +1015,8 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, long long cap, bool exact)
   const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
   const long long items = ((long long)T * G / (8 * nt) + B) * Hkv;
   const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
-  const long long most = (long long)num_sms() * (nt == 1 && D <= 128 ? 2 : 1);
+  const long long most =
+      std::min((long long)kMaxPieces, (long long)num_sms() * (nt == 1 && D <= 128 ? 2 : 1));
   return {nt, (int)std::max(1LL, std::min(most, items * chunks))};
 }
 
