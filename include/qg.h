@@ -488,10 +488,10 @@ typedef struct qg_paged_kv {
  * int8 pages, for each block of 16 tokens that gets rows: let o be the first
  * such row's place in the block (0..15) and s_old the block's scale if
  * o > 0, else 0. The new scale is s = max(s_old, max|x| / 127) over the new
- * rows' values of that head. The rows before o are brought to it, code <-
- * rint(code * (s_old / s)) (half a step of s at most per change), and the
- * new rows get code = clamp(rint(x / s), -127, 127) (0 where s is 0). Rows
- * after the new ones stay as they are. A NaN or infinite value, or a NaN
+ * rows' values of that head (0 below 2^-126). The rows before o are brought
+ * to it, code <- rint(code * (s_old / s)) (half a step of s at most per
+ * change), and the new rows get code = clamp(rint(x / s), -127, 127), both in
+ * fp32 (all 0 where s is 0). Rows after the new ones stay as they are. A NaN or infinite value, or a NaN
  * s_old, makes s NaN, and with it every value of the block until a call
  * writes the block from its first row again.
  *

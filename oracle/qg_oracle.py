@@ -896,7 +896,7 @@ KV_BLOCK = 16
 def kv_block_append(codes, s_old, o, x):
     """Append rows ``x [n, D]`` (float64) at place ``o`` of an int8 block
     ``codes [16, D]`` with scale ``s_old``: (codes after, scale after). The
-    scale is max(s_old, max|x| / 127), without s_old when o = 0; rows before
+    scale is max(s_old, max|x| / 127), 0 below 2^-126, without s_old when o = 0; rows before
     o are requantised to it, rows after the new ones stay. Non-finite values
     or a NaN s_old give a NaN scale (codes of the written rows are then
     unspecified: 0 here)."""
@@ -908,6 +908,7 @@ def kv_block_append(codes, s_old, o, x):
         codes[:o + n] = 0
         return codes, math.nan
     s = max(s_old, float(np.abs(x).max(initial=0.0)) / 127.0)
+    s = s if s >= 2.0 ** -126 else 0.0
     if s > 0.0:
         codes[:o] = np.rint(codes[:o] * (s_old / s))
         codes[o:o + n] = np.clip(np.rint(x / s), -127, 127)

@@ -5,12 +5,13 @@
 // Append. A CTA owns one block of 16 tokens of one sequence, the unit that
 // shares a scale of an int8 page: whoever writes a row of it has to see all
 // its new rows (for their maximum) and may have to bring the block's earlier
-// rows to a larger scale. Its warps take (q, K or V; head) items: a lane
-// holds D/32 neighbouring values of each of the block's rows in registers,
-// so the norm's sum, the rotation's partner (D/2 away: another lane) and the
-// block's maximum are warp shuffles, and each value is read once and written
-// once. The (cos, sin) pairs of the block's tokens are formed once per CTA
-// in shared memory and serve all heads.
+// rows to a larger scale. Its warps take (q, K or V; head) items, one warp
+// for up to 8 new rows and two past that: a lane holds D/32 neighbouring
+// values of each row in registers, so the norm's sum, the rotation's partner
+// (D/2 away: another lane) and the block's maximum are warp shuffles, and
+// each value is read once and written once. The cosines and sines of the
+// block's tokens are formed once per CTA in shared memory and serve all
+// heads.
 //
 // The mapping of CTAs to (sequence, block) needs no host knowledge of the
 // lengths: n rows touch at most n/16 + 2 blocks, so slot ranges
@@ -133,56 +134,210 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int (&c)[EPL]) {
   for (int j = 0; j < EPL; ++j) c[j] = (int)(int8_t)(w[j >> 2] >> (8 * (j & 3)));
 }
 
+// EPL codes of values already divided by the scale: the sum with 1.5 * 2^23
+// rounds to the nearest integer, whose low byte is the code.
 template <int EPL>
-__device__ __forceinline__ void store_codes(uint8_t* p, const int (&c)[EPL]) {
-  uint32_t w[2] = {0, 0};
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[EPL]) {
+  uint32_t c[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) w[j >> 2] |= (uint32_t)(uint8_t)c[j] << (8 * (j & 3));
-  if constexpr (EPL == 2)
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
-  else if constexpr (EPL == 4)
-    *reinterpret_cast<uint32_t*>(p) = w[0];
-  else
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  for (int j = 0; j < EPL; ++j)
+    c[j] = __float_as_uint(fminf(fmaxf(x[j], -127.f), 127.f) + 12582912.f);
+  if constexpr (EPL == 2) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)__byte_perm(c[0], c[1], 0x40);
+  } else {
+    uint32_t w[EPL / 4];
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4)
+      w[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x40), __byte_perm(c[j + 2], c[j + 3], 0x40),
+                             0x5410);
+    if constexpr (EPL == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
 }
 
-// RMSNorm of one head's row across the warp (as qg_rmsnorm_perhead).
-template <int D>
-__device__ __forceinline__ void norm_row(float (&x)[D / 32], const float (&w)[D / 32], float eps) {
+// EPL consecutive floats of shared memory.
+template <int EPL>
+__device__ __forceinline__ void lds(const float* p, float (&x)[EPL]) {
+  if constexpr (EPL == 2) {
+    const float2 t = *reinterpret_cast<const float2*>(p);
+    x[0] = t.x;
+    x[1] = t.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p + j);
+      x[j] = t.x;
+      x[j + 1] = t.y;
+      x[j + 2] = t.z;
+      x[j + 3] = t.w;
+    }
+  }
+}
+
+// RMSNorm of NR rows of one head across the warp (as qg_rmsnorm_perhead),
+// the rows' sums side by side.
+template <int D, int NR>
+__device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const uint16_t* w, float eps,
+                                          int lane) {
   constexpr int EPL = D / 32;
-  float ss = 0.f;
+  float nw[EPL], ss[NR];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) ss = fmaf(x[j], x[j], ss);
-  const float inv = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
+  for (int j = 0; j < EPL; ++j) nw[j] = bf16_bits_to_f32(__ldcg(w + lane * EPL + j));
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) x[j] = x[j] * inv * w[j];
+  for (int r = 0; r < NR; ++r) {
+    ss[r] = 0.f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) ss[r] = fmaf(x[r][j], x[r][j], ss[r]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], o);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const float inv = 1.0f / sqrtf(ss[r] / (float)D + eps);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[r][j] = x[r][j] * inv * nw[j];
+  }
 }
 
-// Rotation of one head's row: dim d < half pairs with d + half, which the
-// lane `half / EPL` further holds at the same place (half is a multiple of
-// EPL). cs: the row's (cos, sin).
-template <int D>
-__device__ __forceinline__ void rotate_row(float (&x)[D / 32], const float2* cs, int half,
-                                           int lane) {
+// Rotation of NR rows of one head: dim d < half pairs with d + half, which
+// the lane `half / EPL` further holds at the same place (half is a multiple
+// of EPL). cs, sn: the rows' cosines and sines, `half` a row.
+template <int D, int NR>
+__device__ __forceinline__ void rotate_rows(float (&x)[NR][D / 32], const float* cs,
+                                            const float* sn, int half, int lane) {
   constexpr int EPL = D / 32;
   const int hl = half / EPL;  // lanes per half
   const bool lo = lane < hl, hi = !lo && lane < 2 * hl;
   const int src = lo ? lane + hl : hi ? lane - hl : lane;
   const int i0 = (lo ? lane : hi ? lane - hl : 0) * EPL;
+  const float sign = lo ? -1.f : 1.f;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const float other = __shfl_sync(0xffffffffu, x[j], src);
-    if (lo || hi) {
-      const float2 t = cs[i0 + j];
-      x[j] = lo ? x[j] * t.x - other * t.y : x[j] * t.x + other * t.y;
+  for (int r = 0; r < NR; ++r) {
+    float c[EPL], s[EPL];
+    lds<EPL>(cs + r * half + i0, c);
+    lds<EPL>(sn + r * half + i0, s);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const float t = __shfl_sync(0xffffffffu, x[r][j], src) * s[j];
+      const float y = fmaf(sign, t, x[r][j] * c[j]);
+      if (lo || hi) x[r][j] = y;
+    }
+  }
+}
+
+// Where a warp's rows of one head go.
+struct Task {
+  const uint8_t* src;     // the lane's values of the first row
+  long long ld;           // bytes between rows
+  const uint16_t* norm;   // or null
+  const float* cs;        // null: no rotation
+  const float* sn;
+  int rows;               // 1 .. NR
+};
+
+template <int D, bool XF32, int NR>
+__device__ __forceinline__ void take_rows(const Task& t, float (&x)[NR][D / 32], float eps,
+                                          int half, int lane) {
+  constexpr int EPL = D / 32;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[r][j] = 0.f;
+    if (r < t.rows) load_vals<EPL, XF32>(t.src + r * t.ld, x[r]);
+  }
+  if (t.norm) norm_rows<D, NR>(x, t.norm, eps, lane);
+  if (t.cs) rotate_rows<D, NR>(x, t.cs, t.sn, half, lane);
+}
+
+template <int D, bool XF32, int NR>
+__device__ __forceinline__ void query_task(const AppendParams& P, const Task& t, long long at,
+                                           int lane) {
+  float x[NR][D / 32];
+  take_rows<D, XF32, NR>(t, x, P.eps, P.half, lane);
+  __syncwarp();  // q_out may be q: every lane has its values
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    if (r >= t.rows) break;
+    if (P.q_bf16)
+      store_bf16<D / 32>(reinterpret_cast<uint16_t*>(P.qo) + at + (long long)r * P.H * D, x[r]);
+    else
+      store_f32<D / 32>(reinterpret_cast<float*>(P.qo) + at + (long long)r * P.H * D, x[r]);
+  }
+}
+
+// K or V rows of one head into a page. int8: `o` rows of the block lie before
+// the block's new ones; `pair`: another warp has the block's other new rows
+// (the block's maximum meets in smax, barrier `bar`).
+template <int D, bool I8, bool XF32, int NR>
+__device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t, uint8_t* block,
+                                           int first, float* scale, int o, bool pair, int half,
+                                           float* smax, int bar, int lane) {
+  constexpr int EPL = D / 32;
+  float x[NR][EPL];
+  take_rows<D, XF32, NR>(t, x, P.eps, P.half, lane);
+  if constexpr (!I8) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (r >= t.rows) break;
+      store_bf16<EPL>(reinterpret_cast<uint16_t*>(block) + (first + r) * D, x[r]);
+    }
+  } else {
+    const float s_old = o > 0 ? __ldcg(scale) : 0.f;
+    float top = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const float a = r < t.rows ? fabsf(x[r][j]) : 0.f;
+        top = a <= FLT_MAX ? fmaxf(top, a) : INFINITY;  // (a NaN too; it stays)
+      }
+    top = warp_max(top);
+    if (pair) {
+      if (lane == 0) smax[half] = top;
+      asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+      top = fmaxf(smax[0], smax[1]);
+      asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // smax is used again
+    }
+    float s = fmaxf(s_old, top / 127.0f);
+    if (!(top <= FLT_MAX) || s_old != s_old) s = __int_as_float(0x7FC00000);
+    if (s < FLT_MIN) s = 0.f;
+    const float inv = s > 0.f ? 1.f / s : 0.f;  // (false for a NaN scale)
+    if (half == 0 && o > 0 && s != s_old) {  // the block's earlier rows to the new scale
+      const float ratio = s > 0.f ? s_old / s : 0.f;
+      for (int r = 0; r < o; ++r) {
+        int c[EPL];
+        load_codes<EPL>(block + r * D + lane * EPL, c);
+        float y[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) y[j] = (float)c[j] * ratio;
+        store_codes<EPL>(block + r * D + lane * EPL, y);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (r >= t.rows) break;
+      float y[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) y[j] = inv > 0.f ? x[r][j] * inv : 0.f;
+      store_codes<EPL>(block + (first + r) * D + lane * EPL, y);
+    }
+    if (half == 0) {
+      __syncwarp();  // every lane has read s_old
+      if (lane == 0) *scale = s;
     }
   }
 }
 
 template <int D, bool I8, bool XF32>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendParams P) {
-  constexpr int EPL = D / 32;
-  __shared__ float2 cs[kBlock * D / 2];
+  constexpr int EPL = D / 32, XB = XF32 ? 4 : 2, NR = 8;
+  __shared__ __align__(16) float cs[kBlock * D / 2];
+  __shared__ __align__(16) float sn[kBlock * D / 2];
+  __shared__ float smax[kWarps];
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
@@ -214,119 +369,53 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
   const int page = __ldcg(P.table + (long long)b * P.max_pages + first / P.page_size);
   const bool in_pool = page >= 0 && page < P.num_pages;
 
-  // (cos, sin) of the new rows: the angle pos * theta^(-2i/rd) in units of
-  // pi and its reduction to [-1, 1] in float64 (positions in the millions
+  // cosines and sines of the new rows: the angle pos * theta^(-2i/rd) in units
+  // of pi and its reduction to [-1, 1] in float64 (positions in the millions
   // keep the full fp32 accuracy), sincospi in fp32: within 2^-22 of the
   // exact values, at a fraction of the cost of a float64 sincos.
   for (int i = tid; i < nr * P.half; i += kWarps * 32) {
-    const int r = i / P.half, f = i % P.half;
+    const int r = i / P.half, f = i - r * P.half;
     const double t = (double)(lo + r) * P.turns[f];
-    float sn, cn;
-    sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn, &cn);
-    cs[i] = make_float2(cn, sn);
+    sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn[i], &cs[i]);
   }
   __syncthreads();
 
-  constexpr int XB = XF32 ? 4 : 2;
-  const int items = 2 * P.Hkv + P.H;
-  for (int it = blockIdx.y * kWarps + warp; it < items; it += gridDim.y * kWarps) {
+  // A warp has up to 8 rows of a head; past 8 new rows two neighbouring
+  // warps share the head's block.
+  const bool pair = nr > NR;
+  const int half = pair ? warp & 1 : 0, base = half * NR;
+  const int items = 2 * P.Hkv + P.H, step = pair ? kWarps / 2 : kWarps;
+  for (int it = blockIdx.y * step + (pair ? warp >> 1 : warp); it < items; it += gridDim.y * step) {
     const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
     const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
-    const uint16_t* wp = isk ? P.kn : isv ? nullptr : P.qn;
-    float nw[EPL];  // the norm weights of the lane's values
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) nw[j] = wp ? bf16_bits_to_f32(__ldcg(wp + lane * EPL + j)) : 1.f;
-    if (!isk && !isv) {  // a query head
-      const uint8_t* src = P.q + (row * P.q_ld + h * D + lane * EPL) * XB;
-      for (int r = 0; r < nr; r += 4) {
-        float x[4][EPL];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r + e < nr) load_vals<EPL, XF32>(src + (r + e) * P.q_ld * XB, x[e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (r + e >= nr) break;
-          if (P.qn) norm_row<D>(x[e], nw, P.eps);
-          if (P.half) rotate_row<D>(x[e], cs + (r + e) * P.half, P.half, lane);
-          __syncwarp();  // q_out may be q: every lane has its values
-          const long long at = (row + r + e) * P.H * D + h * D + lane * EPL;
-          if (P.q_bf16)
-            store_bf16<EPL>(reinterpret_cast<uint16_t*>(P.qo) + at, x[e]);
-          else
-            store_f32<EPL>(reinterpret_cast<float*>(P.qo) + at, x[e]);
-        }
-      }
+    const long long ld = isk ? P.k_ld : isv ? P.v_ld : P.q_ld;
+    Task t;
+    t.src = (isk ? P.k : isv ? P.v : P.q) + ((row + base) * ld + h * D + lane * EPL) * XB;
+    t.ld = ld * XB;
+    t.norm = isk ? P.kn : isv ? nullptr : P.qn;
+    t.cs = isv || !P.half ? nullptr : cs + base * P.half;
+    t.sn = sn + base * P.half;
+    t.rows = min(NR, nr - base);
+    if (!isk && !isv) {
+      const long long at = (row + base) * P.H * D + h * D + lane * EPL;
+      if (nr == 1)
+        query_task<D, XF32, 1>(P, t, at, lane);
+      else
+        query_task<D, XF32, NR>(P, t, at, lane);
       continue;
     }
     if (!in_pool) continue;
-    const uint8_t* src = isk ? P.k + (row * P.k_ld + h * D + lane * EPL) * XB
-                             : P.v + (row * P.v_ld + h * D + lane * EPL) * XB;
-    const long long ld = (isk ? P.k_ld : P.v_ld) * XB;
-    // the block's first row in the pool
-    const long long at =
-        (((long long)page * P.Hkv + h) * P.page_size + first % P.page_size) * D + lane * EPL;
-    uint8_t* dst = (isk ? P.kp : P.vp) + at * (I8 ? 1 : 2);
-    if constexpr (!I8) {
-      for (int r = 0; r < nr; r += 4) {
-        float x[4][EPL];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r + e < nr) load_vals<EPL, XF32>(src + (r + e) * ld, x[e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (r + e >= nr) break;
-          if (isk && P.kn) norm_row<D>(x[e], nw, P.eps);
-          if (isk && P.half) rotate_row<D>(x[e], cs + (r + e) * P.half, P.half, lane);
-          store_bf16<EPL>(reinterpret_cast<uint16_t*>(dst) + (o + r + e) * D, x[e]);
-        }
-      }
-    } else {
-      float* sp = (isk ? P.ks : P.vs) + ((long long)page * P.Hkv + h) * (P.page_size / kBlock) +
-                  (first % P.page_size) / kBlock;
-      const float s_old = o > 0 ? __ldcg(sp) : 0.f;
-      float x[kBlock][EPL];
-#pragma unroll
-      for (int r = 0; r < kBlock; ++r)
-        if (r < nr) load_vals<EPL, XF32>(src + r * ld, x[r]);
-      float top = 0.f;
-      bool bad = s_old != s_old;
-#pragma unroll
-      for (int r = 0; r < kBlock; ++r) {
-        if (r >= nr) break;
-        if (isk && P.kn) norm_row<D>(x[r], nw, P.eps);
-        if (isk && P.half) rotate_row<D>(x[r], cs + r * P.half, P.half, lane);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          top = fmaxf(top, fabsf(x[r][j]));
-          bad |= !(fabsf(x[r][j]) <= FLT_MAX);
-        }
-      }
-      const bool nan = __any_sync(0xffffffffu, bad);
-      const float s = nan ? __int_as_float(0x7FC00000) : fmaxf(s_old, warp_max(top) / 127.0f);
-      if (o > 0 && s != s_old) {  // the block's earlier rows to the new scale
-        const float ratio = s_old / s;
-        for (int r = 0; r < o; ++r) {
-          int c[EPL];
-          load_codes<EPL>(dst + r * D, c);
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) c[j] = __float2int_rn((float)c[j] * ratio);
-          store_codes<EPL>(dst + r * D, c);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kBlock; ++r) {
-        if (r >= nr) break;
-        int c[EPL];
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          const float t = s > 0.f ? x[r][j] / s : 0.f;  // (false for a NaN scale)
-          c[j] = min(127, max(-127, __float2int_rn(t)));
-        }
-        store_codes<EPL>(dst + (o + r) * D, c);
-      }
-      __syncwarp();  // every lane has read s_old
-      if (lane == 0) *sp = s;
-    }
+    const long long hp = (long long)page * P.Hkv + h;
+    const int in_page = first % P.page_size;
+    uint8_t* block = (isk ? P.kp : P.vp) + (hp * P.page_size + in_page) * D * (I8 ? 1 : 2) +
+                     (I8 ? 0 : lane * EPL * 2);
+    float* scale =
+        I8 ? (isk ? P.ks : P.vs) + hp * (P.page_size / kBlock) + in_page / kBlock : nullptr;
+    if (nr == 1)
+      cache_task<D, I8, XF32, 1>(P, t, block, o, scale, o, false, 0, nullptr, 0, lane);
+    else
+      cache_task<D, I8, XF32, NR>(P, t, block, o + base, scale, o, pair, half,
+                                  smax + (warp & ~1), 1 + (warp >> 1), lane);
   }
 }
 
@@ -504,10 +593,10 @@ extern "C" qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* pa
   for (int i = 0; i < P.half; ++i)
     P.turns[i] = pow(theta, -2.0 * i / rotary_dim) / 3.14159265358979323846;
   const int slots = row_start ? T / pk::kBlock + 2 * B : B;
-  // heads spread over CTAs until the grid fills the GPU twice or each warp
-  // has one item
+  // heads spread over CTAs until the grid fills the GPU four times (CTAs that
+  // resident SMs hold) or each warp has one item
   const int most = (2 * Hkv + H + pk::kWarps - 1) / pk::kWarps;
-  const int ny = std::max(1, std::min(most, 2 * num_sms() / std::max(slots, 1)));
+  const int ny = std::max(1, std::min(most, 4 * num_sms() / std::max(slots, 1)));
   const dim3 grid(slots, ny);
   const bool i8 = kv->dtype == QG_KV_INT8, xf32 = x_dtype == QG_F32;
   cudaStream_t st = (cudaStream_t)stream;
