@@ -134,14 +134,15 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int (&c)[EPL]) {
   for (int j = 0; j < EPL; ++j) c[j] = (int)(int8_t)(w[j >> 2] >> (8 * (j & 3)));
 }
 
-// EPL codes of values already divided by the scale: the sum with 1.5 * 2^23
-// rounds to the nearest integer, whose low byte is the code.
+// EPL codes x * f: the sum with 1.5 * 2^23 rounds the product to the nearest
+// integer, whose low byte is the code. |x * f| is at most 127 but for
+// roundings (f = 1 / scale, and the scale is a normal number), so nothing is
+// clamped; f = 0 gives 0 (and any code under a NaN scale).
 template <int EPL>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[EPL]) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[EPL], float f) {
   uint32_t c[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    c[j] = __float_as_uint(fminf(fmaxf(x[j], -127.f), 127.f) + 12582912.f);
+  for (int j = 0; j < EPL; ++j) c[j] = __float_as_uint(fmaf(x[j], f, 12582912.f));
   if constexpr (EPL == 2) {
     *reinterpret_cast<uint16_t*>(p) = (uint16_t)__byte_perm(c[0], c[1], 0x40);
   } else {
@@ -176,8 +177,10 @@ __device__ __forceinline__ void lds(const float* p, float (&x)[EPL]) {
   }
 }
 
-// RMSNorm of NR rows of one head across the warp (as qg_rmsnorm_perhead),
-// the rows' sums side by side.
+// RMSNorm of NR rows of one head across the warp (as qg_rmsnorm_perhead).
+// For 8 rows the sums are scattered while they are reduced: after three
+// exchanges a lane holds one row's (row lane / 4), so that its root and
+// reciprocal are formed once, not on every lane, and 9 shuffles replace 40.
 template <int D, int NR>
 __device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const uint16_t* w, float eps,
                                           int lane) {
@@ -192,14 +195,22 @@ __device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const uint16_t
     for (int j = 0; j < EPL; ++j) ss[r] = fmaf(x[r][j], x[r][j], ss[r]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int n = NR / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) ss[r] += __shfl_xor_sync(0xffffffffu, ss[r], o);
+    for (int r = 0; r < n; ++r) {
+      const float mine = up ? ss[n + r] : ss[r], other = up ? ss[r] : ss[n + r];
+      ss[r] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+#pragma unroll
+  for (int o = 16 / NR; o > 0; o >>= 1) ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
+  const float inv = 1.0f / sqrtf(ss[0] / (float)D + eps);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-    const float inv = 1.0f / sqrtf(ss[r] / (float)D + eps);
+    const float f = __shfl_sync(0xffffffffu, inv, r * (32 / NR));
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) x[r][j] = x[r][j] * inv * nw[j];
+    for (int j = 0; j < EPL; ++j) x[r][j] = x[r][j] * f * nw[j];
   }
 }
 
@@ -275,7 +286,7 @@ __device__ __forceinline__ void query_task(const AppendParams& P, const Task& t,
 template <int D, bool I8, bool XF32, int NR>
 __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t, uint8_t* block,
                                            int first, float* scale, int o, bool pair, int half,
-                                           float* smax, int bar, int lane) {
+                                           unsigned* smax, int bar, int lane) {
   constexpr int EPL = D / 32;
   float x[NR][EPL];
   take_rows<D, XF32, NR>(t, x, P.eps, P.half, lane);
@@ -287,23 +298,24 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
     }
   } else {
     const float s_old = o > 0 ? __ldcg(scale) : 0.f;
-    float top = 0.f;
+    // the largest |x| by its bits, where infinities and NaN stand above all
+    unsigned top = 0;
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+    for (int r = 0; r < NR; ++r) {
+      unsigned m = 0;
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const float a = r < t.rows ? fabsf(x[r][j]) : 0.f;
-        top = a <= FLT_MAX ? fmaxf(top, a) : INFINITY;  // (a NaN too; it stays)
-      }
-    top = warp_max(top);
+      for (int j = 0; j < EPL; ++j) m = max(m, __float_as_uint(x[r][j]) & 0x7FFFFFFFu);
+      top = max(top, r < t.rows ? m : 0u);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
     if (pair) {
       if (lane == 0) smax[half] = top;
       asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-      top = fmaxf(smax[0], smax[1]);
+      top = max(smax[0], smax[1]);
       asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // smax is used again
     }
-    float s = fmaxf(s_old, top / 127.0f);
-    if (!(top <= FLT_MAX) || s_old != s_old) s = __int_as_float(0x7FC00000);
+    float s = fmaxf(s_old, __uint_as_float(top) / 127.0f);
+    if (top >= 0x7F800000u || s_old != s_old) s = __int_as_float(0x7FC00000);
     if (s < FLT_MIN) s = 0.f;
     const float inv = s > 0.f ? 1.f / s : 0.f;  // (false for a NaN scale)
     if (half == 0 && o > 0 && s != s_old) {  // the block's earlier rows to the new scale
@@ -313,17 +325,14 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
         load_codes<EPL>(block + r * D + lane * EPL, c);
         float y[EPL];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) y[j] = (float)c[j] * ratio;
-        store_codes<EPL>(block + r * D + lane * EPL, y);
+        for (int j = 0; j < EPL; ++j) y[j] = (float)c[j];
+        store_codes<EPL>(block + r * D + lane * EPL, y, ratio);
       }
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       if (r >= t.rows) break;
-      float y[EPL];
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) y[j] = inv > 0.f ? x[r][j] * inv : 0.f;
-      store_codes<EPL>(block + (first + r) * D + lane * EPL, y);
+      store_codes<EPL>(block + (first + r) * D + lane * EPL, x[r], inv);
     }
     if (half == 0) {
       __syncwarp();  // every lane has read s_old
@@ -333,11 +342,12 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
 }
 
 template <int D, bool I8, bool XF32>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2)
+append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int EPL = D / 32, XB = XF32 ? 4 : 2, NR = 8;
   __shared__ __align__(16) float cs[kBlock * D / 2];
   __shared__ __align__(16) float sn[kBlock * D / 2];
-  __shared__ float smax[kWarps];
+  __shared__ unsigned smax[kWarps];
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
@@ -433,61 +443,85 @@ struct GatherParams {
   int B, T, Hkv, page_size, max_pages, num_pages;
 };
 
-// One warp per (row, head), K and V.
+// A CTA reads kGatherRows rows; a thread takes 8 neighbouring values of K or
+// V, the same place in each row, so that its loads are independent.
+constexpr int kGatherRows = 4;
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams P) {
-  constexpr int EPL = D / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ int s_page[kGatherRows], s_off[kGatherRows];  // page -1: NaN, -2: no row
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int row = (int)(w / P.Hkv), h = (int)(w % P.Hkv);
-  if (row >= P.T) return;
-  int b = row;
-  if (P.row_start) {  // the last sequence that starts at or before the row and holds it
-    b = -1;
-    for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < P.B && row_begin(P.row_start, i, P.T) <= row &&
-                      row < row_begin(P.row_start, i + 1, P.T);
-      const unsigned m = __ballot_sync(0xffffffffu, in);
-      if (m) b = i0 + __ffs(m) - 1;
-    }
-    if (b < 0) return;
-  }
-  const long long t =
-      (long long)(P.first ? __ldcg(P.first + b) : 0) + (row - row_begin(P.row_start, b, P.T));
-  int page = -1;
-  if (t >= 0 && t < (long long)P.max_pages * P.page_size)
-    page = __ldcg(P.table + (long long)b * P.max_pages + t / P.page_size);
-  const bool ok = page >= 0 && page < P.num_pages;
-  const int off = ok ? (int)(t % P.page_size) : 0;
-  const long long at = (((long long)(ok ? page : 0) * P.Hkv + h) * P.page_size + off) * D + lane * EPL;
-  const long long sat =
-      ((long long)(ok ? page : 0) * P.Hkv + h) * (P.page_size / kBlock) + off / kBlock;
-  const long long to = ((long long)row * P.Hkv + h) * D + lane * EPL;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    void* out = which ? P.vo : P.ko;
-    if (!out) continue;
-    const uint8_t* pages = which ? P.vp : P.kp;
-    float x[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) x[j] = __int_as_float(0x7FC00000);
-    if (ok) {
-      if constexpr (I8) {
-        int c[EPL];
-        load_codes<EPL>(pages + at, c);
-        const float s = __ldcg((which ? P.vs : P.ks) + sat);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) x[j] = (float)c[j] * s;
-      } else {
-        load_vals<EPL, false>(pages + at * 2, x);
+  const int row0 = blockIdx.x * kGatherRows;
+  if (warp < kGatherRows) {  // a warp finds a row's sequence and page
+    const int row = row0 + warp;
+    int b = row < P.T ? row : -1;
+    if (P.row_start) {
+      b = -1;
+      for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < P.B && row < P.T && row_begin(P.row_start, i, P.T) <= row &&
+                        row < row_begin(P.row_start, i + 1, P.T);
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m) b = i0 + __ffs(m) - 1;
       }
     }
-    if (P.out_bf16)
-      store_bf16<EPL>(reinterpret_cast<uint16_t*>(out) + to, x);
-    else
-      store_f32<EPL>(reinterpret_cast<float*>(out) + to, x);
+    if (lane == 0) {
+      int page = -2, off = 0;
+      if (b >= 0) {
+        const long long t =
+            (long long)(P.first ? __ldcg(P.first + b) : 0) + (row - row_begin(P.row_start, b, P.T));
+        page = -1;
+        if (t >= 0 && t < (long long)P.max_pages * P.page_size) {
+          const int pi = (int)t / P.page_size;
+          off = (int)t - pi * P.page_size;
+          page = __ldcg(P.table + (long long)b * P.max_pages + pi);
+          if (page < 0 || page >= P.num_pages) page = -1;
+        }
+      }
+      s_page[warp] = page;
+      s_off[warp] = off;
+    }
+  }
+  __syncthreads();
+  const int half = P.Hkv * (D / 8);  // places per row of K, then as many of V
+  for (int i = tid; i < 2 * half; i += kWarps * 32) {
+    const bool isv = i >= half;
+    const int at = isv ? i - half : i, h = at / (D / 8), d = at % (D / 8) * 8;
+    void* out = isv ? P.vo : P.ko;
+    if (!out) continue;
+    const uint8_t* pages = isv ? P.vp : P.kp;
+    const float* scales = isv ? P.vs : P.ks;
+    float x[kGatherRows][8];
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+      const int page = s_page[r];
+      if (page < 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[r][j] = __int_as_float(0x7FC00000);
+        continue;
+      }
+      const long long hp = (long long)page * P.Hkv + h;
+      const long long from = (hp * P.page_size + s_off[r]) * D + d;
+      if constexpr (I8) {
+        int c[8];
+        load_codes<8>(pages + from, c);
+        const float s = __ldcg(scales + hp * (P.page_size / kBlock) + s_off[r] / kBlock);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[r][j] = (float)c[j] * s;
+      } else {
+        load_vals<8, false>(pages + from * 2, x[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+      if (s_page[r] == -2) continue;
+      const long long to = ((long long)(row0 + r) * P.Hkv + h) * D + d;
+      if (P.out_bf16)
+        store_bf16<8>(reinterpret_cast<uint16_t*>(out) + to, x[r]);
+      else
+        store_f32<8>(reinterpret_cast<float*>(out) + to, x[r]);
+    }
   }
 }
 
@@ -618,8 +652,6 @@ extern "C" qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* pa
   if (qg_status s = pk::check_pool(who, kv, max_pages)) return s;
   QG_REQUIRE(B >= 0 && T >= 0 && B <= (1 << 24) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE,
              "%s: B=%d T=%d", who, B, T);
-  QG_REQUIRE((long long)T * kv->kv_heads < (1LL << 33), QG_ERR_UNSUPPORTED_SHAPE,
-             "%s: T=%d x kv_heads=%d too large", who, T, kv->kv_heads);
   QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
              "%s: T=%d rows without row_start must be B=%d", who, T, B);
   QG_REQUIRE(out_dtype == QG_F32 || out_dtype == QG_BF16, QG_ERR_INVALID_ARGUMENT,
@@ -648,8 +680,7 @@ extern "C" qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* pa
   P.page_size = kv->page_size;
   P.max_pages = max_pages;
   P.num_pages = kv->num_pages;
-  const long long warps = (long long)T * kv->kv_heads;
-  const dim3 grid((unsigned)((warps + pk::kWarps - 1) / pk::kWarps));
+  const dim3 grid((unsigned)((T + pk::kGatherRows - 1) / pk::kGatherRows));
   const bool i8 = kv->dtype == QG_KV_INT8;
   cudaStream_t st = (cudaStream_t)stream;
   if (kv->head_dim == 64)
