@@ -6,9 +6,10 @@
 // (equal values by index), and the draw is the place in that prefix where
 // the running weight reaches u times the prefix's weight. So everything is
 // one operation: find the candidate at which a running count, or a running
-// weight, reaches a target. A histogram of (count, weight) over 1024 bins
-// that are monotone in the value answers it up to one bin; the bin's members
-// (a handful) are then collected and ranked against each other.
+// weight, reaches a target. A histogram of (count, weight) over 2048 bins
+// that are monotone in the value answers it up to one bin; the members of the
+// few bins that can matter are collected in one more pass and sorted. With a small top-k only counts go into the histogram, and weights
+// are formed for the members of the first bins alone.
 //
 // A row belongs to a cluster of CTAs, each holding a slice of it in shared
 // memory: the row is read from HBM once, and the cluster's histograms and
@@ -21,6 +22,7 @@
 // borders by 2^-24 of the total, more than a rare token's whole weight.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <cstddef>
 
 #include "qg_internal.cuh"
@@ -28,12 +30,13 @@
 namespace qg {
 namespace sf {
 
+constexpr int kBins = 2048;
+constexpr int kFine = 1536;         // bins for the values whose weight is not 0
 constexpr int kThreads = 512;
-constexpr int kBins = 1024;
-constexpr int kFine = 768;          // bins for the values whose weight is not 0
-constexpr int kList = 1024;         // members of a bin that rank 0 ranks directly
+constexpr int kList = kThreads;     // members that rank 0 can hold, one a thread
 constexpr int kMaxCluster = 16;
-constexpr int kResident = 38016;    // values of a slice that shared memory holds
+constexpr int kResident = 37984;    // values of a slice that shared memory holds
+constexpr int kSteps = 64;          // entries of the table of 2^(i / kSteps)
 
 typedef unsigned long long u64;
 
@@ -49,31 +52,54 @@ struct Params {
   int32_t* kept;
   float* logprob;
   int V, slice, resident, frac;  // frac: fraction bits of a fixed-point weight
+  double pow2[kSteps];
 };
 
-enum Op { kDone, kCollect, kMinMax, kHist };
+enum Op { kDone, kCollect, kMinMax, kHist, kWeights };
 struct Cmd {
   int op, bin, shift;
   u64 lo, hi;
+};
+
+// A place in the descending order: candidates before it, running weight with
+// it, its key; or, for a bin: what lies before it, and what it holds.
+struct Found {
+  u64 rank, cum, key;
+};
+struct Bin {
+  int at;
+  u64 pc, pw, c, w;
 };
 
 struct Shared {
   u64 key_max[kMaxCluster], key_min[kMaxCluster];  // pushed by every rank
   unsigned count[kMaxCluster], above[kMaxCluster]; // candidates; weights >= min_p
   Cmd cmd;
+  unsigned wanted[kBins / 32];  // bins to collect
   unsigned list_n;
-  u64 red[kThreads / 32], red2[kThreads / 32];
-  unsigned red3[kThreads / 32];
-  // a search's answer (rank 0)
-  int s_bin;
-  u64 a_rank, a_cum, a_key;
-  u64 list_key[kList];
-  u64 list_w[kList];
-  u64 hist_w[kBins];      // this CTA's
-  u64 tot_w[kBins], sub_w[kBins];        // the cluster's (rank 0): row, and inside a bin
-  u64 tot_pw[kBins], sub_pw[kBins];      // exclusive prefixes
-  unsigned hist_c[kBins], tot_c[kBins], sub_c[kBins], tot_pc[kBins], sub_pc[kBins];
+  u64 red[32], red2[32];
+  unsigned red3[32];
+  double pow2[kSteps];
+  u64 mine[kList];                       // this CTA's members of a collection
+  unsigned mine_n;
+  int path;                              // rank 0: how the row goes on
+  u64 list_key[kList], list_w[kList];    // rank 0's list: sorted keys, running weights
+  // rank 0: the cluster's counts and weights by bin, and what lies before
+  // each group of 32 bins (the whole at the end)
+  u64 tot_w[kBins], sup_w[kBins / 32 + 1];
+  unsigned tot_c[kBins], sup_c[kBins / 32 + 1];
+  // this CTA's histogram: counts; weights in two halves, since a 64-bit
+  // shared-memory atomic costs several 32-bit ones
+  unsigned hist_c[kBins];
+  uint2 hist_w[kBins];
 };
+// Inside one bin (rank 0, rare): lies over the list.
+constexpr int kSubBins = 512;
+struct Sub {
+  u64 w[kSubBins];
+  unsigned c[kSubBins];
+};
+static_assert(sizeof(Sub) <= 2 * kList * sizeof(u64), "Sub lies over list_key and list_w");
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
@@ -84,11 +110,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t remote(const void* p, unsigned rank) {
-  const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+__device__ __forceinline__ uint32_t remote_at(uint32_t local, unsigned rank) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
   return r;
+}
+__device__ __forceinline__ uint32_t remote(const void* p, unsigned rank) {
+  return remote_at(static_cast<uint32_t>(__cvta_generic_to_shared(p)), rank);
 }
 __device__ __forceinline__ void st_u64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
@@ -98,12 +126,12 @@ __device__ __forceinline__ void st_u32(uint32_t a, unsigned v) {
 }
 __device__ __forceinline__ u64 ld_u64(uint32_t a) {
   u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ unsigned ld_u32(uint32_t a) {
   unsigned v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ unsigned add_u32(uint32_t a, unsigned v) {
@@ -137,189 +165,403 @@ __device__ __forceinline__ u64 warp_min64(u64 v) {
   return v;
 }
 
+__device__ __forceinline__ void add_weight(uint2* at, u64 w) {
+  const unsigned lo = (unsigned)w, old = atomicAdd(&at->x, lo);
+  const unsigned hi = (unsigned)(w >> 32) + (old + lo < old);
+  if (hi) atomicAdd(&at->y, hi);
+}
+
 // The row's bins and weights.
 struct Row {
   float top;       // the largest value
   double inv_t;    // 1 / temperature
-  double unit;     // 2^frac
-  double floor_;   // (l - max) / T below this has weight 0
+  int frac;        // fraction bits of a weight
+  double least;    // (l - max) / T below this has weight 0
   float fine, coarse, edge;  // bins: d * fine up to d = edge, then (d - edge) * coarse
+  const double* pow2;
 
+  __device__ __forceinline__ double exponent(float v) const {
+    return v == top ? 0.0 : ((double)v - (double)top) * inv_t;  // (0 for +inf too)
+  }
+  // exp(x) for least <= x <= 0, times 2^up: table-driven (Tang, "Table-driven
+  // implementation of the exponential function", 1989) with 64 steps an
+  // octave: x = (64 k + i) ln2/64 + r, |r| <= ln2/128, and a polynomial of
+  // degree 5 in r (next term r^6/720 < 2^-54).
+  __device__ __forceinline__ double power(double x, int up) const {
+    const double magic = 6755399441055744.0;  // 1.5 * 2^52: the sum rounds to an integer
+    const double t = fma(x, 92.33248261689366, magic);  // 64 / ln 2
+    const int k = __double2loint(t);
+    const double n = t - magic;
+    double r = fma(n, -0.010830424696249145, x);            // ln2 / 64, rounded
+    r = fma(n, -3.623510646634843e-19, r);                  // what the rounding left
+    double p = fma(r, 1.0 / 120.0, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0) * r;
+    const double s = pow2[k & (kSteps - 1)];
+    const double y = fma(s, p, s);
+    return __hiloint2double(__double2hiint(y) + (((k >> 6) + up) << 20), __double2loint(y));
+  }
   __device__ __forceinline__ double weight(float v) const {
-    if (v == top) return 1.0;  // (also +inf; below it everything is then 0)
-    const double x = ((double)v - (double)top) * inv_t;
-    return x > -INFINITY ? exp(x) : 0.0;
+    const double x = exponent(v);
+    return x >= least ? power(x, 0) : 0.0;
+  }
+  // power(x, frac) and the weight in units of 2^-frac, 0 where it rounds to
+  // less: the sum with 2^52 rounds it.
+  __device__ __forceinline__ u64 fixed_of(double x, double* y) const {
+    const bool in = x >= least;
+    *y = power(in ? x : 0.0, frac);
+    const u64 w = (u64)__double_as_longlong(*y + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
+    return in ? w : 0;
   }
   __device__ __forceinline__ u64 fixed(float v) const {
-    if (v == top) return (u64)unit;
-    const double x = ((double)v - (double)top) * inv_t;
-    return x > floor_ ? __double2ull_rn(exp(x) * unit) : 0;
+    double y;
+    return fixed_of(exponent(v), &y);
   }
-  // Monotone in v: each step (difference, product, conversion) is.
+  // Monotone in v: each step (difference, product, minimum, and the sum with
+  // 2^23 that rounds to an integer) is.
   __device__ __forceinline__ int bin(float v) const {
-    if (v == top) return 0;
     const float d = top - v;
-    if (d <= edge) return (int)fminf(d * fine, (float)(kFine - 1));
-    return kFine + (int)fminf((d - edge) * coarse, (float)(kBins - kFine - 1));
+    const float near = fminf(d * fine, (float)(kFine - 1));
+    const float far = fminf((d - edge) * coarse, (float)(kBins - kFine - 1)) + (float)kFine;
+    const int b = __float_as_int((d <= edge ? near : far) + 8388608.f) & (kBins - 1);
+    return v == top ? 0 : b;
   }
 };
 
-template <class F>
-__device__ __forceinline__ void each(const Params& P, const float* data, const float* row,
-                                     int begin, int n, F f) {
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    f(P.resident ? data[i] : __ldcg(row + begin + i), begin + i);
-}
+// What a CTA of the cluster works on.
+struct Work {
+  const Params& P;
+  Shared& S;
+  const Row row_;
+  const float* data;
+  const float* row;
+  int begin, n;
+  unsigned rank, C;
 
-// Exclusive prefixes of the cluster's counts and weights over the bins
-// (rank 0, all threads): two neighbouring bins a thread.
-__device__ __forceinline__ void prefixes(Shared& S, const unsigned* c, const u64* w, unsigned* pc,
-                                         u64* pw) {
-  static_assert(kBins == 2 * kThreads, "two bins a thread");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned c0 = c[2 * tid], c1 = c[2 * tid + 1];
-  const u64 w0 = w[2 * tid], w1 = w[2 * tid + 1];
-  unsigned xc = c0 + c1;
-  u64 xw = w0 + w1;
+  // f(value, index) for the slice, four values side by side (their chains
+  // hide each other's latency); -inf past its end.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    const float* const from = P.resident ? data : row + begin;
+    const int len = n, first = begin;  // (in registers, whatever f does to memory)
+#pragma unroll 1
+    for (int i = threadIdx.x; i < len; i += 4 * kThreads) {
+      float v[4];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned yc = __shfl_up_sync(0xffffffffu, xc, o);
-    const u64 yw = __shfl_up_sync(0xffffffffu, xw, o);
-    if (lane >= o) {
-      xc += yc;
-      xw += yw;
+      for (int e = 0; e < 4; ++e)
+        v[e] = i + e * kThreads < len ? from[i + e * kThreads] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(v[e], first + i + e * kThreads);
     }
   }
-  if (lane == 31) {
-    S.red3[warp] = xc;
-    S.red[warp] = xw;
-  }
-  __syncthreads();
-  unsigned bc = xc - c0 - c1;
-  u64 bw = xw - w0 - w1;
-  for (int i = 0; i < warp; ++i) {
-    bc += S.red3[i];
-    bw += S.red[i];
-  }
-  pc[2 * tid] = bc;
-  pc[2 * tid + 1] = bc + c0;
-  pw[2 * tid] = bw;
-  pw[2 * tid + 1] = bw + w0;
-  __syncthreads();
-}
 
-// The cluster's sums of the CTAs' histograms into rank 0's (c, w): each rank
-// sums a share of the bins.
-__device__ __forceinline__ void sum_bins(Shared& S, unsigned rank, unsigned C, unsigned* c,
-                                         u64* w) {
-  const int per = kBins / C;
-  for (int i = threadIdx.x; i < per; i += kThreads) {
-    const int b = rank * per + i;
-    unsigned nc = 0;
-    u64 nw = 0;
-    for (unsigned r = 0; r < C; ++r) {
-      nc += ld_u32(remote(&S.hist_c[b], r));
-      nw += ld_u64(remote(&S.hist_w[b], r));
+  __device__ __forceinline__ void sync() const {
+    if (C == 1)
+      __syncthreads();
+    else
+      cluster_sync();
+  }
+
+  // The cluster's sums of the CTAs' histograms into rank 0's (c, w), each rank
+  // a share of the bins, and the sums of groups of 32 bins.
+  __device__ __forceinline__ void sum_bins(int bins, unsigned* c, u64* w) const {
+    const int per = bins / C;  // a multiple of 32
+    for (int i = threadIdx.x; i < per; i += kThreads) {
+      const int b = rank * per + i;
+      unsigned nc = 0;
+      u64 nw = 0;
+      const uint32_t ac = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_c[b]));
+      const uint32_t aw = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_w[b]));
+#pragma unroll 4
+      for (unsigned r = 0; r < C; ++r) {
+        nc += ld_u32(remote_at(ac, r));
+        if (w) nw += ld_u64(remote_at(aw, r));
+      }
+      st_u32(remote(&c[b], 0), nc);
+      if (w) st_u64(remote(&w[b], 0), nw);
+      nc = __reduce_add_sync(0xffffffffu, nc);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) nw += __shfl_xor_sync(0xffffffffu, nw, o);
+      if ((threadIdx.x & 31) == 0) {
+        st_u32(remote(&S.sup_c[b / 32], 0), nc);
+        if (w) st_u64(remote(&S.sup_w[b / 32], 0), nw);
+      }
     }
-    st_u32(remote(&c[b], 0), nc);
-    st_u64(remote(&w[b], 0), nw);
   }
-}
 
-// One collective step of the cluster on the members of a bin whose keys lie
-// in [lo, hi].
-__device__ __forceinline__ void serve(const Params& P, Shared& S, const Row& R, const float* data,
-                                      const float* row, int begin, int n, unsigned rank,
-                                      unsigned C) {
-  const Cmd c = S.cmd;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (c.op == kCollect) {
-    const uint32_t cnt = remote(&S.list_n, 0);
-    each(P, data, row, begin, n, [&](float v, int i) {
-      const u64 k = key_of(v, i);
-      if (k && R.bin(v) == c.bin && k >= c.lo && k <= c.hi) {
-        const unsigned at = add_u32(cnt, 1);
-        if (at < kList) {
-          st_u64(remote(&S.list_key[at], 0), k);
-          st_u64(remote(&S.list_w[at], 0), R.fixed(v));
-        }
+  // This thread's candidates with a weight of at least min_p: the CTA's sum to
+  // rank 0.
+  __device__ __forceinline__ void push_above(unsigned above) const {
+    above = __reduce_add_sync(0xffffffffu, above);
+    if ((threadIdx.x & 31) == 0) S.red3[threadIdx.x >> 5] = above;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kThreads / 32; ++i) above += S.red3[i];
+      st_u32(remote(&S.above[rank], 0), above);
+    }
+  }
+
+  // The slice's weights (and, with `count`, counts) into the histogram.
+  __device__ __forceinline__ void weigh(const Row& R, double min_p, bool count) const {
+    unsigned above = 0;
+    each([&](float v, int) {
+      const bool in = v > -INFINITY;
+      const int k = R.bin(v);
+      double y;
+      const u64 w = in ? R.fixed_of(R.exponent(v), &y) : 0;
+      if (in && count) atomicAdd(&S.hist_c[k], 1u);
+      if (w) {
+        add_weight(&S.hist_w[k], w);
+        // (scaling by 2^frac is exact: this is power(x, 0) >= min_p)
+        above += __hiloint2double(__double2hiint(y) - (R.frac << 20), __double2loint(y)) >= min_p;
       }
     });
-  } else if (c.op == kMinMax) {
-    u64 lo = ~0ull, hi = 0;
-    each(P, data, row, begin, n, [&](float v, int i) {
-      const u64 k = key_of(v, i);
-      if (k && R.bin(v) == c.bin) {
+    if (min_p > 0.0) push_above(above);
+  }
+
+  // One collective step of the cluster.
+  __device__ __noinline__ void serve(double min_p) const {
+    const Row R = row_;
+    const Cmd c = S.cmd;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (c.op == kCollect) {  // members of the wanted bins whose keys lie in [lo, hi]
+      // the CTA's own first, then all of them at once to rank 0
+      if (tid == 0) S.mine_n = 0;
+      __syncthreads();
+      each([&](float v, int i) {
+        const int b = R.bin(v);
+        if (S.wanted[b >> 5] >> (b & 31) & 1) {
+          const u64 k = key_of(v, i);
+          if (k != 0 && k >= c.lo && k <= c.hi) {
+            const unsigned at = atomicAdd(&S.mine_n, 1u);
+            if (at < kList) S.mine[at] = k;
+          }
+        }
+      });
+      __syncthreads();
+      const unsigned m = S.mine_n;
+      if (tid == 0) S.mine_n = add_u32(remote(&S.list_n, 0), m);
+      __syncthreads();
+      const unsigned at = S.mine_n + tid;
+      if (tid < (int)min(m, (unsigned)kList) && at < kList)
+        st_u64(remote(&S.list_key[at], 0), S.mine[tid]);
+    } else if (c.op == kMinMax) {  // of the bin's keys
+      u64 lo = ~0ull, hi = 0;
+      each([&](float v, int i) {
+        if (!(v > -INFINITY) || R.bin(v) != c.bin) return;
+        const u64 k = key_of(v, i);
         lo = min(lo, k);
         hi = max(hi, k);
+      });
+      lo = warp_min64(lo);
+      hi = warp_max64(hi);
+      if (lane == 0) {
+        S.red[warp] = lo;
+        S.red2[warp] = hi;
       }
-    });
-    lo = warp_min64(lo);
-    hi = warp_max64(hi);
-    if (lane == 0) {
-      S.red[warp] = lo;
-      S.red2[warp] = hi;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      for (int i = 1; i < kThreads / 32; ++i) {
-        lo = min(lo, S.red[i]);
-        hi = max(hi, S.red2[i]);
+      __syncthreads();
+      if (tid == 0) {
+        for (int i = 1; i < kThreads / 32; ++i) {
+          lo = min(lo, S.red[i]);
+          hi = max(hi, S.red2[i]);
+        }
+        st_u64(remote(&S.key_min[rank], 0), lo);
+        st_u64(remote(&S.key_max[rank], 0), hi);
       }
-      st_u64(remote(&S.key_min[rank], 0), lo);
-      st_u64(remote(&S.key_max[rank], 0), hi);
-    }
-  } else {
-    for (int i = tid; i < kBins; i += kThreads) {
-      S.hist_c[i] = 0;
-      S.hist_w[i] = 0;
-    }
-    __syncthreads();
-    each(P, data, row, begin, n, [&](float v, int i) {
-      const u64 k = key_of(v, i);
-      if (k && R.bin(v) == c.bin && k >= c.lo && k <= c.hi) {
+    } else if (c.op == kWeights) {  // the whole row's weights by bin
+      weigh(R, min_p, false);
+      sync();
+      sum_bins(kBins, S.tot_c, S.tot_w);
+    } else {  // kHist: the bin's keys in [lo, hi] by their distance to hi
+      for (int i = tid; i < kSubBins; i += kThreads) {
+        S.hist_c[i] = 0;
+        S.hist_w[i] = make_uint2(0, 0);
+      }
+      __syncthreads();
+      each([&](float v, int i) {
+        const u64 k = key_of(v, i);
+        if (!(v > -INFINITY) || R.bin(v) != c.bin || k < c.lo || k > c.hi) return;
         const int b = (int)((c.hi - k) >> c.shift);
         atomicAdd(&S.hist_c[b], 1u);
         const u64 w = R.fixed(v);
-        if (w) atomicAdd(&S.hist_w[b], w);
+        if (w) add_weight(&S.hist_w[b], w);
+      });
+      sync();
+      Sub& sub = *reinterpret_cast<Sub*>(S.list_key);
+      sum_bins(kSubBins, sub.c, sub.w);
+    }
+    sync();
+  }
+
+  // Rank 0: one collective step (every thread calls it).
+  __device__ __forceinline__ void ask(const Cmd& c, double min_p) const {
+    __syncthreads();
+    if (threadIdx.x == 0) S.list_n = 0;
+    if (threadIdx.x < C) {
+      const uint32_t a = remote(&S.cmd, threadIdx.x);
+      st_u32(a + offsetof(Cmd, op), c.op);
+      st_u32(a + offsetof(Cmd, bin), c.bin);
+      st_u32(a + offsetof(Cmd, shift), c.shift);
+      st_u64(a + offsetof(Cmd, lo), c.lo);
+      st_u64(a + offsetof(Cmd, hi), c.hi);
+    }
+    if (c.op == kCollect)
+      for (unsigned i = threadIdx.x; i < (C - 1) * (kBins / 32); i += kThreads)
+        st_u32(remote(&S.wanted[i % (kBins / 32)], 1 + i / (kBins / 32)),
+               S.wanted[i % (kBins / 32)]);
+    sync();
+    if (c.op != kDone) serve(min_p);
+  }
+
+  // Warp 0 of rank 0: the groups' sums into what lies before each.
+  __device__ __forceinline__ void scan_groups(int bins) const {
+    const int lane = threadIdx.x & 31, groups = bins / 32;  // at most 64: two a lane
+    const unsigned c0 = 2 * lane < groups ? S.sup_c[2 * lane] : 0;
+    const unsigned c1 = 2 * lane < groups ? S.sup_c[2 * lane + 1] : 0;
+    const u64 w0 = 2 * lane < groups ? S.sup_w[2 * lane] : 0;
+    const u64 w1 = 2 * lane < groups ? S.sup_w[2 * lane + 1] : 0;
+    unsigned xc = c0 + c1;
+    u64 xw = w0 + w1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned yc = __shfl_up_sync(0xffffffffu, xc, o);
+      const u64 yw = __shfl_up_sync(0xffffffffu, xw, o);
+      if (lane >= o) {
+        xc += yc;
+        xw += yw;
       }
-    });
-    cluster_sync();
-    sum_bins(S, rank, C, S.sub_c, S.sub_w);
+    }
+    if (2 * lane < groups) {
+      S.sup_c[2 * lane + 1] = xc - c1;
+      S.sup_c[2 * lane + 2] = xc;
+      S.sup_w[2 * lane + 1] = xw - w1;
+      S.sup_w[2 * lane + 2] = xw;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      S.sup_c[0] = 0;
+      S.sup_w[0] = 0;
+    }
+    __syncwarp();
   }
-  cluster_sync();
-}
 
-// Rank 0: one collective step (every thread calls it).
-__device__ __forceinline__ void ask(const Params& P, Shared& S, const Row& R, const float* data,
-                                    const float* row, int begin, int n, unsigned C, const Cmd& c) {
-  __syncthreads();
-  if (threadIdx.x == 0) S.list_n = 0;
-  if (threadIdx.x < C) {
-    const uint32_t a = remote(&S.cmd, threadIdx.x);
-    st_u32(a + offsetof(Cmd, op), c.op);
-    st_u32(a + offsetof(Cmd, bin), c.bin);
-    st_u32(a + offsetof(Cmd, shift), c.shift);
-    st_u64(a + offsetof(Cmd, lo), c.lo);
-    st_u64(a + offsetof(Cmd, hi), c.hi);
+  // Warp 0 of rank 0: the bin where the running count passes the target
+  // (by_weight: where the running weight reaches it).
+  __device__ __noinline__ Bin find_bin(int bins, const unsigned* c, const u64* w, bool by_weight,
+                                       u64 target) const {
+    const int lane = threadIdx.x & 31, groups = bins / 32;
+    const u64 t = by_weight ? target - 1 : target;
+    // groups that begin at or before t: the last one holds it
+    const int g0 = lane, g1 = lane + 32;
+    const bool in0 = g0 < groups && (by_weight ? S.sup_w[g0] : S.sup_c[g0]) <= t;
+    const bool in1 = g1 < groups && (by_weight ? S.sup_w[g1] : S.sup_c[g1]) <= t;
+    int g = __popc(__ballot_sync(0xffffffffu, in0)) + __popc(__ballot_sync(0xffffffffu, in1)) - 1;
+    // (empty groups share their start with the next one, and come before it)
+    const unsigned mc = c[g * 32 + lane];
+    const u64 mw = w[g * 32 + lane];
+    unsigned xc = mc;
+    u64 xw = mw;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned yc = __shfl_up_sync(0xffffffffu, xc, o);
+      const u64 yw = __shfl_up_sync(0xffffffffu, xw, o);
+      if (lane >= o) {
+        xc += yc;
+        xw += yw;
+      }
+    }
+    const u64 ic = S.sup_c[g] + xc, iw = S.sup_w[g] + xw;
+    const unsigned m = __ballot_sync(0xffffffffu, (by_weight ? iw : ic) > t);
+    const int l = m ? __ffs(m) - 1 : 31;
+    Bin b;
+    b.at = g * 32 + l;
+    b.pc = __shfl_sync(0xffffffffu, ic - mc, l);
+    b.pw = __shfl_sync(0xffffffffu, iw - mw, l);
+    b.c = __shfl_sync(0xffffffffu, mc, l);
+    b.w = __shfl_sync(0xffffffffu, mw, l);
+    return b;
   }
-  cluster_sync();
-  if (c.op != kDone) serve(P, S, R, data, row, begin, n, 0, C);
-}
 
-// The bin where the running count passes `target` (by_weight: where the
-// running weight reaches it).
-__device__ __forceinline__ int find_bin(Shared& S, const unsigned* c, const u64* w,
-                                        const unsigned* pc, const u64* pw, bool by_weight,
-                                        u64 target) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    const bool in = by_weight ? pw[i] < target && target <= pw[i] + w[i]
-                              : pc[i] <= target && target < (u64)pc[i] + c[i];
-    if (in) S.s_bin = i;
+  // Warp 0: the first of n places for which f holds (n if none; f changes once).
+  template <class F>
+  __device__ __forceinline__ unsigned first_of(unsigned n, F f) const {
+    const unsigned lane = threadIdx.x & 31;
+    unsigned base = 0;
+    if (n == 0) return 0;
+    if (n > 32) {  // groups of 32 (at most 32 of them) by their last place
+      const unsigned m = __ballot_sync(0xffffffffu, f(min(lane * 32 + 31, n - 1)));
+      base = m ? 32 * (__ffs(m) - 1) : n - 1;
+    }
+    const unsigned q = min(base + lane, n - 1);
+    const unsigned m = __ballot_sync(0xffffffffu, f(q));
+    return m ? min(base + __ffs(m) - 1, n - 1) : n;
   }
-  __syncthreads();
-  return S.s_bin;
+
+  // A place in the list's part of a bin.
+  __device__ __forceinline__ Found in_list(const Bin& b, unsigned start, unsigned n, bool by_weight,
+                                           u64 target) const {
+    const u64 base = start ? S.list_w[start - 1] : 0;
+    const unsigned q =
+        start + (by_weight ? first_of(n - start,
+                                      [&](unsigned i) {
+                                        return S.list_w[start + i] - base + b.pw >= target;
+                                      })
+                           : (unsigned)(target - b.pc));
+    const unsigned at = min(q, max(n, 1u) - 1);
+    return Found{b.pc + (at - start), S.list_w[at] - base + b.pw, S.list_key[at]};
+  }
+
+  // Sorts the list's n keys, largest first, one a thread (bitonic; strides
+  // below a warp by shuffles, the others through the list's two arrays in
+  // turn), and forms the running weights.
+  __device__ __noinline__ void sort_list(unsigned n) const {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Row R = row_;
+    u64 k = tid < (int)n ? S.list_key[tid] : 0;
+    u64* buf[2] = {S.list_w, S.list_key};
+    int turn = 0;
+    if (n > 32 || warp == 0) {
+#pragma unroll 1
+      for (unsigned size = 2; size < 2 * n; size <<= 1) {
+#pragma unroll 1
+        for (unsigned stride = size >> 1; stride > 0; stride >>= 1) {
+          u64 o;
+          if (stride < 32) {
+            o = __shfl_xor_sync(0xffffffffu, k, stride);
+          } else {
+            buf[turn][tid] = k;
+            __syncthreads();
+            o = buf[turn][tid ^ stride];
+            turn ^= 1;
+          }
+          const bool larger = ((tid & stride) == 0) == ((tid & size) == 0);
+          k = larger ? max(k, o) : min(k, o);
+        }
+      }
+    }
+    u64 x = k ? R.fixed(value_of(k)) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) S.red[warp] = x;
+    __syncthreads();
+    u64 before = lane < warp ? S.red[lane] : 0;
+    if (warp > 0)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    S.list_key[tid] = k;
+    S.list_w[tid] = x + before;
+    __syncthreads();
+  }
+};
+
+// f of a weight, at least 1, at most all of it.
+__device__ __noinline__ u64 share(double f, u64 total) {
+  const double t = ceil(fmin(fmax(f, 0.0), 1.0) * (double)total);
+  return max((u64)1, min(total, __double2ull_rn(t)));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ Params P) {
@@ -333,24 +575,48 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   const float* row = P.logits + (long long)b * P.ld;
   for (int i = tid; i < kBins; i += kThreads) {
     S.hist_c[i] = 0;
-    S.hist_w[i] = 0;
+    S.hist_w[i] = make_uint2(0, 0);
   }
+  if (tid < kSteps) S.pow2[tid] = P.pow2[tid];
   pdl_wait();
+  const float T = P.temperature ? __ldcg(P.temperature + b) : 1.f;
+  const int top_k = P.top_k ? __ldcg(P.top_k + b) : 0;
+  const float top_p = P.top_p ? __ldcg(P.top_p + b) : 1.f;
+  const float min_p = P.min_p ? __ldcg(P.min_p + b) : 0.f;
 
-  // ---- the row's candidates: largest, smallest, how many
-  u64 hi = 0, lo = ~0ull;
+  // ---- the row's candidates: largest (the first of equal ones), smallest,
+  // how many
+  float fhi = -INFINITY, flo = INFINITY;
+  int ihi = 0;
   unsigned cnt = 0;
-#pragma unroll 8
-  for (int i = tid; i < n; i += kThreads) {
+  auto note = [&](float v, int i) {
+    if (v > -INFINITY) {
+      if (v > fhi) {
+        fhi = v;
+        ihi = i;
+      }
+      flo = fminf(flo, v);
+      ++cnt;
+    }
+  };
+  int i = tid;
+  for (; i + 7 * kThreads < n; i += 8 * kThreads) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __ldcg(row + begin + i + e * kThreads);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (P.resident) data[i + e * kThreads] = v[e];
+      note(v[e], begin + i + e * kThreads);
+    }
+  }
+  for (; i < n; i += kThreads) {
     const float v = __ldcg(row + begin + i);
     if (P.resident) data[i] = v;
-    const u64 k = key_of(v, begin + i);
-    hi = max(hi, k);
-    lo = min(lo, k ? k : ~0ull);
-    cnt += k != 0;
+    note(v, begin + i);
   }
-  hi = warp_max64(hi);
-  lo = warp_min64(lo);
+  u64 hi = warp_max64(cnt ? key_of(fhi, ihi) : 0);
+  u64 lo = warp_min64(cnt ? key_of(flo, 0) : ~0ull);
   cnt = __reduce_add_sync(0xffffffffu, cnt);
   if (lane == 0) {
     S.red[warp] = hi;
@@ -358,20 +624,20 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     S.red3[warp] = cnt;
   }
   __syncthreads();
-  if (tid < (int)C) {  // to every rank
-    hi = S.red[0];
-    lo = S.red2[0];
-    cnt = S.red3[0];
-    for (int i = 1; i < kThreads / 32; ++i) {
-      hi = max(hi, S.red[i]);
-      lo = min(lo, S.red2[i]);
-      cnt += S.red3[i];
+  if (warp == 0) {  // to every rank
+    hi = warp_max64(lane < kThreads / 32 ? S.red[lane] : 0);
+    lo = warp_min64(lane < kThreads / 32 ? S.red2[lane] : ~0ull);
+    cnt = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? S.red3[lane] : 0);
+    if (lane < (int)C) {
+      st_u64(remote(&S.key_max[rank], lane), hi);
+      st_u64(remote(&S.key_min[rank], lane), lo);
+      st_u32(remote(&S.count[rank], lane), cnt);
     }
-    st_u64(remote(&S.key_max[rank], tid), hi);
-    st_u64(remote(&S.key_min[rank], tid), lo);
-    st_u32(remote(&S.count[rank], tid), cnt);
   }
-  cluster_sync();
+  if (C == 1)
+    __syncthreads();
+  else
+    cluster_sync();
   hi = 0;
   lo = ~0ull;
   cnt = 0;
@@ -380,12 +646,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     lo = min(lo, S.key_min[r]);
     cnt += S.count[r];
   }
-
-  // ---- the row's parameters
-  const float T = P.temperature ? __ldcg(P.temperature + b) : 1.f;
-  const int top_k = P.top_k ? __ldcg(P.top_k + b) : 0;
-  const float top_p = P.top_p ? __ldcg(P.top_p + b) : 1.f;
-  const float min_p = P.min_p ? __ldcg(P.min_p + b) : 0.f;
   if (cnt == 0 || !(T > 0.f) || top_k == 1) {  // no candidate, or the first one
     if (rank == 0 && tid == 0) {
       P.out[b] = cnt ? index_of(hi) : 0;
@@ -395,153 +655,256 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     return;  // (nobody reads another CTA's shared memory any more)
   }
   Row R;
+  R.pow2 = S.pow2;
   R.top = value_of(hi);
   R.inv_t = 1.0 / (double)T;
-  R.unit = (double)(1ull << P.frac);
-  R.floor_ = -0.6931471805599453 * (P.frac + 1);
+  R.frac = P.frac;
+  R.least = -0.6931471805599453 * (P.frac + 1);
   // fine bins up to the last value with a weight, coarse ones beyond
   const float span = R.top - value_of(lo);
-  R.edge = fminf(fminf(span, (float)(-R.floor_ * (double)T)), FLT_MAX);
+  R.edge = fminf(fminf(span, (float)(-R.least * (double)T)), FLT_MAX);
   R.fine = R.edge > 0.f ? (float)kFine / R.edge : 0.f;
   const float rest = fminf(span, 32.f * R.edge + 64.f) - R.edge;
   R.coarse = rest > 0.f ? (float)(kBins - kFine) / rest : 0.f;
+  const Work W = {P, S, R, data, row, begin, n, rank, C};
 
-  // ---- histogram of counts and weights
-  const bool use_m = min_p > 0.f;
-  const double mp = fmin(1.0, (double)min_p);
-  unsigned above = 0;
-  each(P, data, row, begin, n, [&](float v, int i) {
-    if (!(v > -INFINITY)) return;
-    const int k = R.bin(v);
-    atomicAdd(&S.hist_c[k], 1u);
-    const u64 w = R.fixed(v);
-    if (w) atomicAdd(&S.hist_w[k], w);
-    if (use_m) above += R.weight(v) >= mp;
-  });
-  above = __reduce_add_sync(0xffffffffu, above);
-  if (lane == 0) S.red3[warp] = above;
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) above += S.red3[i];
-    st_u32(remote(&S.above[rank], 0), above);
-  }
-  cluster_sync();
-  sum_bins(S, rank, C, S.tot_c, S.tot_w);
-  cluster_sync();
+  // ---- histogram of counts and, unless a small top-k will do without, of
+  // weights
+  const double mp = min_p > 0.f ? fmin(1.0, (double)min_p) : 0.0;
+  const bool few = top_k > 0 && top_k <= kThreads / 2 && (unsigned)top_k < cnt;
+  if (few)
+    W.each([&](float v, int) {
+      const int k = R.bin(v);
+      if (v > -INFINITY) atomicAdd(&S.hist_c[k], 1u);
+    });
+  else
+    W.weigh(R, mp, true);
+  W.sync();
+  W.sum_bins(kBins, S.tot_c, few ? nullptr : S.tot_w);
+  W.sync();
 
   if (rank != 0) {  // rank 0 leads from here
     for (;;) {
-      cluster_sync();
+      W.sync();
       if (S.cmd.op == kDone) return;
-      serve(P, S, R, data, row, begin, n, rank, C);
+      W.serve(mp);
     }
   }
-  prefixes(S, S.tot_c, S.tot_w, S.tot_pc, S.tot_pw);
-
-  int listed = -1;  // the bin whose members are in the list, all of them
-  unsigned list_n = 0;
-  u64 list_pc = 0, list_pw = 0;  // candidates and weight before the list
-
-  // The candidate where the running count passes `target`, or the running
-  // weight reaches it: a_rank (candidates before it), a_cum (running weight
-  // with it) and, if `want_key`, a_key.
-  auto search = [&](bool by_weight, u64 target, bool want_key) {
-    const int bin = find_bin(S, S.tot_c, S.tot_w, S.tot_pc, S.tot_pw, by_weight, target);
-    const u64 pc = S.tot_pc[bin], pw = S.tot_pw[bin];
-    const unsigned c = S.tot_c[bin];
-    if (!want_key && (c == 1 || (!by_weight && target == pc + c - 1))) {
-      __syncthreads();
-      if (tid == 0) {
-        S.a_rank = pc + c - 1;
-        S.a_cum = pw + S.tot_w[bin];
-      }
-      __syncthreads();
-      return;
+  // ---- rank 0. Decisions are warp 0's; the other warps help with collections
+  // and sorting.
+  const float ub = P.u ? __ldcg(P.u + b) : 0.f;
+  u64 kept = cnt, sum = 0;
+  Bin kb = {-1, 0, 0, 0, 0};
+  Found pick = {0, 0, 0};
+  if (top_k > 0 && (u64)top_k < kept) kept = top_k;
+  const bool by_k = kept < cnt;
+  auto want = [&](int from, int to) {  // bins from .. to (warp 0)
+#pragma unroll
+    for (int e = 0; e < kBins / 32; e += 32) {
+      const int q = e + lane, l = max(0, from - 32 * q), h = min(31, to - 32 * q);
+      if (l <= h) S.wanted[q] |= (0xFFFFFFFFu >> (31 - h)) & (0xFFFFFFFFu << l);
     }
-    if (listed != bin) {
-      Cmd cmd = {kCollect, bin, 0, 0, ~0ull};
-      list_n = c;
-      list_pc = pc;
-      list_pw = pw;
-      listed = bin;
-      if (c > kList) {  // narrow the bin down by its keys
-        listed = -1;
-        ask(P, S, R, data, row, begin, n, C, Cmd{kMinMax, bin, 0, 0, 0});
-        cmd.lo = ~0ull;
-        cmd.hi = 0;
-        for (unsigned r = 0; r < C; ++r) {
-          cmd.lo = min(cmd.lo, S.key_min[r]);
-          cmd.hi = max(cmd.hi, S.key_max[r]);
-        }
-        while (list_n > kList) {
-          const u64 width = cmd.hi - cmd.lo;  // keys differ, so it is at least list_n - 1
-          const int bits = 64 - __clzll((long long)width);
-          Cmd h = {kHist, bin, max(0, bits - 10), cmd.lo, cmd.hi};
-          ask(P, S, R, data, row, begin, n, C, h);
-          prefixes(S, S.sub_c, S.sub_w, S.sub_pc, S.sub_pw);
-          const int s = find_bin(S, S.sub_c, S.sub_w, S.sub_pc, S.sub_pw, by_weight,
-                                 by_weight ? target - list_pw : target - list_pc);
-          list_n = S.sub_c[s];
-          list_pc += S.sub_pc[s];
-          list_pw += S.sub_pw[s];
-          const u64 top = cmd.hi - ((u64)s << h.shift);
-          const u64 low = top - (((u64)1 << h.shift) - 1);
-          cmd.lo = low > top || low < cmd.lo ? cmd.lo : low;
-          cmd.hi = top;
-        }
-      }
-      ask(P, S, R, data, row, begin, n, C, cmd);
-    }
-    // rank the members against each other
-    for (unsigned i = tid; i < list_n; i += kThreads) {
-      const u64 k = S.list_key[i];
-      u64 before = list_pc, sum = list_pw;
-      for (unsigned j = 0; j < list_n; ++j) {
-        const bool ahead = S.list_key[j] > k;
-        before += ahead;
-        sum += ahead ? S.list_w[j] : 0;
-      }
-      const u64 w = S.list_w[i];
-      if (by_weight ? sum < target && target <= sum + w : before == target) {
-        S.a_rank = before;
-        S.a_cum = sum + w;
-        S.a_key = k;
-      }
-    }
+  };
+  auto bin_at = [&](bool by_weight, u64 target) {
+    return W.find_bin(kBins, S.tot_c, S.tot_w, by_weight, target);
+  };
+  auto go_on = [&](int path) {  // warp 0's decision, known to all
     __syncthreads();
+    if (tid == 0) S.path = path;
+    __syncthreads();
+    return S.path;
   };
-  auto share = [&](double f, u64 total) {  // f of a weight, at least 1, at most all of it
-    const double t = ceil(fmin(fmax(f, 0.0), 1.0) * (double)total);
-    return max((u64)1, min(total, __double2ull_rn(t)));
-  };
+  enum { kPathFew, kPathList, kPathSlow, kPathWeigh, kPathEnd };
 
-  u64 kept = cnt, sum = S.tot_pw[kBins - 1] + S.tot_w[kBins - 1];
-  if (top_k > 0 && (u64)top_k < kept) {
-    kept = top_k;
-    search(false, kept - 1, false);
-    sum = S.a_cum;
-  }
-  if (top_p < 1.f) {
-    search(true, share(top_p, sum), false);
-    kept = min(kept, S.a_rank + 1);
-    sum = S.a_cum;
-  }
-  if (use_m) {
-    u64 m = 0;
-    for (unsigned r = 0; r < C; ++r) m += S.above[r];
-    if (m < kept) {
-      kept = m;
-      search(false, kept - 1, false);
-      sum = S.a_cum;
+  int path = 0;
+  if (warp == 0) {
+    for (int q = lane; q < kBins / 32; q += 32) S.wanted[q] = 0;
+    if (few)
+      for (int q = lane; q < kBins / 32; q += 32) S.sup_w[q] = 0;
+    __syncwarp();
+    W.scan_groups(kBins);
+    if (few) {
+      kb = bin_at(false, kept - 1);
+      path = kb.pc + kb.c <= kThreads ? kPathFew : kPathWeigh;
+      if (path == kPathFew) want(0, kb.at);
+    } else {
+      path = kPathSlow;
     }
   }
-  search(true, share(P.u ? (double)__ldcg(P.u + b) : 0.0, sum), true);
-  const u64 pick = S.a_key;
-  ask(P, S, R, data, row, begin, n, C, Cmd{kDone, 0, 0, 0, 0});
+  if (few) path = go_on(path);
+  if (few && path == kPathFew) {
+    // ---- the members of the first bins, sorted; the filters shorten the list
+    W.ask(Cmd{kCollect, 0, 0, 0, ~0ull}, mp);
+    W.sort_list(S.list_n);
+    if (warp == 0) {
+      auto first_at = [&](unsigned len, u64 target) {  // whose running weight reaches it
+        return min(len - 1, W.first_of(len, [&](unsigned q) { return S.list_w[q] >= target; }));
+      };
+      unsigned len = (unsigned)kept;
+      if (top_p < 1.f) len = first_at(len, share(top_p, S.list_w[len - 1])) + 1;
+      if (mp > 0.0)
+        len = W.first_of(len, [&](unsigned q) { return R.weight(value_of(S.list_key[q])) < mp; });
+      kept = len;
+      sum = S.list_w[len - 1];
+      pick.key = S.list_key[first_at(len, share(ub, sum))];
+    }
+  } else {
+    if (few) {  // too many share the first bins: weights after all
+      W.ask(Cmd{kWeights, 0, 0, 0, 0}, mp);
+      if (warp == 0) W.scan_groups(kBins);
+    }
+    u64 total = 0, above = cnt;
+    if (warp == 0) {
+      // ---- the bins that can hold a filter's end or the draw, from what the
+      // histogram bounds; their members in one collection
+      total = S.sup_w[kBins / 32];
+      if (mp > 0.0) above = __reduce_add_sync(0xffffffffu, lane < (int)C ? S.above[lane] : 0);
+      u64 z0 = total, z1 = total;    // bounds of the weight that top-k keeps
+      u64 s0 = total, s1 = total;    // of the kept weight
+      u64 many = 0;
+      if (by_k) {
+        kb = bin_at(false, kept - 1);
+        z1 = kb.pw + kb.w;
+        z0 = kept == kb.pc + kb.c ? z1 : min(z1, kb.pw + 1);
+        s0 = z0;
+        s1 = z1;
+        want(kb.at, kb.at);
+        many += kb.c;
+      }
+      if (top_p < 1.f) {
+        const Bin p0 = bin_at(true, share(top_p, z0)), p1 = bin_at(true, share(top_p, z1));
+        s0 = min(s0, p0.pw + 1);
+        s1 = min(s1, p1.pw + p1.w);
+        want(p0.at, p1.at);
+        many += p1.pc + p1.c - p0.pc;
+      }
+      if (above < kept) {
+        const Bin m = bin_at(false, above - 1);
+        s0 = min(s0, m.pw + 1);
+        s1 = min(s1, m.pw + m.w);
+        want(m.at, m.at);
+        many += m.c;
+      }
+      const Bin d0 = bin_at(true, share(ub, min(s0, total)));
+      const Bin d1 = bin_at(true, share(ub, max(s1, (u64)1)));
+      want(d0.at, d1.at);
+      many += d1.pc + d1.c - d0.pc;
+      path = many <= kThreads ? kPathList : kPathSlow;
+    }
+    path = go_on(path);
+    if (path == kPathList) {
+      W.ask(Cmd{kCollect, 0, 0, 0, ~0ull}, mp);
+      const unsigned n_list = S.list_n;
+      W.sort_list(n_list);
+      if (warp == 0) {
+        bool lost = false;  // a bin outside the collection: the bounds did not hold
+        auto search = [&](bool by_weight, u64 target) {
+          const Bin q = bin_at(by_weight, target);
+          if (!(S.wanted[q.at >> 5] >> (q.at & 31) & 1)) {
+            lost = true;
+            return Found{0, 1, 0};
+          }
+          const unsigned start = W.first_of(
+              n_list, [&](unsigned i) { return R.bin(value_of(S.list_key[i])) >= q.at; });
+          return W.in_list(q, start, min(n_list, start + (unsigned)q.c), by_weight, target);
+        };
+        u64 k = kept, run = total;
+        if (by_k) run = search(false, k - 1).cum;
+        if (top_p < 1.f) {
+          const Found f = search(true, share(top_p, run));
+          k = min(k, f.rank + 1);
+          run = f.cum;
+        }
+        if (above < k) {
+          k = above;
+          run = search(false, k - 1).cum;
+        }
+        pick = search(true, share(ub, run));
+        path = lost ? kPathSlow : kPathEnd;
+        if (!lost) {
+          kept = k;
+          sum = run;
+        }
+      }
+      path = go_on(path);
+    }
+    if (path == kPathSlow) {
+      // ---- one bin after another: those with many members (equal or crowded
+      // values) are narrowed down by the keys first. `kept`, `sum` and `pick`
+      // are the same in all threads here
+      total = S.sup_w[kBins / 32];
+      above = cnt;
+      if (mp > 0.0) {
+        above = 0;
+        for (unsigned r = 0; r < C; ++r) above += S.above[r];
+      }
+      auto search = [&](bool by_weight, u64 target) {
+        Sub& sub = *reinterpret_cast<Sub*>(S.list_key);
+        __syncthreads();
+        Bin q = W.find_bin(kBins, S.tot_c, S.tot_w, by_weight, target);  // (every warp)
+        const int bin = q.at;
+        Cmd cmd = {kCollect, bin, 0, 0, ~0ull};
+        if (q.c > kThreads) {
+          W.ask(Cmd{kMinMax, bin, 0, 0, 0}, mp);
+          cmd.lo = ~0ull;
+          cmd.hi = 0;
+          for (unsigned r = 0; r < C; ++r) {
+            cmd.lo = min(cmd.lo, S.key_min[r]);
+            cmd.hi = max(cmd.hi, S.key_max[r]);
+          }
+          // the row's groups make way for the bin's and come back after it
+          const unsigned keep_c = tid <= kBins / 32 ? S.sup_c[tid] : 0;
+          const u64 keep_w = tid <= kBins / 32 ? S.sup_w[tid] : 0;
+          while (q.c > kThreads) {
+            const u64 width = cmd.hi - cmd.lo;  // keys differ: at least q.c - 1
+            const int bits = 64 - __clzll((long long)width);
+            const Cmd h = {kHist, bin, max(0, bits - 9), cmd.lo, cmd.hi};
+            W.ask(h, mp);
+            if (warp == 0) W.scan_groups(kSubBins);
+            __syncthreads();
+            const Bin s = W.find_bin(kSubBins, sub.c, sub.w, by_weight,
+                                     by_weight ? target - q.pw : target - q.pc);
+            q.pc += s.pc;
+            q.pw += s.pw;
+            q.c = s.c;
+            q.w = s.w;
+            const u64 top = cmd.hi - ((u64)s.at << h.shift);
+            const u64 low = top - (((u64)1 << h.shift) - 1);
+            cmd.lo = low > top || low < cmd.lo ? cmd.lo : low;
+            cmd.hi = top;
+          }
+          __syncthreads();
+          if (tid <= kBins / 32) {
+            S.sup_c[tid] = keep_c;
+            S.sup_w[tid] = keep_w;
+          }
+        }
+        __syncthreads();
+        if (tid < kBins / 32) S.wanted[tid] = tid == bin >> 5 ? 1u << (bin & 31) : 0;
+        W.ask(cmd, mp);
+        W.sort_list(S.list_n);
+        return W.in_list(q, 0, (unsigned)q.c, by_weight, target);  // (every warp)
+      };
+      sum = total;
+      if (by_k) sum = search(false, kept - 1).cum;
+      if (top_p < 1.f) {
+        const Found f = search(true, share(top_p, sum));
+        kept = min(kept, f.rank + 1);
+        sum = f.cum;
+      }
+      if (above < kept) {
+        kept = above;
+        sum = search(false, kept - 1).cum;
+      }
+      pick = search(true, share(ub, sum));
+    }
+  }
+  W.ask(Cmd{kDone, 0, 0, 0, 0}, mp);
   if (tid == 0) {
-    P.out[b] = index_of(pick);
+    P.out[b] = index_of(pick.key);
     if (P.kept) P.kept[b] = (int32_t)kept;
-    if (P.logprob) P.logprob[b] = (float)log(R.weight(value_of(pick)) / ((double)sum / R.unit));
+    if (P.logprob)
+      P.logprob[b] = (float)log(R.power(R.exponent(value_of(pick.key)), R.frac) / (double)sum);
   }
 }
 
@@ -553,6 +916,38 @@ inline int cluster_for(int B, int V) {
   while (c < kMaxCluster && (V + c - 1) / c > kResident) c *= 2;
   return c;
 }
+
+cudaError_t launch(const Params& P, int C, int B, cudaStream_t st) {
+  const void* f = (const void*)sample_kernel;
+  ensure_smem(f, (int)(sizeof(Shared) + kResident * 4));
+  if (C > 8) {
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared) + (P.resident ? (size_t)P.slice * 4 : 0);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, sample_kernel, P);
+}
+
+struct Pow2 {
+  double v[kSteps];
+  Pow2() {
+    for (int i = 0; i < kSteps; ++i) v[i] = exp2((double)i / kSteps);
+  }
+};
 
 }  // namespace sf
 }  // namespace qg
@@ -577,6 +972,7 @@ extern "C" qg_status qg_sample_filtered(const float* logits, long long ld, int B
                  aligned(top_p, 4) && aligned(min_p, 4) && aligned(u, 4) && aligned(out, 4) &&
                  aligned(kept, 4) && aligned(logprob, 4),
              QG_ERR_MISALIGNED, "%s: a pointer is not 4-byte aligned", who);
+  static const sf::Pow2 pow2;
   const int C = sf::cluster_for(B, V);
   sf::Params P = {};
   P.logits = logits;
@@ -594,28 +990,13 @@ extern "C" qg_status qg_sample_filtered(const float* logits, long long ld, int B
   P.resident = P.slice <= sf::kResident;
   P.frac = 44;
   while (((unsigned long long)V << P.frac) > (1ull << 62)) --P.frac;
-  const size_t smem = sizeof(sf::Shared) + (P.resident ? (size_t)P.slice * 4 : 0);
-  ensure_smem((const void*)sf::sample_kernel, (int)(sizeof(sf::Shared) + sf::kResident * 4));
-  if (C > 8) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)sf::sample_kernel,
-                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    QG_REQUIRE(e == cudaSuccess, QG_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  for (int i = 0; i < sf::kSteps; ++i) P.pow2[i] = pow2.v[i];
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = sf::launch(P, C, B, st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_error("%s: CUDA launch failed: %s", who, cudaGetErrorString(e));
+    return QG_ERR_CUDA;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C, B);
-  cfg.blockDim = dim3(sf::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  count_launch();
-  cudaLaunchKernelEx(&cfg, sf::sample_kernel, P);
   return check_launch(who);
 }
