@@ -32,8 +32,7 @@ namespace sf {
 
 constexpr int kBins = 2048;
 constexpr int kFine = 1536;         // bins for the values whose weight is not 0
-constexpr int kThreads = 512;
-constexpr int kList = kThreads;     // members that rank 0 can hold, one a thread
+constexpr int kList = 512;          // members that rank 0 can hold at most (one a thread)
 constexpr int kMaxCluster = 16;
 constexpr int kResident = 37984;    // values of a slice that shared memory holds
 constexpr int kSteps = 64;          // entries of the table of 2^(i / kSteps)
@@ -165,6 +164,15 @@ __device__ __forceinline__ u64 warp_min64(u64 v) {
   return v;
 }
 
+// Sum over the warp in three parts of 26, 26 and 12 bits (the parts' sums
+// fit 32 bits).
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+  const u64 a = __reduce_add_sync(0xffffffffu, (unsigned)v & 0x3FFFFFFu);
+  const u64 b = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 26) & 0x3FFFFFFu);
+  const u64 c = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 52));
+  return a + (b << 26) + (c << 52);
+}
+
 __device__ __forceinline__ void add_weight(uint2* at, u64 w) {
   const unsigned lo = (unsigned)w, old = atomicAdd(&at->x, lo);
   const unsigned hi = (unsigned)(w >> 32) + (old + lo < old);
@@ -230,6 +238,7 @@ struct Row {
 };
 
 // What a CTA of the cluster works on.
+template <int NTHR>
 struct Work {
   const Params& P;
   Shared& S;
@@ -246,13 +255,13 @@ struct Work {
     const float* const from = P.resident ? data : row + begin;
     const int len = n, first = begin;  // (in registers, whatever f does to memory)
 #pragma unroll 1
-    for (int i = threadIdx.x; i < len; i += 4 * kThreads) {
+    for (int i = threadIdx.x; i < len; i += 4 * NTHR) {
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        v[e] = i + e * kThreads < len ? from[i + e * kThreads] : -INFINITY;
+        v[e] = i + e * NTHR < len ? from[i + e * NTHR] : -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f(v[e], first + i + e * kThreads);
+      for (int e = 0; e < 4; ++e) f(v[e], first + i + e * NTHR);
     }
   }
 
@@ -267,22 +276,25 @@ struct Work {
   // a share of the bins, and the sums of groups of 32 bins.
   __device__ __forceinline__ void sum_bins(int bins, unsigned* c, u64* w) const {
     const int per = bins / C;  // a multiple of 32
-    for (int i = threadIdx.x; i < per; i += kThreads) {
+    for (int i = threadIdx.x; i < per; i += NTHR) {
       const int b = rank * per + i;
-      unsigned nc = 0;
-      u64 nw = 0;
-      const uint32_t ac = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_c[b]));
-      const uint32_t aw = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_w[b]));
+      unsigned nc = S.hist_c[b];
+      u64 nw = w ? *reinterpret_cast<const u64*>(&S.hist_w[b]) : 0;
+      if (C > 1) {
+        nc = 0;
+        nw = 0;
+        const uint32_t ac = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_c[b]));
+        const uint32_t aw = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_w[b]));
 #pragma unroll 4
-      for (unsigned r = 0; r < C; ++r) {
-        nc += ld_u32(remote_at(ac, r));
-        if (w) nw += ld_u64(remote_at(aw, r));
+        for (unsigned r = 0; r < C; ++r) {
+          nc += ld_u32(remote_at(ac, r));
+          if (w) nw += ld_u64(remote_at(aw, r));
+        }
       }
       st_u32(remote(&c[b], 0), nc);
       if (w) st_u64(remote(&w[b], 0), nw);
       nc = __reduce_add_sync(0xffffffffu, nc);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) nw += __shfl_xor_sync(0xffffffffu, nw, o);
+      nw = warp_sum64(nw);
       if ((threadIdx.x & 31) == 0) {
         st_u32(remote(&S.sup_c[b / 32], 0), nc);
         if (w) st_u64(remote(&S.sup_w[b / 32], 0), nw);
@@ -297,7 +309,7 @@ struct Work {
     if ((threadIdx.x & 31) == 0) S.red3[threadIdx.x >> 5] = above;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int i = 1; i < kThreads / 32; ++i) above += S.red3[i];
+      for (int i = 1; i < NTHR / 32; ++i) above += S.red3[i];
       st_u32(remote(&S.above[rank], 0), above);
     }
   }
@@ -335,7 +347,7 @@ struct Work {
           const u64 k = key_of(v, i);
           if (k != 0 && k >= c.lo && k <= c.hi) {
             const unsigned at = atomicAdd(&S.mine_n, 1u);
-            if (at < kList) S.mine[at] = k;
+            if (at < NTHR) S.mine[at] = k;
           }
         }
       });
@@ -344,7 +356,7 @@ struct Work {
       if (tid == 0) S.mine_n = add_u32(remote(&S.list_n, 0), m);
       __syncthreads();
       const unsigned at = S.mine_n + tid;
-      if (tid < (int)min(m, (unsigned)kList) && at < kList)
+      if (tid < (int)min(m, (unsigned)NTHR) && at < NTHR)
         st_u64(remote(&S.list_key[at], 0), S.mine[tid]);
     } else if (c.op == kMinMax) {  // of the bin's keys
       u64 lo = ~0ull, hi = 0;
@@ -362,7 +374,7 @@ struct Work {
       }
       __syncthreads();
       if (tid == 0) {
-        for (int i = 1; i < kThreads / 32; ++i) {
+        for (int i = 1; i < NTHR / 32; ++i) {
           lo = min(lo, S.red[i]);
           hi = max(hi, S.red2[i]);
         }
@@ -374,7 +386,7 @@ struct Work {
       sync();
       sum_bins(kBins, S.tot_c, S.tot_w);
     } else {  // kHist: the bin's keys in [lo, hi] by their distance to hi
-      for (int i = tid; i < kSubBins; i += kThreads) {
+      for (int i = tid; i < kSubBins; i += NTHR) {
         S.hist_c[i] = 0;
         S.hist_w[i] = make_uint2(0, 0);
       }
@@ -407,7 +419,7 @@ struct Work {
       st_u64(a + offsetof(Cmd, hi), c.hi);
     }
     if (c.op == kCollect)
-      for (unsigned i = threadIdx.x; i < (C - 1) * (kBins / 32); i += kThreads)
+      for (unsigned i = threadIdx.x; i < (C - 1) * (kBins / 32); i += NTHR)
         st_u32(remote(&S.wanted[i % (kBins / 32)], 1 + i / (kBins / 32)),
                S.wanted[i % (kBins / 32)]);
     sync();
@@ -548,10 +560,7 @@ struct Work {
     }
     if (lane == 31) S.red[warp] = x;
     __syncthreads();
-    u64 before = lane < warp ? S.red[lane] : 0;
-    if (warp > 0)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    const u64 before = warp_sum64(lane < warp ? S.red[lane] : 0);
     S.list_key[tid] = k;
     S.list_w[tid] = x + before;
     __syncthreads();
@@ -564,7 +573,8 @@ __device__ __noinline__ u64 share(double f, u64 total) {
   return max((u64)1, min(total, __double2ull_rn(t)));
 }
 
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ Params P) {
+template <int NTHR>
+__global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& S = *reinterpret_cast<Shared*>(smem);
   float* data = reinterpret_cast<float*>(smem + sizeof(Shared));
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   const int b = blockIdx.y;
   const int begin = min(P.V, (int)rank * P.slice), n = min(P.slice, P.V - begin);
   const float* row = P.logits + (long long)b * P.ld;
-  for (int i = tid; i < kBins; i += kThreads) {
+  for (int i = tid; i < kBins; i += NTHR) {
     S.hist_c[i] = 0;
     S.hist_w[i] = make_uint2(0, 0);
   }
@@ -600,17 +610,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
   };
   int i = tid;
-  for (; i + 7 * kThreads < n; i += 8 * kThreads) {
+  for (; i + 7 * NTHR < n; i += 8 * NTHR) {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __ldcg(row + begin + i + e * kThreads);
+    for (int e = 0; e < 8; ++e) v[e] = __ldcg(row + begin + i + e * NTHR);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (P.resident) data[i + e * kThreads] = v[e];
-      note(v[e], begin + i + e * kThreads);
+      if (P.resident) data[i + e * NTHR] = v[e];
+      note(v[e], begin + i + e * NTHR);
     }
   }
-  for (; i < n; i += kThreads) {
+  for (; i < n; i += NTHR) {
     const float v = __ldcg(row + begin + i);
     if (P.resident) data[i] = v;
     note(v, begin + i);
@@ -625,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   }
   __syncthreads();
   if (warp == 0) {  // to every rank
-    hi = warp_max64(lane < kThreads / 32 ? S.red[lane] : 0);
-    lo = warp_min64(lane < kThreads / 32 ? S.red2[lane] : ~0ull);
-    cnt = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? S.red3[lane] : 0);
+    hi = warp_max64(lane < NTHR / 32 ? S.red[lane] : 0);
+    lo = warp_min64(lane < NTHR / 32 ? S.red2[lane] : ~0ull);
+    cnt = __reduce_add_sync(0xffffffffu, lane < NTHR / 32 ? S.red3[lane] : 0);
     if (lane < (int)C) {
       st_u64(remote(&S.key_max[rank], lane), hi);
       st_u64(remote(&S.key_min[rank], lane), lo);
@@ -666,12 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   R.fine = R.edge > 0.f ? (float)kFine / R.edge : 0.f;
   const float rest = fminf(span, 32.f * R.edge + 64.f) - R.edge;
   R.coarse = rest > 0.f ? (float)(kBins - kFine) / rest : 0.f;
-  const Work W = {P, S, R, data, row, begin, n, rank, C};
+  const Work<NTHR> W = {P, S, R, data, row, begin, n, rank, C};
 
   // ---- histogram of counts and, unless a small top-k will do without, of
   // weights
   const double mp = min_p > 0.f ? fmin(1.0, (double)min_p) : 0.0;
-  const bool few = top_k > 0 && top_k <= kThreads / 2 && (unsigned)top_k < cnt;
+  const bool few = top_k > 0 && top_k <= NTHR / 2 && (unsigned)top_k < cnt;
   if (few)
     W.each([&](float v, int) {
       const int k = R.bin(v);
@@ -725,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     W.scan_groups(kBins);
     if (few) {
       kb = bin_at(false, kept - 1);
-      path = kb.pc + kb.c <= kThreads ? kPathFew : kPathWeigh;
+      path = kb.pc + kb.c <= NTHR ? kPathFew : kPathWeigh;
       if (path == kPathFew) want(0, kb.at);
     } else {
       path = kPathSlow;
@@ -789,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
       const Bin d1 = bin_at(true, share(ub, max(s1, (u64)1)));
       want(d0.at, d1.at);
       many += d1.pc + d1.c - d0.pc;
-      path = many <= kThreads ? kPathList : kPathSlow;
+      path = many <= NTHR ? kPathList : kPathSlow;
     }
     path = go_on(path);
     if (path == kPathList) {
@@ -844,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         Bin q = W.find_bin(kBins, S.tot_c, S.tot_w, by_weight, target);  // (every warp)
         const int bin = q.at;
         Cmd cmd = {kCollect, bin, 0, 0, ~0ull};
-        if (q.c > kThreads) {
+        if (q.c > NTHR) {
           W.ask(Cmd{kMinMax, bin, 0, 0, 0}, mp);
           cmd.lo = ~0ull;
           cmd.hi = 0;
@@ -855,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
           // the row's groups make way for the bin's and come back after it
           const unsigned keep_c = tid <= kBins / 32 ? S.sup_c[tid] : 0;
           const u64 keep_w = tid <= kBins / 32 ? S.sup_w[tid] : 0;
-          while (q.c > kThreads) {
+          while (q.c > NTHR) {
             const u64 width = cmd.hi - cmd.lo;  // keys differ: at least q.c - 1
             const int bits = 64 - __clzll((long long)width);
             const Cmd h = {kHist, bin, max(0, bits - 9), cmd.lo, cmd.hi};
@@ -917,8 +927,9 @@ inline int cluster_for(int B, int V) {
   return c;
 }
 
+template <int NTHR>
 cudaError_t launch(const Params& P, int C, int B, cudaStream_t st) {
-  const void* f = (const void*)sample_kernel;
+  const void* f = (const void*)sample_kernel<NTHR>;
   ensure_smem(f, (int)(sizeof(Shared) + kResident * 4));
   if (C > 8) {
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -926,7 +937,7 @@ cudaError_t launch(const Params& P, int C, int B, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, B);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NTHR);
   cfg.dynamicSmemBytes = sizeof(Shared) + (P.resident ? (size_t)P.slice * 4 : 0);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -939,7 +950,7 @@ cudaError_t launch(const Params& P, int C, int B, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, sample_kernel, P);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<NTHR>, P);
 }
 
 struct Pow2 {
@@ -992,7 +1003,9 @@ extern "C" qg_status qg_sample_filtered(const float* logits, long long ld, int B
   while (((unsigned long long)V << P.frac) > (1ull << 62)) --P.frac;
   for (int i = 0; i < sf::kSteps; ++i) P.pow2[i] = pow2.v[i];
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = sf::launch(P, C, B, st);
+  // a slice of a few thousand values: fewer threads, whose barriers cost less
+  // and of which an SM takes two blocks
+  const cudaError_t e = P.slice > 4096 ? sf::launch<512>(P, C, B, st) : sf::launch<256>(P, C, B, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_error("%s: CUDA launch failed: %s", who, cudaGetErrorString(e));
