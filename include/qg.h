@@ -547,7 +547,8 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  * bf16 values, q) but for the softmax weights (fp16 with int8 pages, bf16
  * with bf16 pages); sums, maxima and scales in fp32. With an fp32 q or out,
  * q and the weights are carried in several 16-bit terms (22 bits or more).
- * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0. */
+ * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0, and
+ * (T * H / 8 + B * kv_heads) * (max_pages * page_size / 128 + 1) < 2^31. */
 size_t qg_paged_attention_workspace_size(int head_dim);
 qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
                              const int32_t* kv_len, const int32_t* row_start, const void* q,

@@ -528,27 +528,35 @@ __device__ __forceinline__ float o_unit(float r) {
 }
 
 // q of the item's column tile into shared memory, a warp per column, with
-// the factor that turns a column's products into log2 units in sf.
-template <int D, bool I8, int NT, int QS>
-__device__ __forceinline__ void stage_q(const Params& P, const Item& it, uint16_t* sq, float* sf,
-                                        int warp, int warps, int lane) {
-#pragma unroll 8
-  for (int n = warp; n < NT * 8; n += warps) {
-    float x[D / 32];
-    load_q<D>(P, it, it.ct * NT * 8 + n, lane, x);
-    float unit = 1.f;
-    if constexpr (I8) {
-      float top = 0.f;
+// the factor that turns a column's products into log2 units in sf. The loads
+// go out first (take), so that they overlap the first keys' ones.
+template <int D, bool I8, int NT, int QS, int PER>
+struct StageQ {  // columns first, first + step, ... (PER of them)
+  float x[PER][D / 32];
+  __device__ __forceinline__ void take(const Params& P, const Item& it, int first, int step,
+                                       int lane) {
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(x[e]));
-      unit = q_unit(warp_max(top));
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) x[e] *= unit;
-    }
-    put_q<D, I8, NT, QS>(sq, n, lane, x);
-    if (lane == 0) sf[n] = P.scale_log2 / unit;
+    for (int i = 0; i < PER; ++i) load_q<D>(P, it, it.ct * NT * 8 + first + i * step, lane, x[i]);
   }
-}
+  __device__ __forceinline__ void put(const Params& P, uint16_t* sq, float* sf, int first, int step,
+                                      int lane) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int n = first + i * step;
+      float unit = 1.f;
+      if constexpr (I8) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        unit = q_unit(warp_max(top));
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) x[i][e] *= unit;
+      }
+      put_q<D, I8, NT, QS>(sq, n, lane, x[i]);
+      if (lane == 0) sf[n] = P.scale_log2 / unit;
+    }
+  }
+};
 
 template <int NT, class W>
 __device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w) {
@@ -577,110 +585,58 @@ __device__ __forceinline__ void store_out(const Params& P, const Item& it, int c
 
 // ------------------------------------------------------------ split kernel --
 
-// Chunks of sequence b's items (at least one, so that empty ones are
-// written) and the item count.
+// A sequence's column tiles and the chunks of each of its items (at least
+// one, so that empty ones are written). The host keeps a call's chunks below
+// 2^31.
 struct SeqWork {
   int tiles, chunks;
-  __device__ __forceinline__ long long total(int Hkv) const {
-    return (long long)tiles * Hkv * chunks;
+  __device__ __forceinline__ SeqWork(const Params& P, const Item& it, int NC) {
+    tiles = (it.n * P.G + NC - 1) / NC;
+    chunks = max(1, (it.len + kChunk - 1) / kChunk);
+  }
+  __device__ __forceinline__ unsigned total(int Hkv) const {
+    return (unsigned)tiles * Hkv * chunks;
   }
 };
-__device__ __forceinline__ SeqWork seq_work(const Params& P, int b, int NC) {
-  Item it;
-  set_seq(P, it, b);
-  SeqWork w;
-  w.tiles = (int)(((long long)it.n * P.G + NC - 1) / NC);
-  w.chunks = max(1, (it.len + kChunk - 1) / kChunk);
-  return w;
-}
-
-// Exclusive prefix over the calling block's NTHR threads of v; *total gets
-// the sum. `buf` holds NTHR / 32 values.
-template <int NTHR>
-__device__ __forceinline__ long long block_prefix(long long v, long long* buf, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) buf[warp] = x;
-  __syncthreads();
-  long long before = 0, sum = 0;
-#pragma unroll
-  for (int i = 0; i < NTHR / 32; ++i) {
-    if (i < warp) before += buf[i];
-    sum += buf[i];
-  }
-  __syncthreads();
-  *total = sum;
-  return before + x - v;
-}
 
 // The line of N chunks cut into pieces: the first `rem` have q + 1 chunks,
 // the others q.
 struct Cut {
-  long long q;
-  int rem;
-  __device__ __forceinline__ Cut(long long N, int pieces) {
-    q = N >> 31 ? N / pieces : (long long)((unsigned)N / (unsigned)pieces);
-    rem = (int)(N - q * pieces);
+  unsigned q, rem;
+  __device__ __forceinline__ Cut(unsigned N, unsigned pieces) {
+    q = N / pieces;
+    rem = N - q * pieces;
   }
-  __device__ __forceinline__ long long begin(int c) const { return q * c + min(c, rem); }
-  __device__ __forceinline__ int piece_of(long long x) const {
-    const long long wide = (q + 1) * rem;
-    const long long y = x < wide ? x : x - wide, d = x < wide ? q + 1 : q;
-    const int i = y >> 31 ? (int)(y / d) : (int)((unsigned)y / (unsigned)d);
-    return x < wide ? i : rem + i;
+  __device__ __forceinline__ unsigned begin(unsigned c) const { return q * c + min(c, rem); }
+  __device__ __forceinline__ unsigned piece_of(unsigned x) const {
+    const unsigned wide = (q + 1) * rem;
+    return x < wide ? x / (q + 1) : rem + (x - wide) / q;
   }
 };
 
-// Sequence whose chunks hold place `pos` of the line, and the place within
-// them; *N gets the line's length. For up to 32 sequences every warp finds it
-// by itself (`pos_of` gets N).
-template <int NTHR, int NC, class F>
-__device__ __forceinline__ int find_seq(const Params& P, F pos_of, long long* N, long long* rest) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (P.B <= 32) {
-    const long long mine = lane < P.B ? seq_work(P, lane, NC).total(P.Hkv) : 0;
-    long long x = mine;
+// Running sums over the sequences, 32 at a time (every warp by itself): f
+// gets a sequence (its item's n is 0 past the last one), its work, and the
+// chunks before it; returns all chunks.
+template <int NC, class F>
+__device__ __forceinline__ unsigned each_seq(const Params& P, F f) {
+  const int lane = threadIdx.x & 31;
+  unsigned before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    Item it = {0, 0, 0, 0, 0, 0};
+    if (b0 + lane < P.B) set_seq(P, it, b0 + lane);
+    const SeqWork w(P, it, NC);
+    const unsigned mine = w.total(P.Hkv);
+    unsigned x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    *N = __shfl_sync(0xffffffffu, x, 31);
-    const long long pos = pos_of(*N);
-    const unsigned m = __ballot_sync(0xffffffffu, pos < x);
-    const int b = m ? __ffs(m) - 1 : 0;
-    *rest = pos - __shfl_sync(0xffffffffu, x - mine, b);
-    return b;
+    f(it, w, before + x - mine, mine);
+    before += __shfl_sync(0xffffffffu, x, 31);
   }
-  __shared__ long long buf[NTHR / 32], s_rest;
-  __shared__ int s_b;
-  const int per = (P.B + NTHR - 1) / NTHR;
-  long long mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < P.B) mine += seq_work(P, b, NC).total(P.Hkv);
-  }
-  const long long before = block_prefix<NTHR>(mine, buf, N);
-  const long long pos = pos_of(*N);
-  if (pos >= before && pos < before + mine) {
-    long long r = pos - before;
-    int b = tid * per;
-    for (;; ++b) {
-      const long long w = seq_work(P, b, NC).total(P.Hkv);
-      if (r < w) break;
-      r -= w;
-    }
-    s_b = b;
-    s_rest = r;
-  }
-  __syncthreads();
-  *rest = s_rest;
-  return s_b;
+  return before;
 }
 
 template <int D, bool I8, int NT, int QS, int PS>
@@ -697,35 +653,63 @@ split_kernel(const __grid_constant__ Params P) {
   pdl_wait();
   pdl_trigger();  // the merge may find its items meanwhile
 
-  long long N, pos = 0, stop = 0, rest;
-  const int b0 = find_seq<kWarps * 32, NC>(
-      P,
-      [&](long long n) {
-        const Cut cut(n, P.pieces);
-        pos = cut.begin(blockIdx.x);
-        stop = cut.begin(blockIdx.x + 1);
-        return pos;
-      },
-      &N, &rest);
-  if (pos >= stop) return;
-  Item it;
-  set_seq(P, it, b0);
-  SeqWork w = seq_work(P, b0, NC);
+  // This CTA's piece [pos, stop) of the line, and the item where it begins.
+  // Up to 32 sequences: one look at them tells both; more: a first look for
+  // the line's length, a second for the place.
+  Item it = {0, 0, 0, 0, 0, 0};
+  unsigned pos = 0, stop = 0, rest = 0;
+  const auto piece = [&](unsigned N) {
+    const Cut cut(N, P.pieces);
+    pos = cut.begin(blockIdx.x);
+    stop = cut.begin(blockIdx.x + 1);
+  };
+  const auto settle = [&](const Item& mine, unsigned before, unsigned len) {
+    const unsigned m = __ballot_sync(0xffffffffu, pos >= before && pos - before < len);
+    if (!m) return;
+    const int l = __ffs(m) - 1;
+    it.b = __shfl_sync(0xffffffffu, mine.b, l);
+    it.r0 = __shfl_sync(0xffffffffu, mine.r0, l);
+    it.n = __shfl_sync(0xffffffffu, mine.n, l);
+    it.len = __shfl_sync(0xffffffffu, mine.len, l);
+    rest = pos - __shfl_sync(0xffffffffu, before, l);
+  };
+  if (P.B <= 32) {
+    Item mine;
+    unsigned before, len;
+    piece(each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
+      mine = i;
+      before = b;
+      len = l;
+    }));
+    if (pos >= stop) return;
+    settle(mine, before, len);
+  } else {
+    piece(each_seq<NC>(P, [](const Item&, const SeqWork&, unsigned, unsigned) {}));
+    if (pos >= stop) return;
+    each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
+      settle(i, b, l);
+    });
+  }
+  SeqWork w(P, it, NC);
   // (head, column tile) of the sequence, and the item's first chunk here
-  int unit = rest >> 31 ? (int)(rest / w.chunks) : (int)((unsigned)rest / (unsigned)w.chunks);
-  int c0 = (int)(rest - (long long)unit * w.chunks);
+  int unit = (int)(rest / (unsigned)w.chunks);
+  int c0 = (int)rest - unit * w.chunks;
+  it.h = unit / w.tiles;
+  it.ct = unit - it.h * w.tiles;
 
   Walk<D, I8, NT, QS, PS> walk(P, lane);
+  StageQ<D, I8, NT, QS, NT * 8 / kWarps> qs;
   walk.sq = sq;
   State<D, NT> S;
-  while (pos < stop) {
-    it.h = unit / w.tiles;
-    it.ct = unit - it.h * w.tiles;
-    const int c1 = (int)min((long long)w.chunks, c0 + (stop - pos));
-    walk.len = it.len;
-    walk.begin(it, c0 * kWarps + warp, kWarps,
-               min(c1 * kWarps, (it.len + kBlock - 1) / kBlock));
-    stage_q<D, I8, NT, QS>(P, it, sq, sf, warp, kWarps, lane);
+  const auto start = [&](const Item& i, int first, int last) {  // chunks [first, last)
+    qs.take(P, i, warp, kWarps, lane);
+    walk.len = i.len;
+    walk.begin(i, first * kWarps + warp, kWarps, min(last * kWarps, (i.len + kBlock - 1) / kBlock));
+  };
+  int c1 = (int)min((unsigned)w.chunks, c0 + (stop - pos));
+  start(it, c0, c1);
+  for (;;) {
+    qs.put(P, sq, sf, warp, kWarps, lane);
     set_limits<NT>(P, it, walk);
     __syncthreads();
 #pragma unroll
@@ -735,9 +719,29 @@ split_kernel(const __grid_constant__ Params P) {
     }
     S.clear();
     walk.run(S, it);
+    // the next item's first keys and q go out before this one is put away
+    const Item cur = it;
+    const bool first_part = c0 == 0, whole = c0 == 0 && c1 == w.chunks;
+    pos += c1 - c0;
+    const bool more = pos < stop;
+    if (more) {
+      if (++unit == w.tiles * P.Hkv) {
+        unit = 0;
+        do {  // the next sequence with rows (one exists: chunks are left)
+          if (it.b + 1 >= P.B) return;  // (unless row starts decrease)
+          set_seq(P, it, it.b + 1);
+        } while (it.n == 0);
+        w = SeqWork(P, it, NC);
+      }
+      it.h = unit / w.tiles;
+      it.ct = unit - it.h * w.tiles;
+      c0 = 0;
+      c1 = (int)min((unsigned)w.chunks, stop - pos);
+      start(it, c0, c1);
+    }
     // the warps' states to shared memory: weights summed over the lanes that
     // share a column, outputs in plain units
-    const int cols = min(NC, it.n * P.G - it.ct * NC);  // of the tile, real ones
+    const int cols = min(NC, cur.n * P.G - cur.ct * NC);  // of the tile, real ones
     const float u = o_unit<I8>(S.r);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -761,8 +765,7 @@ split_kernel(const __grid_constant__ Params P) {
       }
     }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == w.chunks;
-    float* part = P.part + (long long)(2 * blockIdx.x + (c0 == 0)) * NC * (D + 2);
+    float* part = P.part + (long long)(2 * blockIdx.x + first_part) * NC * (D + 2);
     for (int i = tid; i < cols * D; i += kWarps * 32) {
       const int n = i / D, d = i % D;
       float M = sm[n];
@@ -776,7 +779,7 @@ split_kernel(const __grid_constant__ Params P) {
         O = fmaf(a, so[(k * NC + n) * D + d], O);
       }
       if (whole) {
-        store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+        store_out(P, cur, cur.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
       } else {
         part[2 * NC + i] = O;
         if (d == 0) {
@@ -785,18 +788,7 @@ split_kernel(const __grid_constant__ Params P) {
         }
       }
     }
-    pos += c1 - c0;
-    c0 = 0;
-    if (pos < stop) {
-      __syncthreads();  // shared memory is used again
-      if (++unit == w.tiles * P.Hkv) {
-        unit = 0;
-        do {  // the next sequence with rows (one exists: chunks are left)
-          set_seq(P, it, it.b + 1);
-          w = seq_work(P, it.b, NC);
-        } while (w.tiles == 0);
-      }
-    }
+    if (!more) return;
   }
 }
 
@@ -808,53 +800,33 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   constexpr int NC = NT * 8;
   __shared__ float sw[NC][kMaxPieces];  // pieces' factors
   __shared__ float acc[kMergeThreads];
-  __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (the split kernel's CTAs have passed their own wait, so what came before
   // it on the stream is complete: lengths and row starts may be read)
   const int u = blockIdx.x;
-  if (tid == 0) s_b = -1;
-  __syncthreads();
-  for (int i = tid; i < P.B; i += kMergeThreads) {
-    const long long lo = (long long)row_begin(P.row_start, i, P.T) * P.G / NC + i;
-    const long long hi = (long long)row_begin(P.row_start, i + 1, P.T) * P.G / NC + i + 1;
-    if (lo <= u && u < hi) s_b = i;
-  }
-  __syncthreads();
-  if (s_b < 0) return;
-  Item it;
-  set_seq(P, it, s_b);
-  const SeqWork w = seq_work(P, s_b, NC);
-  it.ct = u - (int)((long long)it.r0 * P.G / NC + s_b);
+  Item it = {-1, 0, 0, 0, 0, 0};
+  unsigned before = 0;
+  const unsigned N = each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned) {
+    const int end = i.r0 + i.n;
+    const bool in = i.n && u >= (int)((long long)i.r0 * P.G / NC + i.b) &&
+                    u <= (int)((long long)end * P.G / NC + i.b);
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (!m) return;
+    const int l = __ffs(m) - 1;
+    it.b = __shfl_sync(0xffffffffu, i.b, l);
+    it.r0 = __shfl_sync(0xffffffffu, i.r0, l);
+    it.n = __shfl_sync(0xffffffffu, i.n, l);
+    it.len = __shfl_sync(0xffffffffu, i.len, l);
+    before = __shfl_sync(0xffffffffu, b, l);
+  });
+  if (it.b < 0) return;
+  const SeqWork w(P, it, NC);
+  it.ct = u - (int)((long long)it.r0 * P.G / NC + it.b);
   it.h = blockIdx.y;
   if (it.ct >= w.tiles) return;
-  // chunks before the sequence, and the line's length
-  long long before = 0, N = 0;
-  for (int i = tid; i < P.B; i += kMergeThreads) {
-    const long long c = seq_work(P, i, NC).total(P.Hkv);
-    N += c;
-    before += i < s_b ? c : 0;
-  }
-  __shared__ long long r_n[kMergeThreads / 32], r_b[kMergeThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    N += __shfl_xor_sync(0xffffffffu, N, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    r_n[warp] = N;
-    r_b[warp] = before;
-  }
-  __syncthreads();
-  N = before = 0;
-#pragma unroll
-  for (int i = 0; i < kMergeThreads / 32; ++i) {
-    N += r_n[i];
-    before += r_b[i];
-  }
-  const long long begin = before + (long long)(it.h * w.tiles + it.ct) * w.chunks;
+  const unsigned begin = before + (unsigned)(it.h * w.tiles + it.ct) * w.chunks;
   const Cut cut(N, P.pieces);
-  const int p0 = cut.piece_of(begin), p1 = cut.piece_of(begin + w.chunks - 1);
+  const int p0 = (int)cut.piece_of(begin), p1 = (int)cut.piece_of(begin + w.chunks - 1);
   if (p0 == p1) return;  // written by its piece
   pdl_wait();
   const int np = p1 - p0 + 1, cols = min(NC, it.n * P.G - it.ct * NC);
@@ -938,7 +910,12 @@ __global__ void __launch_bounds__(kWholeWarps * 32) whole_kernel(const __grid_co
   const int last = min(it.n - 1, (it.ct * NC + NC - 1) / P.G);
   const int keys = it.len ? it.len - it.n + last + 1 : 0;
   walk.begin(it, 0, 1, (keys + kBlock - 1) / kBlock);
-  stage_q<D, I8, NT, QS>(P, it, sq, sf[warp], 0, 1, lane);
+#pragma unroll 1
+  for (int n = 0; n < NC; n += 8) {
+    StageQ<D, I8, NT, QS, 8> qs;
+    qs.take(P, it, n, 1, lane);
+    qs.put(P, sq, sf[warp], n, 1, lane);
+  }
   set_limits<NT>(P, it, walk);
   __syncwarp();
 #pragma unroll
@@ -1015,6 +992,7 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, long long cap, bool exact)
   const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
   const long long items = ((long long)T * G / (8 * nt) + B) * Hkv;
   const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
+  if (items > 0x7FFFFFFFLL / chunks) return {0, -1};  // the line has 31 bits
   const long long most =
       std::min((long long)kMaxPieces, (long long)num_sms() * (nt == 1 && D <= 128 ? 2 : 1));
   return {nt, (int)std::max(1LL, std::min(most, items * chunks))};
@@ -1087,6 +1065,9 @@ extern "C" qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* pa
   const bool exact = q_dtype == QG_F32 || out_dtype == QG_F32;
   const pa::Plan plan =
       pa::plan(B, T, H, Hkv, D, (long long)max_pages * kv->page_size, exact);
+  QG_REQUIRE(plan.pieces >= 0, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d rows of H=%d heads over max_pages=%d pages are too many for one call", who,
+             T, H, max_pages);
   pa::Params P = {};
   P.q = q;
   P.out = out;
