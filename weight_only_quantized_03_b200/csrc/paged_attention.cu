@@ -42,11 +42,12 @@
 // piece's tiles in turn and merge in shared memory. An item inside one piece
 // is written out; the others' parts go to the workspace and a second small
 // launch merges them in order (results do not depend on scheduling).
-// Kernel "whole" (long prompts): a warp takes 32 columns over all their keys.
+// Prompts with a bf16 q and out go to the tcgen05 kernel of
+// paged_attention_tc.cu.
 #include <cuda_fp16.h>
 
 #include "mma_sync.cuh"
-#include "paged_kv.cuh"
+#include "paged_attention.cuh"
 
 #include <algorithm>
 #include <cfloat>
@@ -55,39 +56,11 @@
 namespace qg {
 namespace pa {
 
-using pk::kBlock;
-using pk::row_begin;
-
 constexpr int kWarps = 8;            // split kernel
 constexpr int kChunk = kWarps * kBlock;
-constexpr int kWholeWarps = 4;       // whole kernel
-constexpr int kWholeNT = 4;
 constexpr int kMergeThreads = 512;
 constexpr int kMaxPieces = 320;      // of the split kernel (two CTAs on each of 148 SMs)
-constexpr float kMargin = 4.f;       // log2 of how far a weight may pass 1
 
-struct Params {
-  const void* q;
-  void* out;
-  const uint8_t* kp;
-  const uint8_t* vp;
-  const float* ks;
-  const float* vs;
-  const int32_t* table;
-  const int32_t* kv_len;
-  const int32_t* row_start;
-  float* part;  // [2 * pieces][NC * (D + 2)]
-  int q_bf16, out_bf16;
-  int B, T, H, Hkv, G, bpp, max_pages, num_pages;  // bpp: blocks of 16 tokens per page
-  int pieces;
-  float scale_log2;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -127,21 +100,6 @@ __device__ __forceinline__ uint32_t take16(float& lo, float& hi) {
 }
 __device__ __forceinline__ uint4 ldcg16(const uint8_t* p) {
   return __ldcg(reinterpret_cast<const uint4*>(p));
-}
-
-// One (sequence, KV head, column tile) item.
-struct Item {
-  int b, h, ct;   // sequence, KV head, column tile
-  int r0, n;      // the sequence's first packed row and rows
-  int len;        // cached tokens, 0 for a length out of range
-};
-
-__device__ __forceinline__ void set_seq(const Params& P, Item& it, int b) {
-  it.b = b;
-  it.r0 = row_begin(P.row_start, b, P.T);
-  it.n = max(0, row_begin(P.row_start, b + 1, P.T) - it.r0);
-  const int len = __ldcg(P.kv_len + b);
-  it.len = len >= it.n && (long long)len <= (long long)P.max_pages * P.bpp * kBlock ? len : 0;
 }
 
 // Visible tokens of column c of the item's sequence. Columns past the last
@@ -201,13 +159,6 @@ __device__ __forceinline__ void put_q(uint16_t* sq, int n, int lane, float (&x)[
     for (int e = 0; e < D / 32; e += 2)
       *reinterpret_cast<uint32_t*>(sq + q_at<I8, NT, QS>(n, lane * (D / 32) + e, s)) =
           take16<I8>(x[e], x[e + 1]);
-}
-
-// 2^e that brings the largest |q| into [2^13, 2^14) (int8 pages).
-__device__ __forceinline__ float q_unit(float top) {
-  const int ex = (__float_as_int(top) >> 23) & 255;  // 0: zero or subnormal, 255: not finite
-  if (ex == 0 || ex == 255) return 1.f;
-  return __int_as_float(min(254, max(1, 127 + 13 - (ex - 127))) << 23);
 }
 
 // A warp's running state over the columns of its item.
@@ -878,87 +829,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
 }
 
-// ------------------------------------------------------------ whole kernel --
-
-template <int D, bool I8, int QS, int PS>
-__global__ void __launch_bounds__(kWholeWarps * 32) whole_kernel(const __grid_constant__ Params P) {
-  constexpr int NT = kWholeNT, NC = NT * 8;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint16_t* sq = reinterpret_cast<uint16_t*>(smem) + warp * (NC * D * QS);
-  __shared__ float sf[kWholeWarps][NC];
-  pdl_wait();
-  pdl_trigger();
-  // later column tiles see more keys: they go first
-  const long long u = (long long)(gridDim.x - 1 - blockIdx.x) * kWholeWarps + warp;
-  int b = -1;
-  for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
-    const int i = i0 + lane;
-    bool in = false;
-    if (i < P.B) {
-      const long long lo = (long long)row_begin(P.row_start, i, P.T) * P.G / NC + i;
-      const long long hi = (long long)row_begin(P.row_start, i + 1, P.T) * P.G / NC + i + 1;
-      in = lo <= u && u < hi;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    if (m) b = i0 + __ffs(m) - 1;
-  }
-  if (b < 0) return;
-  Item it;
-  set_seq(P, it, b);
-  it.ct = (int)(u - ((long long)it.r0 * P.G / NC + b));
-  it.h = blockIdx.y;
-  if ((long long)it.ct * NC >= (long long)it.n * P.G) return;
-  Walk<D, I8, NT, QS, PS> walk(P, lane);
-  walk.sq = sq;
-  walk.len = it.len;
-  // keys of the tile's last row
-  const int last = min(it.n - 1, (it.ct * NC + NC - 1) / P.G);
-  const int keys = it.len ? it.len - it.n + last + 1 : 0;
-  walk.begin(it, 0, 1, (keys + kBlock - 1) / kBlock);
-#pragma unroll 1
-  for (int n = 0; n < NC; n += 8) {
-    StageQ<D, I8, NT, QS, 8> qs;
-    qs.take(P, it, n, 1, lane);
-    qs.put(P, sq, sf[warp], n, 1, lane);
-  }
-  set_limits<NT>(P, it, walk);
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    walk.qf[j][0] = sf[warp][j * 8 + 2 * walk.t];
-    walk.qf[j][1] = sf[warp][j * 8 + 2 * walk.t + 1];
-  }
-  State<D, NT> S;
-  S.clear();
-  walk.run(S, it);
-  const float un = o_unit<I8>(S.r);
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = S.l[j][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const float a = l != 0.f ? un / l : 0.f;
-      const int c = it.ct * NC + j * 8 + 2 * walk.t + e, i = c / P.G;
-      if (i >= it.n) continue;
-      const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D +
-                           walk.g * (D / 8);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const float x = S.o[k][j][e] * a, y = S.o[k][j][2 + e] * a;
-        if (P.out_bf16)
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(P.out) + at + 2 * k) =
-              mm::pack_bf16(x, y);
-        else
-          *reinterpret_cast<float2*>(reinterpret_cast<float*>(P.out) + at + 2 * k) =
-              make_float2(x, y);
-      }
-    }
-}
-
 // ---------------------------------------------------------------- launches --
 
 template <int D, bool I8, int NT, int QS, int PS>
@@ -977,27 +847,14 @@ cudaError_t launch_split(const Params& P, cudaStream_t st) {
                     st, true, P);
 }
 
-template <int D, bool I8, int QS, int PS>
-cudaError_t launch_whole(const Params& P, cudaStream_t st) {
-  constexpr int NC = kWholeNT * 8;
-  const size_t smem = (size_t)kWholeWarps * NC * D * QS * 2;
-  ensure_smem((const void*)whole_kernel<D, I8, QS, PS>, (int)smem);
-  const long long slots = (long long)P.T * P.G / NC + P.B;
-  return launch_pdl(whole_kernel<D, I8, QS, PS>,
-                    dim3((unsigned)((slots + kWholeWarps - 1) / kWholeWarps), P.Hkv),
-                    dim3(kWholeWarps * 32), smem, st, true, P);
-}
-
-// How a call runs: columns per tile, pieces of the split kernel (0: the
-// whole kernel).
+// How a call runs: column tiles of 8 side by side, pieces of the split kernel
+// (0: the prompt kernel).
 struct Plan {
   int nt, pieces;
 };
 inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bool exact) {
   const long long G = H / Hkv;
-  // a warp per 32 columns needs enough of them to fill the GPU
-  const long long warps = ((long long)T * G / 32 + B) * Hkv;
-  if (D <= 128 && !exact && T * G >= 16LL * B && warps >= 4LL * num_sms()) return {kWholeNT, 0};
+  if (D <= 128 && !exact && T * G >= 32LL * B) return {0, 0};
   const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
   const long long items = ((long long)T * G / (8 * nt) + B) * Hkv;
   const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
@@ -1012,7 +869,7 @@ cudaError_t launch(const Params& P, const Plan& p, bool exact, cudaStream_t st) 
   constexpr int E = I8 ? 2 : 3;  // terms of fp32 q and weights
   if (exact) return launch_split<D, I8, 1, E, E>(P, st);
   if constexpr (D <= 128) {
-    if (p.pieces == 0) return launch_whole<D, I8, 1, 1>(P, st);
+    if (p.pieces == 0) return launch_prompt(P, D, I8, st);
     if (p.nt == 2) return launch_split<D, I8, 2, 1, 1>(P, st);
   }
   return launch_split<D, I8, 1, 1, 1>(P, st);

@@ -1,0 +1,608 @@
+// Prompt rows over a paged K/V cache on the tcgen05 tensor cores
+// (include/qg.h, qg_paged_attention; the other kernels and the units of the
+// int8 operands: paged_attention.cu).
+//
+// A CTA takes 128 (row, query head) pairs of one KV head of one sequence and
+// walks their keys 64 at a time: S = Q K^T and O += P V are tcgen05.mma with
+// M = 128, accumulators in tensor memory (O: head_dim columns, S: two buffers
+// of 64). Warps 4-7 bring K and V from the pages: int8 codes become fp16
+// (exact) on the way into shared memory, in the 128-byte swizzled layout, K
+// as the K-major operand and V, in the same [token][dim] order, as the
+// MN-major one. Warps 0-3 own a row a thread: no maximum or sum crosses
+// threads. They read S, form the weights with the lazy maximum of the decode
+// kernel and write them as 16-bit pairs over S, where the second product
+// reads them as its A operand. One thread of warp 8 issues the products; S of
+// the next keys is in flight while the rows work on the current ones.
+//
+// 96 KB of shared memory and 256 tensor-memory columns at head size 128, so
+// that an SM holds two CTAs and one's softmax meets the other's products.
+// What bounds it: a 64-key step is 640 cycles of tensor core (S reads both
+// operands from shared memory, 6 KB per 16 dims), and about 700 issue slots
+// per scheduler for two CTAs' conversions and weights. 128 keys a step at one
+// CTA an SM would halve S's operand reads, but leave each phase's waits bare.
+//
+// A value of V that is infinite or NaN at a token that some of the rows do
+// not see must not reach them as 0 * inf: it is taken out of the operand and
+// added at the end to the rows that see it (bf16 pages; under an int8 block's
+// NaN scale the weights of rows that do not see it are exact zeros and the
+// codes are finite).
+//
+// Every wait is bounded (1 s). One that gives up ends the CTA's work; its
+// rows are then NaN.
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "mma_sync.cuh"
+#include "paged_attention.cuh"
+#include "tcgen05_util.cuh"
+
+namespace qg {
+namespace pa {
+
+using namespace tc;
+
+constexpr int kRows = 128;         // rows of a CTA
+constexpr int kKeys = 64;          // keys of a step
+constexpr int kPThreads = 288;     // 4 softmax warps, 4 loading warps, the issuing warp
+constexpr int kOdd = 32;           // V values that are not finite, kept aside
+constexpr int kTmemCols = 256;
+constexpr int kScol = 128;         // S buffers at columns 128 and 192; O at 0
+
+template <int D>
+struct PromptSmem {
+  static constexpr int kQ = kRows * D * 2, kKV = kKeys * D * 2;
+  static constexpr int kBytes = 1024 + kQ + 4 * kKV + 1024;
+};
+
+struct PromptShared {  // behind the operands
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
+  float scale[4][8];   // ring: a step's K and V scales (4 blocks of 16 tokens each)
+  uint32_t tmem;
+  int abort;
+  int odd_n, odd_from;  // entries below; the first token of one that found no room
+  int odd_key[kOdd], odd_dim[kOdd];
+  float odd_val[kOdd];
+};
+
+#define QG_R8(a, i) "r"((a)[i]), "r"((a)[i + 1]), "r"((a)[i + 2]), "r"((a)[i + 3]), \
+                    "r"((a)[i + 4]), "r"((a)[i + 5]), "r"((a)[i + 6]), "r"((a)[i + 7])
+#define QG_W8(a, i) "=r"((a)[i]), "=r"((a)[i + 1]), "=r"((a)[i + 2]), "=r"((a)[i + 3]), \
+                    "=r"((a)[i + 4]), "=r"((a)[i + 5]), "=r"((a)[i + 6]), "=r"((a)[i + 7])
+
+// 32 or 64 columns of the warp's 32 lanes, a register each. The load and the
+// wait for it are one statement: the compiler may move or spill the registers
+// of a load that has not been waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31},"
+      " [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : QG_W8(v, 0), QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,"
+      "%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,"
+      "%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : QG_W8(v, 0), QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24), QG_W8(v, 32), QG_W8(v, 40),
+        QG_W8(v, 48), QG_W8(v, 56)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      QG_R8(v, 0), QG_R8(v, 8), QG_R8(v, 16), QG_R8(v, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+// Shared-memory writes visible to the tensor core.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// MN-major operand, 128-byte swizzle: 64 neighbouring dims of a token are a
+// 128-byte row, 8 tokens a 1024-byte group (SBO between groups), the next 64
+// dims a panel further (LBO).
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(panel >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint32_t kBisMnMajor = 1u << 16;  // instruction descriptor: B is MN-major
+
+// Byte offset of 16-byte chunk c (8 dims) of a row in panels of 64 dims.
+template <int ROWS>
+__device__ __forceinline__ int at_chunk(int row, int c) {
+  return (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_constant__ Params P) {
+  using L = PromptSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sq = smem;
+  uint8_t* sk = sq + L::kQ;        // [2]
+  uint8_t* sv = sk + 2 * L::kKV;   // [2]
+  PromptShared& S = *reinterpret_cast<PromptShared*>(sv + 2 * L::kKV);
+  volatile int* abort = &S.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+
+  // The tile: slots as in the other kernels; the last ones (more keys) first.
+  const long long u = gridDim.x - 1 - blockIdx.x;
+  Item it = {-1, 0, 0, 0, 0, 0};
+#pragma unroll 1
+  for (int b0 = 0; b0 < P.B && it.b < 0; b0 += 32) {
+    Item mine = {-1, 0, 0, 0, 0, 0};
+    bool in = false;
+    if (b0 + lane < P.B) {
+      set_seq(P, mine, b0 + lane);
+      in = mine.n && u >= (long long)mine.r0 * P.G / kRows + mine.b &&
+           u <= (long long)(mine.r0 + mine.n) * P.G / kRows + mine.b;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      it.b = __shfl_sync(0xffffffffu, mine.b, l);
+      it.r0 = __shfl_sync(0xffffffffu, mine.r0, l);
+      it.n = __shfl_sync(0xffffffffu, mine.n, l);
+      it.len = __shfl_sync(0xffffffffu, mine.len, l);
+    }
+  }
+  if (it.b < 0) return;
+  it.ct = (int)(u - ((long long)it.r0 * P.G / kRows + it.b));
+  it.h = blockIdx.y;
+  const int first = it.ct * kRows, cols = it.n * P.G;  // (row, head) pairs of the sequence
+  if (first >= cols) return;
+  const int before = it.len - it.n;  // tokens cached before the rows
+  // tokens that the last pair sees, and that all pairs see
+  const int keys = it.len ? before + (min(first + kRows, cols) - 1) / P.G + 1 : 0;
+  const int common = before + first / P.G + 1;
+  const int steps = (keys + kKeys - 1) / kKeys;
+
+  // softmax threads: their pair's place in q and out
+  const int c = first + tid, ri = c / P.G;
+  const bool real = tid < kRows && c < cols;
+  const long long at =
+      ((long long)(it.r0 + (real ? ri : 0)) * P.H + it.h * P.G + (real ? c - ri * P.G : 0)) * D;
+  uint16_t* out = reinterpret_cast<uint16_t*>(P.out) + at;
+  if (steps == 0) {
+    if (real)
+      for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+
+  if (tid == 0) {
+    mbar_init(&S.q_full, kRows);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 128);
+      mbar_init(&S.v_full[i], 128);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], kRows);
+    }
+    mbar_init(&S.o_full, 1);
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    S.odd_n = 0;
+    S.odd_from = INT_MAX;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&S.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = S.tmem;
+  bool ok = true;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ the rows
+    const int lim = real ? before + ri + 1 : INT_MAX;  // tokens the pair sees
+    float qf = P.scale_log2;
+    {  // q into shared memory, for int8 pages times a power of two, as fp16
+      uint32_t w[D / 2];
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(P.q) + at;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = real ? __ldcg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      if constexpr (I8) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        const float unit = q_unit(top);
+        qf /= unit;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) {
+          const __half2 h = __floats2half2_rn(bf16_lo(w[i]) * unit, bf16_hi(w[i]) * unit);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(tid, i)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    fence_async();
+    mbar_arrive(&S.q_full);
+
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    float m = -FLT_MAX, l = 0.f, r = FLT_MIN;
+    for (int j = 0; j < steps; ++j) {
+      const int b = j & 1;
+      if (!wait_bar(&S.s_full[b], (uint32_t)(j >> 1) & 1u, abort)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      uint32_t s[64];
+      const uint32_t sc = lanes + kScol + 64 * b;
+      tmem_ld64(sc, s);
+      float ks[4], vs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ks[i] = S.scale[j & 3][i] * qf;
+        vs[i] = I8 ? S.scale[j & 3][4 + i] : 1.f;
+      }
+      const bool part = j * kKeys + kKeys > common;
+      const int left = lim - j * kKeys;  // visible tokens of this step (or more, or none)
+      float top = -FLT_MAX;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        float x = __uint_as_float(s[i]) * ks[i >> 4];
+        if (part && i >= left) x = -INFINITY;
+        s[i] = __float_as_uint(x);
+        top = fmaxf(top, x);
+      }
+      float vtop = 0.f;
+      if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (fabsf(vs[i]) <= FLT_MAX) vtop = fmaxf(vtop, fabsf(vs[i]));
+      }
+      const bool wider = I8 && vtop > r;  // the same in all threads
+      // Every warp waits for every product once, in order (a parity tells a
+      // phase only from its neighbours): here if O has to be rescaled, else at
+      // the end of the step, when it has long been done.
+      bool waited = j == 0;
+      if (__any_sync(0xffffffffu, top > m + kMargin) || wider) {
+        float a = 1.f;
+        if (wider) {
+          const float n =
+              __int_as_float(min(254, ((__float_as_int(vtop) >> 23) & 255) + 1) << 23);
+          a = r / n;
+          r = n;
+        }
+        const float x = fmaxf(m, top), e = ex2(m - x);
+        m = x;
+        l *= e;
+        a *= e;
+        if (j > 0) {  // O is whole up to the step before: rescale it
+          if (!wait_bar(&S.o_full, (uint32_t)(j - 1) & 1u, abort)) {
+            ok = false;
+            break;
+          }
+          waited = true;
+          fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + d, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st32(lanes + d, o);
+          }
+        }
+      }
+      float wv[4];
+      const float inv = I8 ? 2048.f / r : 1.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wv[i] = I8 ? vs[i] * inv : 1.f;
+      uint32_t p[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[e] = ex2(__uint_as_float(s[i + e]) - m);
+          l += y[e];
+          if constexpr (I8) {
+            y[e] *= wv[i >> 4];
+            if (part && i + e >= left) y[e] = 0.f;  // (whatever the block's scale is)
+          }
+        }
+        if constexpr (I8) {
+          const __half2 h = __floats2half2_rn(y[0], y[1]);
+          p[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          p[i / 2] = mm::pack_bf16(y[0], y[1]);
+        }
+      }
+      tmem_st32(sc, p);
+      if (!waited && !wait_bar(&S.o_full, (uint32_t)(j - 1) & 1u, abort)) {
+        ok = false;
+        break;
+      }
+      tmem_wait_st();
+      fence_before();
+      mbar_arrive(&S.p_full[b]);
+    }
+    if (ok && !wait_bar(&S.o_full, (uint32_t)(steps - 1) & 1u, abort)) ok = false;
+    if (!ok) *abort = 1;
+    fence_after();
+    const float f = l != 0.f ? (I8 ? r * (1.f / 2048.f) : 1.f) / l : 0.f;
+    const int odd = min(S.odd_n, kOdd);
+    const bool lost = !ok || lim > S.odd_from;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 32) {
+      uint32_t o[32];
+      tmem_ld32(lanes + d, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float x = __uint_as_float(o[i]) * f;
+        if (!I8)
+          for (int k = 0; k < odd; ++k)
+            if (S.odd_dim[k] == d + i && S.odd_key[k] < lim) x += S.odd_val[k];
+        o[i] = __float_as_uint(lost ? __int_as_float(0x7FC00000) : x);
+      }
+      if (real)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint4 w;
+          w.x = mm::pack_bf16(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
+          w.y = mm::pack_bf16(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+          w.z = mm::pack_bf16(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
+          w.w = mm::pack_bf16(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
+          *reinterpret_cast<uint4*>(out + d + i) = w;
+        }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ the pages
+    constexpr int ES = I8 ? 1 : 2, CPR = D * ES / 16;  // 16-byte chunks of a row
+    constexpr int R = kKeys * CPR / 128;               // chunks of a thread
+    const int t = tid - 128;
+    int ids = -2;  // lanes 0-3: the step's blocks in the pool (-1: bad page, -2: past the keys)
+    auto lookup = [&](int j) {
+      ids = -2;
+      const int blk = j * 4 + lane;
+      if (lane < 4 && blk * kBlock < keys) {
+        const int pi = blk / P.bpp;
+        const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
+        ids = page >= 0 && page < P.num_pages
+                  ? (page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)
+                  : -1;
+      }
+    };
+    auto load = [&](const uint8_t* pool, uint4 (&x)[R], int id, int j, bool v) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int ch = i * 128 + t, row = ch / CPR;
+        const int blk = __shfl_sync(0xffffffffu, id, row / kBlock);  // (the same in the warp)
+        const bool in = blk >= 0 && (I8 || !v || j * kKeys + row < it.len);
+        x[i] = in ? __ldcg(reinterpret_cast<const uint4*>(
+                        pool + (long long)blk * (kBlock * D * ES) + (ch % (kBlock * CPR)) * 16))
+                  : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store = [&](uint8_t* dst, const uint4 (&x)[R]) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int ch = i * 128 + t, row = ch / CPR, cc = ch % CPR;
+        if constexpr (I8) {
+          const uint32_t w[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u,
+                                 x[i].w ^ 0x80808080u};
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc)) =
+              make_uint4(codes01(w[0]), codes23(w[0]), codes01(w[1]), codes23(w[1]));
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc + 1)) =
+              make_uint4(codes01(w[2]), codes23(w[2]), codes01(w[3]), codes23(w[3]));
+        } else {
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, cc)) = x[i];
+        }
+      }
+    };
+    // bf16: values of V that are not finite out of the operand, aside
+    auto set_aside = [&](uint4 (&x)[R], int j) {
+#pragma unroll 1
+      for (int i = 0; i < R; ++i) {
+        const int ch = i * 128 + t, key = j * kKeys + ch / CPR, d0 = ch % CPR * 8;
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (q == i) {
+            w[0] = x[q].x;
+            w[1] = x[q].y;
+            w[2] = x[q].z;
+            w[3] = x[q].w;
+          }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t bits = e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
+          if ((bits & 0x7F800000u) != 0x7F800000u) continue;
+          w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+          const int k = atomicAdd(&S.odd_n, 1);
+          if (k < kOdd) {
+            S.odd_key[k] = key;
+            S.odd_dim[k] = d0 + e;
+            S.odd_val[k] = __uint_as_float(bits);
+          } else {
+            atomicMin(&S.odd_from, key);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (q == i) x[q] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    };
+    uint4 kx[R], vx[R];
+    float s_k, s_v;
+    auto scales = [&](int id) {  // lanes 0-3 of the first loading warp
+      s_k = id == -1 ? __int_as_float(0x7FC00000) : 1.f;
+      s_v = 1.f;
+      if (I8 && t < 4 && id >= 0) {
+        s_k = __ldcg(P.ks + id);
+        s_v = __ldcg(P.vs + id);
+      }
+    };
+    lookup(0);
+    load(P.kp, kx, ids, 0, false);
+    load(P.vp, vx, ids, 0, true);
+    scales(ids);
+    for (int j = 0; j < steps; ++j) {
+      const int b = j & 1;
+      const uint32_t free_parity = (uint32_t)((j >> 1) + 1) & 1u;
+      if (j + 1 < steps) lookup(j + 1);
+      if (j >= 2 && !wait_bar(&S.k_empty[b], free_parity, abort)) {
+        ok = false;
+        break;
+      }
+      store(sk + b * L::kKV, kx);
+      if (t < 4) {
+        S.scale[j & 3][t] = s_k;
+        S.scale[j & 3][4 + t] = s_v;
+      }
+      fence_async();
+      mbar_arrive(&S.k_full[b]);
+      if (j + 1 < steps) {
+        load(P.kp, kx, ids, j + 1, false);
+        scales(ids);
+      }
+      if (j >= 2 && !wait_bar(&S.v_empty[b], free_parity, abort)) {
+        ok = false;
+        break;
+      }
+      if constexpr (!I8) {
+        if (j * kKeys + kKeys > common) {  // some rows do not see all of these tokens
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const uint32_t w[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
+          }
+          if (odd) set_aside(vx, j);
+        }
+      }
+      store(sv + b * L::kKV, vx);
+      fence_async();
+      mbar_arrive(&S.v_full[b]);
+      if (j + 1 < steps) load(P.vp, vx, ids, j + 1, true);
+    }
+    if (!ok) *abort = 1;
+  } else if (lane == 0) {
+    // --------------------------------------------------------- the products
+    const uint32_t is = I8 ? instr_desc_f16<kKeys>() : instr_desc<kKeys>();
+    const uint32_t ip = (I8 ? instr_desc_f16<D>() : instr_desc<D>()) | kBisMnMajor;
+    auto issue_s = [&](int j) {
+      const int b = j & 1;
+      if (!wait_bar(&S.k_full[b], (uint32_t)(j >> 1) & 1u, abort)) return false;
+      fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t da = smem_desc(smem_u32(sq + (k / 4) * (kRows * 128))) + (uint64_t)(2 * (k % 4));
+        const uint64_t db = smem_desc(smem_u32(sk + b * L::kKV + (k / 4) * (kKeys * 128))) +
+                            (uint64_t)(2 * (k % 4));
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+                tmem + (uint32_t)(kScol + 64 * b)),
+            "l"(da), "l"(db), "r"(is), "r"(k > 0 ? 1u : 0u)
+            : "memory");
+      }
+      commit(&S.s_full[b]);
+      commit(&S.k_empty[b]);
+      return true;
+    };
+    ok = wait_bar(&S.q_full, 0, abort) && issue_s(0);
+    for (int j = 0; ok && j < steps; ++j) {
+      const int b = j & 1;
+      if (j + 1 < steps) ok = issue_s(j + 1);
+      ok = ok && wait_bar(&S.p_full[b], (uint32_t)(j >> 1) & 1u, abort) &&
+           wait_bar(&S.v_full[b], (uint32_t)(j >> 1) & 1u, abort);
+      if (!ok) break;
+      fence_after();
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k) {
+        const uint64_t db = mn_desc(smem_u32(sv + b * L::kKV + k * 2048), kKeys * 128);
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
+            "r"(tmem + (uint32_t)(kScol + 64 * b + 8 * k)), "l"(db), "r"(ip),
+            "r"(j > 0 || k > 0 ? 1u : 0u)
+            : "memory");
+      }
+      commit(&S.v_empty[b]);
+      commit(&S.o_full);
+    }
+    if (!ok) {  // products in flight end before tensor memory is given back
+      *abort = 1;
+      commit(&S.drain);
+      const unsigned long long t0 = now_ns();
+      while (!mbar_try_wait(&S.drain, 0))
+        if (now_ns() - t0 > kWaitNs) break;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+template <int D, bool I8>
+static cudaError_t launch_prompt_kernel(const Params& P, cudaStream_t st) {
+  const size_t smem = PromptSmem<D>::kBytes;
+  static_assert(sizeof(PromptShared) <= 1024, "PromptShared fits behind the operands");
+  ensure_smem((const void*)prompt_kernel<D, I8>, (int)smem);
+  const long long slots = (long long)P.T * P.G / kRows + P.B;
+  return launch_pdl(prompt_kernel<D, I8>, dim3((unsigned)slots, P.Hkv), dim3(kPThreads), smem, st,
+                    true, P);
+}
+
+cudaError_t launch_prompt(const Params& P, int D, bool i8, cudaStream_t st) {
+  if (D == 64)
+    return i8 ? launch_prompt_kernel<64, true>(P, st) : launch_prompt_kernel<64, false>(P, st);
+  return i8 ? launch_prompt_kernel<128, true>(P, st) : launch_prompt_kernel<128, false>(P, st);
+}
+
+}  // namespace pa
+}  // namespace qg
