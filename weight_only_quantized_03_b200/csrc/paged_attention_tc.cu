@@ -32,6 +32,7 @@
 #include <cuda_fp16.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "paged_attention.cuh"
@@ -70,8 +71,8 @@ struct PromptShared {  // behind the operands
 #define QG_W8(a, i) "=r"((a)[i]), "=r"((a)[i + 1]), "=r"((a)[i + 2]), "=r"((a)[i + 3]), \
                     "=r"((a)[i + 4]), "=r"((a)[i + 5]), "=r"((a)[i + 6]), "=r"((a)[i + 7])
 
-// 32 or 64 columns of the warp's 32 lanes, a register each. The load and the
-// wait for it are one statement: the compiler may move or spill the registers
+// 32 columns of the warp's 32 lanes, a register each. The load and the wait
+// for it are one statement: the compiler may move or spill the registers
 // of a load that has not been waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
   asm volatile(
@@ -79,17 +80,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
       "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31},"
       " [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : QG_W8(v, 0), QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24)
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,"
-      "%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,"
-      "%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-      : QG_W8(v, 0), QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24), QG_W8(v, 32), QG_W8(v, 40),
-        QG_W8(v, 48), QG_W8(v, 56)
       : "r"(addr)
       : "memory");
 }
@@ -201,8 +191,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
   if (tid == 0) {
     mbar_init(&S.q_full, kRows);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.k_full[i], 128);
-      mbar_init(&S.v_full[i], 128);
+      mbar_init(&S.k_full[i], 64);
+      mbar_init(&S.v_full[i], 64);
       mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
@@ -232,33 +222,35 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     const int lim = real ? before + ri + 1 : INT_MAX;  // tokens the pair sees
     float qf = P.scale_log2;
     {  // q into shared memory, for int8 pages times a power of two, as fp16
-      uint32_t w[D / 2];
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(P.q) + at;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = real ? __ldcg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
-      }
+      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(P.q) + at);
+      float unit = 1.f;
       if constexpr (I8) {
         float top = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = real ? __ldcg(q + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i)
-          top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-        const float unit = q_unit(top);
-        qf /= unit;
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) {
-          const __half2 h = __floats2half2_rn(bf16_lo(w[i]) * unit, bf16_hi(w[i]) * unit);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int e = 0; e < 4; ++e)
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
         }
+        unit = q_unit(top);
+        qf /= unit;
       }
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 x = real ? __ldcg(q + i) : make_uint4(0, 0, 0, 0);
+        if constexpr (I8) {
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(tid, i)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * unit, bf16_hi(w[e]) * unit);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          x = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(tid, i)) = x;
+      }
     }
     fence_async();
     mbar_arrive(&S.q_full);
@@ -272,9 +264,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         break;
       }
       fence_after();
-      uint32_t s[64];
       const uint32_t sc = lanes + kScol + 64 * b;
-      tmem_ld64(sc, s);
       float ks[4], vs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -283,14 +273,75 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       }
       const bool part = j * kKeys + kKeys > common;
       const int left = lim - j * kKeys;  // visible tokens of this step (or more, or none)
-      float top = -FLT_MAX;
+      // The row's largest score. A negative scale turns the order round.
+      auto largest = [&]() {
+        float top = -FLT_MAX;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        float x = __uint_as_float(s[i]) * ks[i >> 4];
-        if (part && i >= left) x = -INFINITY;
-        s[i] = __float_as_uint(x);
-        top = fmaxf(top, x);
-      }
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[32];
+          tmem_ld32(sc + 32 * h, s);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float k = ks[2 * h + q];
+            const uint32_t flip = __float_as_uint(k) & 0x80000000u;
+            float x[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float y = __uint_as_float(s[16 * q + i] ^ flip);
+              if (32 * h + 16 * q + i >= left) y = -FLT_MAX;
+              x[i & 3] = fmaxf(x[i & 3], y);
+            }
+            top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * fabsf(k));
+          }
+        }
+        return top;
+      };
+      // The weights relative to m as 16-bit pairs, their sum, the largest.
+      uint32_t p[32];
+      float sum, most;
+      auto weights = [&](auto masked, float inv) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[32];
+          tmem_ld32(sc + 32 * h, s);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float k = ks[2 * h + q], w = I8 ? vs[2 * h + q] * inv : 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                y[e] = ex2(fmaf(__uint_as_float(s[16 * q + i + e]), k, -m));
+                const bool hid = masked && 32 * h + 16 * q + i + e >= left;
+                if (hid) y[e] = 0.f;
+                t[(i + e) & 3] += y[e];
+                x[(i + e) & 3] = fmaxf(x[(i + e) & 3], y[e]);
+                if constexpr (I8) {
+                  y[e] *= w;
+                  if (hid) y[e] = 0.f;  // (whatever the block's scale is)
+                }
+              }
+              if constexpr (I8) {
+                const __half2 z = __floats2half2_rn(y[0], y[1]);
+                p[16 * h + 8 * q + i / 2] = *reinterpret_cast<const uint32_t*>(&z);
+              } else {
+                p[16 * h + 8 * q + i / 2] = mm::pack_bf16(y[0], y[1]);
+              }
+            }
+          }
+        }
+        sum = (t[0] + t[1]) + (t[2] + t[3]);
+        most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      };
+      auto form = [&]() {
+        const float inv = I8 ? 2048.f / r : 1.f;
+        if (part)
+          weights(std::true_type(), inv);
+        else
+          weights(std::false_type(), inv);
+      };
       float vtop = 0.f;
       if constexpr (I8) {
 #pragma unroll
@@ -302,7 +353,16 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       // phase only from its neighbours): here if O has to be rescaled, else at
       // the end of the step, when it has long been done.
       bool waited = j == 0;
-      if (__any_sync(0xffffffffu, top > m + kMargin) || wider) {
+      // The weights are formed with the reference as it is; only if one of a
+      // warp's rows has outgrown it (or V's unit grows, or there is none yet)
+      // the largest scores are looked for, and the weights formed again.
+      bool again = j == 0 || wider;
+      if (!again) {
+        form();
+        again = __any_sync(0xffffffffu, most > (float)(1 << (int)kMargin));
+      }
+      if (again) {
+        const float top = largest();
         float a = 1.f;
         if (wider) {
           const float n =
@@ -330,31 +390,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
             tmem_st32(lanes + d, o);
           }
         }
+        form();
       }
-      float wv[4];
-      const float inv = I8 ? 2048.f / r : 1.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wv[i] = I8 ? vs[i] * inv : 1.f;
-      uint32_t p[32];
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        float y[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[e] = ex2(__uint_as_float(s[i + e]) - m);
-          l += y[e];
-          if constexpr (I8) {
-            y[e] *= wv[i >> 4];
-            if (part && i + e >= left) y[e] = 0.f;  // (whatever the block's scale is)
-          }
-        }
-        if constexpr (I8) {
-          const __half2 h = __floats2half2_rn(y[0], y[1]);
-          p[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          p[i / 2] = mm::pack_bf16(y[0], y[1]);
-        }
-      }
+      l += sum;
       tmem_st32(sc, p);
       if (!waited && !wait_bar(&S.o_full, (uint32_t)(j - 1) & 1u, abort)) {
         ok = false;
@@ -395,62 +433,54 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ the pages
+    // Warps 4 and 5 bring K, 6 and 7 V, each a step ahead in registers and two
+    // in page numbers.
     constexpr int ES = I8 ? 1 : 2, CPR = D * ES / 16;  // 16-byte chunks of a row
-    constexpr int R = kKeys * CPR / 128;               // chunks of a thread
-    const int t = tid - 128;
-    int ids = -2;  // lanes 0-3: the step's blocks in the pool (-1: bad page, -2: past the keys)
+    constexpr int R = kKeys * CPR / 64;                // chunks of a thread
+    const bool isv = warp >= 6;
+    const int t = tid - (isv ? 192 : 128);
+    const uint8_t* const pool = isv ? P.vp : P.kp;
+    uint8_t* const buf = isv ? sv : sk;
+    uint64_t* const full = isv ? S.v_full : S.k_full;
+    uint64_t* const empty = isv ? S.v_empty : S.k_empty;
+    // lanes 0-3: a step's blocks in the pool (-1: bad page, -2: past the keys)
     auto lookup = [&](int j) {
-      ids = -2;
       const int blk = j * 4 + lane;
-      if (lane < 4 && blk * kBlock < keys) {
-        const int pi = blk / P.bpp;
-        const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
-        ids = page >= 0 && page < P.num_pages
-                  ? (page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)
-                  : -1;
-      }
+      if (lane >= 4 || blk * kBlock >= keys) return -2;
+      const int pi = blk / P.bpp;
+      const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
+      return page >= 0 && page < P.num_pages ? (page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)
+                                             : -1;
     };
-    auto load = [&](const uint8_t* pool, uint4 (&x)[R], int id, int j, bool v) {
+    uint4 x[R];
+    float scale = 1.f, vscale = 1.f;  // lanes 0-3 of warp 4; a bad page gives NaN scores
+    auto load = [&](int j, int ids) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int ch = i * 128 + t, row = ch / CPR;
-        const int blk = __shfl_sync(0xffffffffu, id, row / kBlock);  // (the same in the warp)
-        const bool in = blk >= 0 && (I8 || !v || j * kKeys + row < it.len);
+        const int ch = i * 64 + t, row = ch / CPR;
+        const int blk = __shfl_sync(0xffffffffu, ids, row / kBlock);  // (the same in the warp)
+        const bool in = blk >= 0 && (I8 || !isv || j * kKeys + row < it.len);
         x[i] = in ? __ldcg(reinterpret_cast<const uint4*>(
                         pool + (long long)blk * (kBlock * D * ES) + (ch % (kBlock * CPR)) * 16))
                   : make_uint4(0, 0, 0, 0);
       }
-    };
-    auto store = [&](uint8_t* dst, const uint4 (&x)[R]) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int ch = i * 128 + t, row = ch / CPR, cc = ch % CPR;
-        if constexpr (I8) {
-          const uint32_t w[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u,
-                                 x[i].w ^ 0x80808080u};
-          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc)) =
-              make_uint4(codes01(w[0]), codes23(w[0]), codes01(w[1]), codes23(w[1]));
-          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc + 1)) =
-              make_uint4(codes01(w[2]), codes23(w[2]), codes01(w[3]), codes23(w[3]));
-        } else {
-          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, cc)) = x[i];
-        }
+      scale = ids == -1 ? __int_as_float(0x7FC00000) : 1.f;
+      if (I8 && warp == 4 && ids >= 0) {
+        scale = __ldcg(P.ks + ids);
+        vscale = __ldcg(P.vs + ids);
       }
     };
     // bf16: values of V that are not finite out of the operand, aside
-    auto set_aside = [&](uint4 (&x)[R], int j) {
-#pragma unroll 1
-      for (int i = 0; i < R; ++i) {
-        const int ch = i * 128 + t, key = j * kKeys + ch / CPR, d0 = ch % CPR * 8;
-        uint32_t w[4];
+    auto set_aside = [&](int j) {
 #pragma unroll
-        for (int q = 0; q < R; ++q)
-          if (q == i) {
-            w[0] = x[q].x;
-            w[1] = x[q].y;
-            w[2] = x[q].z;
-            w[3] = x[q].w;
-          }
+      for (int i = 0; i < R; ++i) {
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
+        if (!odd) continue;
+        const int ch = i * 64 + t, key = j * kKeys + ch / CPR, d0 = ch % CPR * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t bits = e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
@@ -465,80 +495,66 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
             atomicMin(&S.odd_from, key);
           }
         }
-#pragma unroll
-        for (int q = 0; q < R; ++q)
-          if (q == i) x[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
-    uint4 kx[R], vx[R];
-    float s_k, s_v;
-    auto scales = [&](int id) {  // lanes 0-3 of the first loading warp
-      s_k = id == -1 ? __int_as_float(0x7FC00000) : 1.f;
-      s_v = 1.f;
-      if (I8 && t < 4 && id >= 0) {
-        s_k = __ldcg(P.ks + id);
-        s_v = __ldcg(P.vs + id);
-      }
-    };
-    lookup(0);
-    load(P.kp, kx, ids, 0, false);
-    load(P.vp, vx, ids, 0, true);
-    scales(ids);
+    int ids = lookup(0);
+    load(0, ids);
+    ids = lookup(1);
     for (int j = 0; j < steps; ++j) {
       const int b = j & 1;
-      const uint32_t free_parity = (uint32_t)((j >> 1) + 1) & 1u;
-      if (j + 1 < steps) lookup(j + 1);
-      if (j >= 2 && !wait_bar(&S.k_empty[b], free_parity, abort)) {
+      if (j >= 2 && !wait_bar(&empty[b], (uint32_t)((j >> 1) + 1) & 1u, abort)) {
         ok = false;
         break;
       }
-      store(sk + b * L::kKV, kx);
-      if (t < 4) {
-        S.scale[j & 3][t] = s_k;
-        S.scale[j & 3][4 + t] = s_v;
-      }
-      fence_async();
-      mbar_arrive(&S.k_full[b]);
-      if (j + 1 < steps) {
-        load(P.kp, kx, ids, j + 1, false);
-        scales(ids);
-      }
-      if (j >= 2 && !wait_bar(&S.v_empty[b], free_parity, abort)) {
-        ok = false;
-        break;
-      }
-      if constexpr (!I8) {
-        if (j * kKeys + kKeys > common) {  // some rows do not see all of these tokens
-          bool odd = false;
+      // (some rows do not see all of a partly masked step's tokens)
+      if (!I8 && isv && j * kKeys + kKeys > common) set_aside(j);
+      uint8_t* const dst = buf + b * L::kKV;
 #pragma unroll
-          for (int i = 0; i < R; ++i) {
-            const uint32_t w[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
-          }
-          if (odd) set_aside(vx, j);
+      for (int i = 0; i < R; ++i) {
+        const int ch = i * 64 + t, row = ch / CPR, cc = ch % CPR;
+        if constexpr (I8) {
+          const uint32_t w[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u,
+                                 x[i].w ^ 0x80808080u};
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc)) =
+              make_uint4(codes01(w[0]), codes23(w[0]), codes01(w[1]), codes23(w[1]));
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc + 1)) =
+              make_uint4(codes01(w[2]), codes23(w[2]), codes01(w[3]), codes23(w[3]));
+        } else {
+          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, cc)) = x[i];
         }
       }
-      store(sv + b * L::kKV, vx);
+      // A ring of four steps. The rows read a step's scales once its S is full,
+      // before V need be there, so K's warps bring V's scales too.
+      if (!isv && t < 4) {
+        S.scale[j & 3][t] = scale;
+        S.scale[j & 3][4 + t] = vscale;
+      }
       fence_async();
-      mbar_arrive(&S.v_full[b]);
-      if (j + 1 < steps) load(P.vp, vx, ids, j + 1, true);
+      mbar_arrive(&full[b]);
+      if (j + 1 < steps) {
+        load(j + 1, ids);
+        ids = lookup(j + 2);
+      }
     }
     if (!ok) *abort = 1;
   } else if (lane == 0) {
     // --------------------------------------------------------- the products
     const uint32_t is = I8 ? instr_desc_f16<kKeys>() : instr_desc<kKeys>();
     const uint32_t ip = (I8 ? instr_desc_f16<D>() : instr_desc<D>()) | kBisMnMajor;
+    // (addresses in a descriptor are in units of 16 bytes; 16 dims are 32
+    // bytes of a K-major row, 16 tokens two groups of an MN-major panel)
+    const uint64_t dq = smem_desc(smem_u32(sq)), dk = smem_desc(smem_u32(sk));
+    const uint64_t dv = mn_desc(smem_u32(sv), kKeys * 128);
     auto issue_s = [&](int j) {
       const int b = j & 1;
       if (!wait_bar(&S.k_full[b], (uint32_t)(j >> 1) & 1u, abort)) return false;
       fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint64_t da = smem_desc(smem_u32(sq + (k / 4) * (kRows * 128))) + (uint64_t)(2 * (k % 4));
-        const uint64_t db = smem_desc(smem_u32(sk + b * L::kKV + (k / 4) * (kKeys * 128))) +
-                            (uint64_t)(2 * (k % 4));
+        const uint64_t da = dq + (uint64_t)((k / 4) * (kRows * 8) + 2 * (k % 4));
+        const uint64_t db =
+            dk + (uint64_t)(b * (L::kKV / 16) + (k / 4) * (kKeys * 8) + 2 * (k % 4));
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
             " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
@@ -560,7 +576,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       fence_after();
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k) {
-        const uint64_t db = mn_desc(smem_u32(sv + b * L::kKV + k * 2048), kKeys * 128);
+        const uint64_t db = dv + (uint64_t)(b * (L::kKV / 16) + k * 128);
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
             " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
