@@ -98,9 +98,6 @@ __device__ __forceinline__ uint32_t take16(float& lo, float& hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-__device__ __forceinline__ uint4 ldcg16(const uint8_t* p) {
-  return __ldcg(reinterpret_cast<const uint4*>(p));
-}
 
 // Visible tokens of column c of the item's sequence. Columns past the last
 // one (their q is zero, nothing is stored for them) see everything, so that
@@ -219,11 +216,11 @@ struct Walk {
     const uint8_t* p = P.kp + (long long)(ok ? blk : 0) * (kBlock * D * ES) + g * (D * ES) + t * 16;
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
-      kr[0][c] = ok ? ldcg16(p + c * 64) : make_uint4(0, 0, 0, 0);
-      kr[1][c] = ok ? ldcg16(p + 8 * D * ES + c * 64) : make_uint4(0, 0, 0, 0);
+      kr[0][c] = load16_if(p + c * 64, ok);
+      kr[1][c] = load16_if(p + 8 * D * ES + c * 64, ok);
     }
     // a bad page: NaN scores for whoever sees its tokens
-    ks = !ok ? __int_as_float(0x7FC00000) : I8 ? __ldcg(P.ks + blk) : 1.f;
+    ks = load_if(P.ks + blk, I8 && ok, ok ? 1.f : __int_as_float(0x7FC00000));
   }
 
   // Rows at or past the sequence's end hold anything: zero (0 * NaN).
@@ -238,13 +235,13 @@ struct Walk {
       const bool in = ok && key < left;
       if constexpr (VB >= 16) {
 #pragma unroll
-        for (int c = 0; c < VC; ++c) vr[i][c] = in ? ldcg16(pi + c * 16) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < VC; ++c) vr[i][c] = load16_if(pi + c * 16, in);
       } else {
-        const uint2 w = in ? __ldcg(reinterpret_cast<const uint2*>(pi)) : make_uint2(0, 0);
+        const uint2 w = load8_if(pi, in);
         vr[i][0] = make_uint4(w.x, w.y, 0, 0);
       }
     }
-    vs = I8 && ok ? __ldcg(P.vs + blk) : 1.f;
+    vs = load_if(P.vs + blk, I8 && ok, 1.f);
   }
 
   static __device__ __forceinline__ uint32_t word(const uint4& v, int i) {

@@ -40,6 +40,40 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// 16 (8) bytes through L2, or zeros: a predicated load, since a choice made
+// after the load would wait for it.
+__device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @p ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)in));
+  return v;
+}
+__device__ __forceinline__ uint2 load8_if(const uint8_t* p, bool in) {
+  uint2 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b32 %0, 0;\n mov.b32 %1, 0;\n"
+      " @p ld.global.cg.v2.u32 {%0, %1}, [%2];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(p), "r"((int)in));
+  return v;
+}
+// A float through L2, or `other`.
+__device__ __forceinline__ float load_if(const float* p, bool in, float other) {
+  float v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, %3;\n"
+      " @p ld.global.cg.f32 %0, [%1];\n}\n"
+      : "=&f"(v)
+      : "l"(p), "r"((int)in), "f"(other));
+  return v;
+}
+
 // One (sequence, KV head, column tile) item.
 struct Item {
   int b, h, ct;   // sequence, KV head, column tile

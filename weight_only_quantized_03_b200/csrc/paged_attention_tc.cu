@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         float top = 0.f;
 #pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = real ? __ldcg(q + i) : make_uint4(0, 0, 0, 0);
+          const uint4 x = load16_if(reinterpret_cast<const uint8_t*>(q + i), real);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       }
 #pragma unroll 8
       for (int i = 0; i < D / 8; ++i) {
-        uint4 x = real ? __ldcg(q + i) : make_uint4(0, 0, 0, 0);
+        uint4 x = load16_if(reinterpret_cast<const uint8_t*>(q + i), real);
         if constexpr (I8) {
           uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -443,14 +443,21 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     uint8_t* const buf = isv ? sv : sk;
     uint64_t* const full = isv ? S.v_full : S.k_full;
     uint64_t* const empty = isv ? S.v_empty : S.k_empty;
-    // lanes 0-3: a step's blocks in the pool (-1: bad page, -2: past the keys)
-    auto lookup = [&](int j) {
+    // Lanes 0-3: the page of each of a step's blocks, loaded a step before it is
+    // looked at (-1 where there is nothing to look up); from it the block's
+    // place in the pool, -1 for a bad page, -2 past the keys.
+    auto page_of = [&](int j) {
+      const int blk = j * 4 + lane;
+      return lane < 4 && blk * kBlock < keys
+                 ? __ldcg(P.table + (long long)it.b * P.max_pages + blk / P.bpp)
+                 : -1;
+    };
+    auto place_of = [&](int j, int page) {
       const int blk = j * 4 + lane;
       if (lane >= 4 || blk * kBlock >= keys) return -2;
-      const int pi = blk / P.bpp;
-      const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
-      return page >= 0 && page < P.num_pages ? (page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)
-                                             : -1;
+      return page >= 0 && page < P.num_pages
+                 ? (page * P.Hkv + it.h) * P.bpp + (blk - blk / P.bpp * P.bpp)
+                 : -1;
     };
     uint4 x[R];
     float scale = 1.f, vscale = 1.f;  // lanes 0-3 of warp 4; a bad page gives NaN scores
@@ -460,15 +467,11 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         const int ch = i * 64 + t, row = ch / CPR;
         const int blk = __shfl_sync(0xffffffffu, ids, row / kBlock);  // (the same in the warp)
         const bool in = blk >= 0 && (I8 || !isv || j * kKeys + row < it.len);
-        x[i] = in ? __ldcg(reinterpret_cast<const uint4*>(
-                        pool + (long long)blk * (kBlock * D * ES) + (ch % (kBlock * CPR)) * 16))
-                  : make_uint4(0, 0, 0, 0);
+        x[i] = load16_if(pool + (long long)blk * (kBlock * D * ES) + (ch % (kBlock * CPR)) * 16, in);
       }
-      scale = ids == -1 ? __int_as_float(0x7FC00000) : 1.f;
-      if (I8 && warp == 4 && ids >= 0) {
-        scale = __ldcg(P.ks + ids);
-        vscale = __ldcg(P.vs + ids);
-      }
+      const bool scaled = I8 && warp == 4 && ids >= 0;
+      scale = load_if(P.ks + ids, scaled, ids == -1 ? __int_as_float(0x7FC00000) : 1.f);
+      vscale = load_if(P.vs + ids, scaled, 1.f);
     };
     // bf16: values of V that are not finite out of the operand, aside
     auto set_aside = [&](int j) {
@@ -498,9 +501,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
-    int ids = lookup(0);
-    load(0, ids);
-    ids = lookup(1);
+    int page = page_of(0);
+    load(0, place_of(0, page));
+    page = page_of(1);
     for (int j = 0; j < steps; ++j) {
       const int b = j & 1;
       if (j >= 2 && !wait_bar(&empty[b], (uint32_t)((j >> 1) + 1) & 1u, abort)) {
@@ -533,13 +536,17 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       fence_async();
       mbar_arrive(&full[b]);
       if (j + 1 < steps) {
-        load(j + 1, ids);
-        ids = lookup(j + 2);
+        load(j + 1, place_of(j + 1, page));
+        page = page_of(j + 2);
       }
     }
     if (!ok) *abort = 1;
-  } else if (lane == 0) {
+  } else {
     // --------------------------------------------------------- the products
+    // The whole warp walks the loop, so that addresses and descriptors stay in
+    // uniform registers; one lane issues.
+    const bool one = lane == 0;
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t is = I8 ? instr_desc_f16<kKeys>() : instr_desc<kKeys>();
     const uint32_t ip = (I8 ? instr_desc_f16<D>() : instr_desc<D>()) | kBisMnMajor;
     // (addresses in a descriptor are in units of 16 bytes; 16 dims are 32
@@ -548,48 +555,58 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     const uint64_t dv = mn_desc(smem_u32(sv), kKeys * 128);
     auto issue_s = [&](int j) {
       const int b = j & 1;
-      if (!wait_bar(&S.k_full[b], (uint32_t)(j >> 1) & 1u, abort)) return false;
+      if (!__all_sync(0xffffffffu, wait_bar(&S.k_full[b], (uint32_t)(j >> 1) & 1u, abort)))
+        return false;
       fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t da = dq + (uint64_t)((k / 4) * (kRows * 8) + 2 * (k % 4));
         const uint64_t db =
             dk + (uint64_t)(b * (L::kKV / 16) + (k / 4) * (kKeys * 8) + 2 * (k % 4));
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
-                tmem + (uint32_t)(kScol + 64 * b)),
-            "l"(da), "l"(db), "r"(is), "r"(k > 0 ? 1u : 0u)
-            : "memory");
+        if (one)
+          asm volatile(
+              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+              " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+                  base + (uint32_t)(kScol + 64 * b)),
+              "l"(da), "l"(db), "r"(is), "r"(k > 0 ? 1u : 0u)
+              : "memory");
       }
-      commit(&S.s_full[b]);
-      commit(&S.k_empty[b]);
+      if (one) {
+        commit(&S.s_full[b]);
+        commit(&S.k_empty[b]);
+      }
+      __syncwarp();
       return true;
     };
-    ok = wait_bar(&S.q_full, 0, abort) && issue_s(0);
+    ok = __all_sync(0xffffffffu, wait_bar(&S.q_full, 0, abort)) && issue_s(0);
     for (int j = 0; ok && j < steps; ++j) {
       const int b = j & 1;
       if (j + 1 < steps) ok = issue_s(j + 1);
-      ok = ok && wait_bar(&S.p_full[b], (uint32_t)(j >> 1) & 1u, abort) &&
-           wait_bar(&S.v_full[b], (uint32_t)(j >> 1) & 1u, abort);
+      ok = __all_sync(0xffffffffu, ok && wait_bar(&S.p_full[b], (uint32_t)(j >> 1) & 1u, abort) &&
+                                       wait_bar(&S.v_full[b], (uint32_t)(j >> 1) & 1u, abort));
       if (!ok) break;
       fence_after();
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k) {
         const uint64_t db = dv + (uint64_t)(b * (L::kKV / 16) + k * 128);
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
-            "r"(tmem + (uint32_t)(kScol + 64 * b + 8 * k)), "l"(db), "r"(ip),
-            "r"(j > 0 || k > 0 ? 1u : 0u)
-            : "memory");
+        if (one)
+          asm volatile(
+              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+              " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(base),
+              "r"(base + (uint32_t)(kScol + 64 * b + 8 * k)), "l"(db), "r"(ip),
+              "r"(j > 0 || k > 0 ? 1u : 0u)
+              : "memory");
       }
-      commit(&S.v_empty[b]);
-      commit(&S.o_full);
+      if (one) {
+        commit(&S.v_empty[b]);
+        commit(&S.o_full);
+      }
+      __syncwarp();
     }
     if (!ok) {  // products in flight end before tensor memory is given back
       *abort = 1;
-      commit(&S.drain);
+      if (one) commit(&S.drain);
+      __syncwarp();
       const unsigned long long t0 = now_ns();
       while (!mbar_try_wait(&S.drain, 0))
         if (now_ns() - t0 > kWaitNs) break;
