@@ -225,16 +225,14 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(P.q) + at);
       float unit = 1.f;
       if constexpr (I8) {
-        float top = 0.f;
+        uint32_t top = 0;  // two 16-bit maxima: magnitudes order as integers
 #pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = load16_if(reinterpret_cast<const uint8_t*>(q + i), real);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                       __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
         }
-        unit = q_unit(top);
+        unit = q_unit(fmaxf(bf16_lo(top), bf16_hi(top)));
         qf /= unit;
       }
 #pragma unroll 8
@@ -443,35 +441,39 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     uint8_t* const buf = isv ? sv : sk;
     uint64_t* const full = isv ? S.v_full : S.k_full;
     uint64_t* const empty = isv ? S.v_empty : S.k_empty;
-    // Lanes 0-3: the page of each of a step's blocks, loaded a step before it is
-    // looked at (-1 where there is nothing to look up); from it the block's
-    // place in the pool, -1 for a bad page, -2 past the keys.
-    auto page_of = [&](int j) {
-      const int blk = j * 4 + lane;
-      return lane < 4 && blk * kBlock < keys
-                 ? __ldcg(P.table + (long long)it.b * P.max_pages + blk / P.bpp)
-                 : -1;
+    // Block base + lane's page, 32 blocks (8 steps) at a time, loaded a step
+    // before it is looked at; from it the block's place in the pool, -1 for a
+    // bad page, -2 past the keys.
+    auto page_of = [&](int base) {
+      const int blk = base + lane;
+      return blk * kBlock < keys ? __ldcg(P.table + (long long)it.b * P.max_pages + blk / P.bpp)
+                                 : -1;
     };
-    auto place_of = [&](int j, int page) {
-      const int blk = j * 4 + lane;
-      if (lane >= 4 || blk * kBlock >= keys) return -2;
+    auto place_of = [&](int base, int page) {
+      const int blk = base + lane;
+      if (blk * kBlock >= keys) return -2;
       return page >= 0 && page < P.num_pages
                  ? (page * P.Hkv + it.h) * P.bpp + (blk - blk / P.bpp * P.bpp)
                  : -1;
     };
+    // Thread t's chunk i: 64 / CPR rows further than chunk i - 1, the same
+    // place in the row; 64 chunks never pass a block of 16 rows.
+    const int row0 = t / CPR, cc = t % CPR;
     uint4 x[R];
     float scale = 1.f, vscale = 1.f;  // lanes 0-3 of warp 4; a bad page gives NaN scores
-    auto load = [&](int j, int ids) {
+    auto load = [&](int j, int places) {
+      const int from = j * 4 % 32;  // the step's blocks: lanes from .. from + 3
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int ch = i * 64 + t, row = ch / CPR;
-        const int blk = __shfl_sync(0xffffffffu, ids, row / kBlock);  // (the same in the warp)
-        const bool in = blk >= 0 && (I8 || !isv || j * kKeys + row < it.len);
-        x[i] = load16_if(pool + (long long)blk * (kBlock * D * ES) + (ch % (kBlock * CPR)) * 16, in);
+        const int blk = __shfl_sync(0xffffffffu, places, from + i * 64 / (kBlock * CPR));
+        const bool in = blk >= 0 && (I8 || !isv || j * kKeys + i * (64 / CPR) + row0 < it.len);
+        x[i] = load16_if(pool + (long long)blk * (kBlock * D * ES) +
+                             (i * 64 % (kBlock * CPR) + t) * 16, in);
       }
-      const bool scaled = I8 && warp == 4 && ids >= 0;
-      scale = load_if(P.ks + ids, scaled, ids == -1 ? __int_as_float(0x7FC00000) : 1.f);
-      vscale = load_if(P.vs + ids, scaled, 1.f);
+      const int id = __shfl_sync(0xffffffffu, places, from + (lane & 3));
+      const bool scaled = I8 && warp == 4 && id >= 0;
+      scale = load_if(P.ks + id, scaled, id == -1 ? __int_as_float(0x7FC00000) : 1.f);
+      vscale = load_if(P.vs + id, scaled, 1.f);
     };
     // bf16: values of V that are not finite out of the operand, aside
     auto set_aside = [&](int j) {
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         for (int e = 0; e < 4; ++e)
           odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
         if (!odd) continue;
-        const int ch = i * 64 + t, key = j * kKeys + ch / CPR, d0 = ch % CPR * 8;
+        const int key = j * kKeys + i * (64 / CPR) + row0, d0 = cc * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t bits = e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
@@ -501,9 +503,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
-    int page = page_of(0);
-    load(0, place_of(0, page));
-    page = page_of(1);
+    int page = page_of(0), places = place_of(0, page);
+    load(0, places);
     for (int j = 0; j < steps; ++j) {
       const int b = j & 1;
       if (j >= 2 && !wait_bar(&empty[b], (uint32_t)((j >> 1) + 1) & 1u, abort)) {
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       uint8_t* const dst = buf + b * L::kKV;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int ch = i * 64 + t, row = ch / CPR, cc = ch % CPR;
+        const int row = i * (64 / CPR) + row0;
         if constexpr (I8) {
           const uint32_t w[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u,
                                  x[i].w ^ 0x80808080u};
@@ -536,8 +537,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       fence_async();
       mbar_arrive(&full[b]);
       if (j + 1 < steps) {
-        load(j + 1, place_of(j + 1, page));
-        page = page_of(j + 2);
+        if ((j + 1) % 8 == 7) page = page_of(4 * (j + 2));
+        if ((j + 1) % 8 == 0) places = place_of(4 * (j + 1), page);
+        load(j + 1, places);
       }
     }
     if (!ok) *abort = 1;
