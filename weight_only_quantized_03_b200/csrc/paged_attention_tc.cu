@@ -53,12 +53,13 @@ constexpr int kScol = 128;         // S buffers at columns 128 and 192; O at 0
 template <int D>
 struct PromptSmem {
   static constexpr int kQ = kRows * D * 2, kKV = kKeys * D * 2;
-  static constexpr int kBytes = 1024 + kQ + 4 * kKV + 1024;
+  static constexpr int kBytes = 1024 + kQ + 4 * kKV + 1536;
 };
 
 struct PromptShared {  // behind the operands
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
   float scale[4][8];   // ring: a step's K and V scales (4 blocks of 16 tokens each)
+  float unit[kRows];   // of each pair's q
   uint32_t tmem;
   int abort;
   int odd_n, odd_from;  // entries below; the first token of one that found no room
@@ -228,34 +229,47 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     // ------------------------------------------------------------ the rows
     const int lim = real ? before + ri + 1 : INT_MAX;  // tokens the pair sees
     float qf = P.scale_log2;
-    {  // q into shared memory, for int8 pages times a power of two, as fp16
-      const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(P.q) + at);
-      float unit = 1.f;
-      if constexpr (I8) {
-        uint32_t top = 0;  // two 16-bit maxima: magnitudes order as integers
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = load16_if(reinterpret_cast<const uint8_t*>(q + i), real);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                       __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-        }
-        unit = q_unit(fmaxf(bf16_lo(top), bf16_hi(top)));
-        qf /= unit;
-      }
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 x = load16_if(reinterpret_cast<const uint8_t*>(q + i), real);
-        if constexpr (I8) {
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    {
+      // q into shared memory, for int8 pages times a power of two, as fp16. A
+      // warp brings its own 32 pairs, whole rows at a time.
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a load
+      const int cc = lane % LPR;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * unit, bf16_hi(w[e]) * unit);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          x = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i0 = 0; i0 < LPR; i0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int cq = first + 32 * warp + (i0 + i) * RPI + lane / LPR, rq = cq / P.G;
+          const bool in = cq < cols;
+          const long long from =
+              ((long long)(it.r0 + (in ? rq : 0)) * P.H + it.h * P.G + (in ? cq - rq * P.G : 0)) * D;
+          x[i] = load16_if(reinterpret_cast<const uint8_t*>(P.q) + 2 * (from + cc * 8), in);
         }
-        *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(tid, i)) = x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 32 * warp + (i0 + i) * RPI + lane / LPR;
+          if constexpr (I8) {
+            // two 16-bit maxima: magnitudes order as integers
+            uint32_t top = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                    __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1)
+              top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float unit = q_unit(fmaxf(bf16_lo(top), bf16_hi(top)));
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * unit, bf16_hi(w[e]) * unit);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (cc == 0) S.unit[row] = unit;
+          }
+          *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(row, cc)) = x[i];
+        }
       }
+      __syncwarp();
+      if constexpr (I8) qf /= S.unit[tid];
     }
     fence_async();
     mbar_arrive(&S.q_full);
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
 template <int D, bool I8>
 static cudaError_t launch_prompt_kernel(const Params& P, cudaStream_t st) {
   const size_t smem = PromptSmem<D>::kBytes;
-  static_assert(sizeof(PromptShared) <= 1024, "PromptShared fits behind the operands");
+  static_assert(sizeof(PromptShared) <= 1536, "PromptShared fits behind the operands");
   ensure_smem((const void*)prompt_kernel<D, I8>, (int)smem);
   const long long slots = (long long)P.T * P.G / kRows + P.B;
   return launch_pdl(prompt_kernel<D, I8>, dim3((unsigned)slots, P.Hkv), dim3(kPThreads), smem, st,
