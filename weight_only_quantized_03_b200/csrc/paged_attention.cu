@@ -249,8 +249,12 @@ struct Walk {
   }
 
   __device__ __forceinline__ void scores(float (&s)[NT][4]) {
+    float rest[QS > 1 ? NT : 1][4];  // of q's lower terms (see weigh)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    for (int j = 0; j < NT; ++j) {
+      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if constexpr (QS > 1) rest[j][0] = rest[j][1] = rest[j][2] = rest[j][3] = 0.f;
+    }
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
 #pragma unroll
@@ -275,10 +279,16 @@ struct Walk {
           for (int e = 0; e < QS; ++e) {
             const uint2 b = *reinterpret_cast<const uint2*>(
                 sq + (((step * NT + j) * QS + e) * 32 + lane) * 4);
-            mma<I8>(s[j], a0, a1, a2, a3, b.x, b.y);
+            mma<I8>(e ? rest[QS > 1 ? j : 0] : s[j], a0, a1, a2, a3, b.x, b.y);
           }
         }
       }
+    }
+    if constexpr (QS > 1) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += rest[j][e];
     }
   }
 
@@ -365,10 +375,23 @@ struct Walk {
         a2 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x5410u);
         a3 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x7632u);
       }
+      // The tensor core's adds truncate. One term: 16 tokens an add, and what a
+      // bf16 result shows of it is nothing. Several: the tile's sum is formed
+      // by itself, smallest term first, and added to the running one with
+      // rounding, which keeps a long cache's sum at fp32's accuracy (32749
+      // tokens: 1.3e-6 off with the terms added to the running sum).
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (PS == 1) {
+          mma<I8>(S.o[i][j], a0, a1, a2, a3, b[j][0][0], b[j][0][1]);
+        } else {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < PS; ++e) mma<I8>(S.o[i][j], a0, a1, a2, a3, b[j][e][0], b[j][e][1]);
+          for (int e = PS - 1; e >= 0; --e) mma<I8>(t, a0, a1, a2, a3, b[j][e][0], b[j][e][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S.o[i][j][e] += t[e];
+        }
+      }
     }
   }
 
