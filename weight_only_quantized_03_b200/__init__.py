@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -197,6 +198,11 @@ def _stream(stream=None):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _current_device():
+    """Index of the current device (tensors on one exist, so CUDA is up)."""
+    return torch._C._cuda_getDevice()
+
+
 def _raw_stream(stream, dev):
     """``_stream`` without building a stream object."""
     if stream is None:
@@ -375,7 +381,7 @@ def qg_sample_filtered(logits, u, out, temperature=None, top_k=None, top_p=None,
     kept (int32) and logprob (fp32), when given, get the number of tokens
     kept and the drawn one's log-probability among them."""
     B, V = logits.shape
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if logits.dtype is not torch.float32:
         raise TypeError(f"logits must be float32, not {logits.dtype}")
     ld = _rows_of("logits", logits, V)
@@ -389,9 +395,8 @@ def qg_sample_filtered(logits, u, out, temperature=None, top_k=None, top_p=None,
             raise ValueError(f"{name} must be a contiguous {dt} tensor of {B} values")
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
-    _call("qg_sample_filtered", logits.data_ptr(), ld, B, V, _p(temperature), _p(top_k), _p(top_p),
-          _p(min_p), u.data_ptr(), out.data_ptr(), _p(kept), _p(logprob),
-          _raw_stream(stream, dev))
+    _sample(logits.data_ptr(), ld, B, V, _p(temperature), _p(top_k), _p(top_p), _p(min_p),
+            u.data_ptr(), out.data_ptr(), _p(kept), _p(logprob), _raw_stream(stream, dev))
 
 
 def qg_decode_attention_static_scratch_capacity():
@@ -423,6 +428,24 @@ def qg_dequant_q4_0(blocks, out, stream=None):
 # ------------------------------------------------------------ paged cache ----
 # A serving loop makes these calls once a layer and token, so their checks
 # are written to cost little: plain loops, no keyword dictionaries.
+
+_PAGED_KV = struct.Struct("@PPPPiiiii").pack  # the fields of qg_paged_kv
+
+
+def _fast_call(name):
+    """``_call`` of one entry point, looked up once."""
+    fn = getattr(lib, name)
+
+    def call(*args):
+        st = fn(*args)
+        if st != QG_OK:
+            raise QGError(name, st, last_error())
+    return call
+
+
+_append, _gather, _attend, _sample = map(_fast_call, (
+    "qg_paged_kv_append", "qg_paged_kv_gather", "qg_paged_attention", "qg_sample_filtered"))
+
 
 def _check_device(dev, *named):
     """Every given tensor of the (name, tensor) pairs is on CUDA device ``dev``."""
@@ -479,9 +502,11 @@ class PagedKV:
         self.k_pages, self.v_pages, self.k_scales, self.v_scales = (k_pages, v_pages, k_scales,
                                                                     v_scales)
         self.kv_heads, self.page_size, self.head_dim = Hkv, size, D
-        self.c_kv = qg_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), _p(k_scales),
-                                _p(v_scales), P, size, Hkv, D, QG_KV_INT8 if int8 else QG_KV_BF16)
-        self._ref = ctypes.byref(self.c_kv)
+        # the C struct qg_paged_kv (read during a call only)
+        self.c_kv = _PAGED_KV(k_pages.data_ptr(), v_pages.data_ptr(),
+                              k_scales.data_ptr() if int8 else 0,
+                              v_scales.data_ptr() if int8 else 0, P, size, Hkv, D,
+                              QG_KV_INT8 if int8 else QG_KV_BF16)
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype=torch.int8, device="cuda"):
@@ -522,7 +547,7 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
     page_table int32 [B, max_pages]; kv_len int32 [B] counts the new rows;
     row_start int32 [B+1], or None for one row per sequence. ``rotary_dim``
     None: the whole head."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     D = kv.head_dim
     W = kv.kv_heads * D
     T, dt = k.shape[0], k.dtype
@@ -541,15 +566,17 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
         if q_out is None or q_out.shape != q.shape or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous with q's shape")
         qdt = _dt(q_out)
-    _check_device(dev, ("k", k), ("v", v), ("q", q), ("q_out", q_out), ("q_norm", q_norm),
-                  ("k_norm", k_norm))
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+    for t in (k, v, q, q_out, q_norm, k_norm):
+        if t is not None and t.get_device() != dev:
+            _check_device(dev, ("k", k), ("v", v), ("q", q), ("q_out", q_out), ("q_norm", q_norm),
+                          ("k_norm", k_norm))
+    for w in (q_norm, k_norm):
         if w is not None and (w.numel() != D or w.element_size() != 2 or not w.is_contiguous()):
-            raise ValueError(f"{name} must be {D} bf16 values")
-    _call("qg_paged_kv_append", kv._ref, page_table.data_ptr(), most, kv_len.data_ptr(),
-          _p(row_start), _p(q), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, _dt(k), _p(q_norm),
-          _p(k_norm), eps, theta, D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
-          _raw_stream(stream, dev))
+            raise ValueError(f"q_norm and k_norm must be {D} bf16 values")
+    _append(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(), _p(row_start), _p(q), q_ld,
+            k.data_ptr(), k_ld, v.data_ptr(), v_ld, _dt(k), _p(q_norm), _p(k_norm), eps, theta,
+            D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
+            _raw_stream(stream, dev))
 
 
 def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None, stream=None):
@@ -559,7 +586,7 @@ def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None,
     one = k_out if k_out is not None else v_out
     if one is None:
         return
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     T = one.shape[0]
     B, most = kv._batch(page_table, first, "first", row_start, T, dev)
     for t in (k_out, v_out):
@@ -568,8 +595,8 @@ def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None,
             raise ValueError(f"k_out and v_out must be contiguous [{T}, "
                              f"{kv.kv_heads * kv.head_dim}] of one type")
     _check_device(dev, ("k_out", k_out), ("v_out", v_out))
-    _call("qg_paged_kv_gather", kv._ref, page_table.data_ptr(), most, _p(first), _p(row_start),
-          _p(k_out), _p(v_out), _dt(one), B, T, _raw_stream(stream, dev))
+    _gather(kv.c_kv, page_table.data_ptr(), most, _p(first), _p(row_start), _p(k_out),
+            _p(v_out), _dt(one), B, T, _raw_stream(stream, dev))
 
 
 def qg_paged_attention_workspace_size(head_dim):
@@ -582,7 +609,7 @@ def qg_paged_attention(kv, page_table, kv_len, q, out, H, scale, ws, row_start=N
     of ``kv`` (a PagedKV). page_table int32 [B, max_pages]; kv_len int32 [B]
     counts the rows' own tokens; row_start int32 [B+1], or None for one row
     per sequence; ws of qg_paged_attention_workspace_size(D) bytes."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     T = q.shape[0]
     if kv_len is None:
         raise ValueError("kv_len is needed")
@@ -591,9 +618,9 @@ def qg_paged_attention(kv, page_table, kv_len, q, out, H, scale, ws, row_start=N
             not (q.is_contiguous() and out.is_contiguous()):
         raise ValueError(f"q and out must be contiguous [T, {H} * {kv.head_dim}]")
     _check_device(dev, ("q", q), ("out", out), ("ws", ws))
-    _call("qg_paged_attention", kv._ref, page_table.data_ptr(), most, kv_len.data_ptr(),
-          _p(row_start), q.data_ptr(), _dt(q), out.data_ptr(), _dt(out), B, T, H, scale,
-          ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    _attend(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(), _p(row_start),
+            q.data_ptr(), _dt(q), out.data_ptr(), _dt(out), B, T, H, scale, ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
 
 
 # ---------------------------------------------------------- decode step ----

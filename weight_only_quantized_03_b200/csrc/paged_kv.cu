@@ -525,6 +525,22 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams 
   }
 }
 
+// Angles of the rotated pairs at position 1 in units of pi. A decode loop asks
+// for the same ones each call, and 64 powers are 4 us of host time: the
+// calling thread's last set is kept.
+static void turns(double theta, int rotary_dim, double* out) {
+  static thread_local double last_theta = 0.0, last[kMaxHalf];
+  static thread_local int last_dim = -1;
+  const int half = rotary_dim / 2;
+  if (rotary_dim != last_dim || theta != last_theta) {
+    for (int i = 0; i < half; ++i)
+      last[i] = pow(theta, -2.0 * i / rotary_dim) / 3.14159265358979323846;
+    last_theta = theta;
+    last_dim = rotary_dim;
+  }
+  for (int i = 0; i < half; ++i) out[i] = last[i];
+}
+
 template <int D, bool I8>
 cudaError_t launch_append(const AppendParams& P, bool xf32, dim3 grid, cudaStream_t st) {
   if (xf32)
@@ -624,8 +640,7 @@ extern "C" qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* pa
   P.page_size = kv->page_size;
   P.max_pages = max_pages;
   P.num_pages = kv->num_pages;
-  for (int i = 0; i < P.half; ++i)
-    P.turns[i] = pow(theta, -2.0 * i / rotary_dim) / 3.14159265358979323846;
+  pk::turns(theta, rotary_dim, P.turns);
   const int slots = row_start ? T / pk::kBlock + 2 * B : B;
   // heads spread over CTAs until the grid fills the GPU four times (CTAs that
   // resident SMs hold) or each warp has one item
