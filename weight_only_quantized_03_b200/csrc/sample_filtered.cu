@@ -87,10 +87,10 @@ struct Shared {
   // each group of 32 bins (the whole at the end)
   u64 tot_w[kBins], sup_w[kBins / 32 + 1];
   unsigned tot_c[kBins], sup_c[kBins / 32 + 1];
-  // this CTA's histogram: counts; weights in two halves, since a 64-bit
-  // shared-memory atomic costs several 32-bit ones
-  unsigned hist_c[kBins];
-  uint2 hist_w[kBins];
+  // this CTA's histogram: counts, and weights in three pieces of 16 bits, whose
+  // sums over a slice fit 32 bits: atomics that return nothing (a 64-bit one
+  // costs several, and two halves would need the carry back)
+  unsigned hist_c[kBins], hist_w0[kBins], hist_w1[kBins], hist_w2[kBins];
 };
 // Inside one bin (rank 0, rare): lies over the list.
 constexpr int kSubBins = 512;
@@ -98,6 +98,7 @@ struct Sub {
   u64 w[kSubBins];
   unsigned c[kSubBins];
 };
+static_assert(sizeof(Shared) + kResident * 4 <= 227 * 1024, "a slice fits beside Shared");
 static_assert(sizeof(Sub) <= 2 * kList * sizeof(u64), "Sub lies over list_key and list_w");
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -173,58 +174,62 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
   return a + (b << 26) + (c << 52);
 }
 
-__device__ __forceinline__ void add_weight(uint2* at, u64 w) {
-  const unsigned lo = (unsigned)w, old = atomicAdd(&at->x, lo);
-  const unsigned hi = (unsigned)(w >> 32) + (old + lo < old);
-  if (hi) atomicAdd(&at->y, hi);
+__device__ __forceinline__ void add_weight(Shared& S, int b, u64 w) {
+  atomicAdd(&S.hist_w0[b], (unsigned)w & 0xFFFFu);
+  if (w >> 16) atomicAdd(&S.hist_w1[b], (unsigned)(w >> 16) & 0xFFFFu);
+  if (w >> 32) atomicAdd(&S.hist_w2[b], (unsigned)(w >> 32));
 }
 
 // The row's bins and weights.
 struct Row {
   float top;       // the largest value
-  double inv_t;    // 1 / temperature
+  double per_unit; // 64 / (ln2 T)
   int frac;        // fraction bits of a weight
-  double least;    // (l - max) / T below this has weight 0
+  float reach;     // values further below the maximum have weight 0
   float fine, coarse, edge;  // bins: d * fine up to d = edge, then (d - edge) * coarse
   const double* pow2;
 
-  __device__ __forceinline__ double exponent(float v) const {
-    return v == top ? 0.0 : ((double)v - (double)top) * inv_t;  // (0 for +inf too)
+  // (l - max) / T in steps of ln2 / 64: 0 for the maximum itself (+inf too).
+  __device__ __forceinline__ double steps(float v) const {
+    const double x = ((double)v - (double)top) * per_unit;  // (the difference is exact)
+    return v == top ? 0.0 : x;
   }
-  // exp(x) for least <= x <= 0, times 2^up: table-driven (Tang, "Table-driven
-  // implementation of the exponential function", 1989) with 64 steps an
-  // octave: x = (64 k + i) ln2/64 + r, |r| <= ln2/128, and a polynomial of
-  // degree 5 in r (next term r^6/720 < 2^-54).
+  // 2^(x / 64 + up) for x <= 0 down to -64 (frac + 2): table-driven (Tang, "Table-driven
+  // implementation of the exponential function", 1989): x = n + f with n an
+  // integer, 2^(n / 64) from the table of 64 and the exponent, e^(f ln2 / 64)
+  // by its series up to the fifth power (the next term is below 2^-54).
   __device__ __forceinline__ double power(double x, int up) const {
     const double magic = 6755399441055744.0;  // 1.5 * 2^52: the sum rounds to an integer
-    const double t = fma(x, 92.33248261689366, magic);  // 64 / ln 2
+    const double t = x + magic;
     const int k = __double2loint(t);
-    const double n = t - magic;
-    double r = fma(n, -0.010830424696249145, x);            // ln2 / 64, rounded
-    r = fma(n, -3.623510646634843e-19, r);                  // what the rounding left
-    double p = fma(r, 1.0 / 120.0, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
-    p = fma(p, r, 0.5);
-    p = fma(p, r, 1.0) * r;
+    const double f = x - (t - magic);
+    constexpr double c = 0.010830424696249145;  // ln2 / 64
+    double p = fma(f, c * c * c * c * c / 120, c * c * c * c / 24);
+    p = fma(p, f, c * c * c / 6);
+    p = fma(p, f, c * c / 2);
+    p = fma(p, f, c) * f;
     const double s = pow2[k & (kSteps - 1)];
     const double y = fma(s, p, s);
     return __hiloint2double(__double2hiint(y) + (((k >> 6) + up) << 20), __double2loint(y));
   }
   __device__ __forceinline__ double weight(float v) const {
-    const double x = exponent(v);
-    return x >= least ? power(x, 0) : 0.0;
+    return weighs(v) ? power(steps(v), 0) : 0.0;
   }
-  // power(x, frac) and the weight in units of 2^-frac, 0 where it rounds to
-  // less: the sum with 2^52 rounds it.
-  __device__ __forceinline__ u64 fixed_of(double x, double* y) const {
-    const bool in = x >= least;
-    *y = power(in ? x : 0.0, frac);
+  // Whether v's weight can be more than 0.
+  __device__ __forceinline__ bool weighs(float v) const {
+    return v == top || (top - v <= reach && v > -INFINITY);
+  }
+  // power(x, frac) and the weight in units of 2^-frac: the sum with 2^52
+  // rounds it.
+  __device__ __forceinline__ u64 fixed_of(float v, double* y) const {
+    const bool in = weighs(v);
+    *y = power(in ? steps(v) : 0.0, frac);
     const u64 w = (u64)__double_as_longlong(*y + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
     return in ? w : 0;
   }
   __device__ __forceinline__ u64 fixed(float v) const {
     double y;
-    return fixed_of(exponent(v), &y);
+    return fixed_of(v, &y);
   }
   // Monotone in v: each step (difference, product, minimum, and the sum with
   // 2^23 that rounds to an integer) is.
@@ -248,8 +253,9 @@ struct Work {
   int begin, n;
   unsigned rank, C;
 
-  // f(value, index) for the slice, four values side by side (their chains
-  // hide each other's latency); -inf past its end.
+  // f(four values, index of the first) for the slice, the indexes NTHR apart;
+  // -inf past its end. Four at once, so that f can form what it needs of all
+  // of them before it branches: their chains hide each other's latency.
   template <class F>
   __device__ __forceinline__ void each(F f) const {
     const float* const from = P.resident ? data : row + begin;
@@ -258,10 +264,8 @@ struct Work {
     for (int i = threadIdx.x; i < len; i += 4 * NTHR) {
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = i + e * NTHR < len ? from[i + e * NTHR] : -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f(v[e], first + i + e * NTHR);
+      for (int e = 0; e < 4; ++e) v[e] = i + e * NTHR < len ? from[i + e * NTHR] : -INFINITY;
+      f(v, first + i);
     }
   }
 
@@ -272,6 +276,10 @@ struct Work {
       cluster_sync();
   }
 
+  __device__ __forceinline__ u64 own_weight(int b) const {
+    return (u64)S.hist_w0[b] + ((u64)S.hist_w1[b] << 16) + ((u64)S.hist_w2[b] << 32);
+  }
+
   // The cluster's sums of the CTAs' histograms into rank 0's (c, w), each rank
   // a share of the bins, and the sums of groups of 32 bins.
   __device__ __forceinline__ void sum_bins(int bins, unsigned* c, u64* w) const {
@@ -279,16 +287,19 @@ struct Work {
     for (int i = threadIdx.x; i < per; i += NTHR) {
       const int b = rank * per + i;
       unsigned nc = S.hist_c[b];
-      u64 nw = w ? *reinterpret_cast<const u64*>(&S.hist_w[b]) : 0;
+      u64 nw = w ? own_weight(b) : 0;
       if (C > 1) {
         nc = 0;
         nw = 0;
         const uint32_t ac = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_c[b]));
-        const uint32_t aw = static_cast<uint32_t>(__cvta_generic_to_shared(&S.hist_w[b]));
+        constexpr uint32_t next = kBins * 4;  // the four arrays follow each other
 #pragma unroll 4
         for (unsigned r = 0; r < C; ++r) {
-          nc += ld_u32(remote_at(ac, r));
-          if (w) nw += ld_u64(remote_at(aw, r));
+          const uint32_t a = remote_at(ac, r);
+          nc += ld_u32(a);
+          if (w)
+            nw += (u64)ld_u32(a + next) + ((u64)ld_u32(a + 2 * next) << 16) +
+                  ((u64)ld_u32(a + 3 * next) << 32);
         }
       }
       st_u32(remote(&c[b], 0), nc);
@@ -317,17 +328,25 @@ struct Work {
   // The slice's weights (and, with `count`, counts) into the histogram.
   __device__ __forceinline__ void weigh(const Row& R, double min_p, bool count) const {
     unsigned above = 0;
-    each([&](float v, int) {
-      const bool in = v > -INFINITY;
-      const int k = R.bin(v);
-      double y;
-      const u64 w = in ? R.fixed_of(R.exponent(v), &y) : 0;
-      if (in && count) atomicAdd(&S.hist_c[k], 1u);
-      if (w) {
-        add_weight(&S.hist_w[k], w);
-        // (scaling by 2^frac is exact: this is power(x, 0) >= min_p)
-        above += __hiloint2double(__double2hiint(y) - (R.frac << 20), __double2loint(y)) >= min_p;
+    each([&](const float (&v)[4], int) {
+      int b[4];
+      u64 w[4];
+      double y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        b[e] = R.bin(v[e]);
+        w[e] = R.fixed_of(v[e], &y[e]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (count && v[e] > -INFINITY) atomicAdd(&S.hist_c[b[e]], 1u);
+        if (w[e]) add_weight(S, b[e], w[e]);
+      }
+      if (min_p > 0.0)  // (scaling by 2^frac is exact: this is power(x, 0) >= min_p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          above += w[e] && __hiloint2double(__double2hiint(y[e]) - (R.frac << 20),
+                                            __double2loint(y[e])) >= min_p;
     });
     if (min_p > 0.0) push_above(above);
   }
@@ -341,11 +360,18 @@ struct Work {
       // the CTA's own first, then all of them at once to rank 0
       if (tid == 0) S.mine_n = 0;
       __syncthreads();
-      each([&](float v, int i) {
-        const int b = R.bin(v);
-        if (S.wanted[b >> 5] >> (b & 31) & 1) {
-          const u64 k = key_of(v, i);
-          if (k != 0 && k >= c.lo && k <= c.hi) {
+      each([&](const float (&v)[4], int i) {
+        unsigned hit = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int b = R.bin(v[e]);
+          hit |= (S.wanted[b >> 5] >> (b & 31) & 1) << e;
+        }
+        if (!hit) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u64 k = key_of(v[e], i + e * NTHR);
+          if ((hit >> e & 1) && k != 0 && k >= c.lo && k <= c.hi) {
             const unsigned at = atomicAdd(&S.mine_n, 1u);
             if (at < NTHR) S.mine[at] = k;
           }
@@ -360,11 +386,14 @@ struct Work {
         st_u64(remote(&S.list_key[at], 0), S.mine[tid]);
     } else if (c.op == kMinMax) {  // of the bin's keys
       u64 lo = ~0ull, hi = 0;
-      each([&](float v, int i) {
-        if (!(v > -INFINITY) || R.bin(v) != c.bin) return;
-        const u64 k = key_of(v, i);
-        lo = min(lo, k);
-        hi = max(hi, k);
+      each([&](const float (&v)[4], int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!(v[e] > -INFINITY) || R.bin(v[e]) != c.bin) continue;
+          const u64 k = key_of(v[e], i + e * NTHR);
+          lo = min(lo, k);
+          hi = max(hi, k);
+        }
       });
       lo = warp_min64(lo);
       hi = warp_max64(hi);
@@ -388,16 +417,20 @@ struct Work {
     } else {  // kHist: the bin's keys in [lo, hi] by their distance to hi
       for (int i = tid; i < kSubBins; i += NTHR) {
         S.hist_c[i] = 0;
-        S.hist_w[i] = make_uint2(0, 0);
+        S.hist_w0[i] = S.hist_w1[i] = S.hist_w2[i] = 0;
       }
       __syncthreads();
-      each([&](float v, int i) {
-        const u64 k = key_of(v, i);
-        if (!(v > -INFINITY) || R.bin(v) != c.bin || k < c.lo || k > c.hi) return;
-        const int b = (int)((c.hi - k) >> c.shift);
-        atomicAdd(&S.hist_c[b], 1u);
-        const u64 w = R.fixed(v);
-        if (w) add_weight(&S.hist_w[b], w);
+      each([&](const float (&v)[4], int i) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const float x = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+          const u64 k = key_of(x, i + e * NTHR);
+          if (!(x > -INFINITY) || R.bin(x) != c.bin || k < c.lo || k > c.hi) continue;
+          const int b = (int)((c.hi - k) >> c.shift);
+          atomicAdd(&S.hist_c[b], 1u);
+          const u64 w = R.fixed(x);
+          if (w) add_weight(S, b, w);
+        }
       });
       sync();
       Sub& sub = *reinterpret_cast<Sub*>(S.list_key);
@@ -585,7 +618,7 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
   const float* row = P.logits + (long long)b * P.ld;
   for (int i = tid; i < kBins; i += NTHR) {
     S.hist_c[i] = 0;
-    S.hist_w[i] = make_uint2(0, 0);
+    S.hist_w0[i] = S.hist_w1[i] = S.hist_w2[i] = 0;
   }
   if (tid < kSteps) S.pow2[tid] = P.pow2[tid];
   pdl_wait();
@@ -667,12 +700,13 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
   Row R;
   R.pow2 = S.pow2;
   R.top = value_of(hi);
-  R.inv_t = 1.0 / (double)T;
+  R.per_unit = 92.33248261689366 / (double)T;
   R.frac = P.frac;
-  R.least = -0.6931471805599453 * (P.frac + 1);
   // fine bins up to the last value with a weight, coarse ones beyond
   const float span = R.top - value_of(lo);
-  R.edge = fminf(fminf(span, (float)(-R.least * (double)T)), FLT_MAX);
+  R.reach = fminf(span, (float)(0.6931471805599453 * (P.frac + 1) * (double)T));
+  R.edge = fminf(R.reach, FLT_MAX);
+  if (!(R.top <= FLT_MAX)) R.reach = -1.f;  // +inf leaves the others nothing
   R.fine = R.edge > 0.f ? (float)kFine / R.edge : 0.f;
   const float rest = fminf(span, 32.f * R.edge + 64.f) - R.edge;
   R.coarse = rest > 0.f ? (float)(kBins - kFine) / rest : 0.f;
@@ -683,9 +717,13 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
   const double mp = min_p > 0.f ? fmin(1.0, (double)min_p) : 0.0;
   const bool few = top_k > 0 && top_k <= NTHR / 2 && (unsigned)top_k < cnt;
   if (few)
-    W.each([&](float v, int) {
-      const int k = R.bin(v);
-      if (v > -INFINITY) atomicAdd(&S.hist_c[k], 1u);
+    W.each([&](const float (&v)[4], int) {
+      int b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = R.bin(v[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v[e] > -INFINITY) atomicAdd(&S.hist_c[b[e]], 1u);
     });
   else
     W.weigh(R, mp, true);
@@ -914,7 +952,7 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
     P.out[b] = index_of(pick.key);
     if (P.kept) P.kept[b] = (int32_t)kept;
     if (P.logprob)
-      P.logprob[b] = (float)log(R.power(R.exponent(value_of(pick.key)), R.frac) / (double)sum);
+      P.logprob[b] = (float)log(R.power(R.steps(value_of(pick.key)), R.frac) / (double)sum);
   }
 }
 
