@@ -796,16 +796,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     it.len = __shfl_sync(0xffffffffu, i.len, l);
     before = __shfl_sync(0xffffffffu, b, l);
   });
-  if (it.b < 0) return;
+  // Every CTA waits before it ends: this grid must not complete before the
+  // split kernel's, for which the next kernel waits only through this one.
+  if (it.b < 0) {
+    pdl_wait();
+    return;
+  }
   const SeqWork w(P, it, NC);
   it.ct = u - (int)((long long)it.r0 * P.G / NC + it.b);
   it.h = blockIdx.y;
-  if (it.ct >= w.tiles) return;
+  if (it.ct >= w.tiles) {
+    pdl_wait();
+    return;
+  }
   const unsigned begin = before + (unsigned)(it.h * w.tiles + it.ct) * w.chunks;
   const Cut cut(N, P.pieces);
-  const int p0 = (int)cut.piece_of(begin), p1 = (int)cut.piece_of(begin + w.chunks - 1);
-  if (p0 == p1) return;  // written by its piece
+  // (within the workspace even if row starts decrease)
+  const int last = P.pieces - 1;
+  const int p0 = (int)min(cut.piece_of(begin), (unsigned)last);
+  const int p1 = (int)min(cut.piece_of(begin + w.chunks - 1), (unsigned)last);
   pdl_wait();
+  if (p0 >= p1) return;  // written by its piece
   const int np = p1 - p0 + 1, cols = min(NC, it.n * P.G - it.ct * NC);
   // part of piece p0 + p: it begins the item in its second slot
   auto part = [&](int p) {

@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
   volatile int* abort = &S.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  pdl_trigger();
 
   // The tile: slots as in the other kernels; the last ones (more keys) first.
   const long long u = gridDim.x - 1 - blockIdx.x;
@@ -222,6 +221,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
   fence_before();
   __syncthreads();
   fence_after();
+  // Not before tensor memory is allocated: the next kernel's CTAs may take
+  // theirs before they wait for this grid, and hold it until they have.
+  pdl_trigger();
   const uint32_t tmem = S.tmem;
   bool ok = true;
 
