@@ -332,3 +332,31 @@ def test_a_pool_beyond_32_bit_offsets():
     want, tol = reference(host64(q), kh, vh, 16, Hkv, D, D ** -0.5, "int8", False, True)
     # (the gathered values are rounded to fp32: u each)
     assert np.all(np.abs(host64(out) - want) <= tol + 4 * U * np.abs(vh).max())
+
+
+def test_rows_of_values_that_are_not_finite():
+    """Whole rows of V past the first prompt rows are infinite or NaN in more
+    than half of their dims; the other dims are as if nothing had happened."""
+    D, H, Hkv, rows = 128, 4, 2, 300
+    L = rows + 40
+    cache = Cache("bf16", 1, Hkv, D, 64, L, [L], 950)
+    k, v = cache.values(0, L)
+    bad = {L - 1: (0x7F80, slice(0, 100)), L - 20: (0xFF80, slice(20, 90)),
+           L - 3: (0x7FC0, slice(64, 80)), 17: (0x7F80, slice(0, 1))}
+    for t, (bits, dims) in bad.items():
+        p, r = cache.place(0, t)
+        cache.v[p, 1, r, dims] = bits
+    got, q = run(cache, [rows], [L], H, BF, BF, 951)
+    want, tol = reference(q, k, v, H, Hkv, D, 1 / math.sqrt(D), "bf16", False, True)
+    g, w, t = (a.reshape(rows, H, D) for a in (got, want, tol))
+    hit = np.zeros((rows, H, D), bool)
+    for at, (_, dims) in bad.items():
+        hit[max(0, at - (L - rows)):, 2:, dims] = True
+    assert not np.isfinite(g[hit]).any()
+    assert np.all(np.abs(g[~hit] - w[~hit]) <= t[~hit])
+    # which kind: the last row sees +inf at dims 0..99, -inf at 20..89, NaN at 64..79
+    last = g[-1, 2:]
+    assert np.isposinf(last[:, 1:20]).all() and np.isnan(last[:, 20:90]).all()
+    assert np.isposinf(last[:, 90:100]).all()
+    before = g[-2, 2:]
+    assert np.isneginf(before[:, 20:64]).all() and np.isnan(before[:, 64:80]).all()

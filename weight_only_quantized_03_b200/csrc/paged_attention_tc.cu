@@ -22,10 +22,10 @@
 // CTA an SM would halve S's operand reads, but leave each phase's waits bare.
 //
 // A value of V that is infinite or NaN at a token that some of the rows do
-// not see must not reach them as 0 * inf: it is taken out of the operand and
-// added at the end to the rows that see it (bf16 pages; under an int8 block's
-// NaN scale the weights of rows that do not see it are exact zeros and the
-// codes are finite).
+// not see must not reach them as 0 * inf: it is left out of the operand, and
+// in the end the rows that see such values read them again and add them (bf16
+// pages; under an int8 block's NaN scale the weights of rows that do not see
+// it are exact zeros and the codes are finite).
 //
 // Every wait is bounded (1 s). One that gives up ends the CTA's work; its
 // rows are then NaN.
@@ -46,7 +46,6 @@ using namespace tc;
 constexpr int kRows = 128;         // rows of a CTA
 constexpr int kKeys = 64;          // keys of a step
 constexpr int kPThreads = 288;     // 4 softmax warps, 4 loading warps, the issuing warp
-constexpr int kOdd = 32;           // V values that are not finite, kept aside
 constexpr int kTmemCols = 256;
 constexpr int kScol = 128;         // S buffers at columns 128 and 192; O at 0
 
@@ -62,9 +61,7 @@ struct PromptShared {  // behind the operands
   float unit[kRows];   // of each pair's q
   uint32_t tmem;
   int abort;
-  int odd_n, odd_from;  // entries below; the first token of one that found no room
-  int odd_key[kOdd], odd_dim[kOdd];
-  float odd_val[kOdd];
+  int odd;             // values of V that are not finite were left out
 };
 
 #define QG_R8(a, i) "r"((a)[i]), "r"((a)[i + 1]), "r"((a)[i + 2]), "r"((a)[i + 3]), \
@@ -208,8 +205,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     mbar_init(&S.o_full, 1);
     mbar_init(&S.drain, 1);
     S.abort = 0;
-    S.odd_n = 0;
-    S.odd_from = INT_MAX;
+    S.odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -427,19 +423,14 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     if (!ok) *abort = 1;
     fence_after();
     const float f = l != 0.f ? (I8 ? r * (1.f / 2048.f) : 1.f) / l : 0.f;
-    const int odd = min(S.odd_n, kOdd);
-    const bool lost = !ok || lim > S.odd_from;
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       uint32_t o[32];
       tmem_ld32(lanes + d, o);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        float x = __uint_as_float(o[i]) * f;
-        if (!I8)
-          for (int k = 0; k < odd; ++k)
-            if (S.odd_dim[k] == d + i && S.odd_key[k] < lim) x += S.odd_val[k];
-        o[i] = __float_as_uint(lost ? __int_as_float(0x7FC00000) : x);
+        const float x = __uint_as_float(o[i]) * f;
+        o[i] = __float_as_uint(ok ? x : __int_as_float(0x7FC00000));
       }
       if (real)
 #pragma unroll
@@ -451,6 +442,32 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
           w.w = mm::pack_bf16(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
           *reinterpret_cast<uint4*>(out + d + i) = w;
         }
+    }
+    if (!I8 && S.odd && real) {  // (rare) what was left out, to the rows that see it
+#pragma unroll 1
+      for (int d = 0; d < D; d += 8) {
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int key = common / kKeys * kKeys; key < lim; ++key) {
+          const int blk = key / kBlock, pi = blk / P.bpp;
+          const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
+          if (page < 0 || page >= P.num_pages) continue;
+          const long long row =
+              ((long long)(page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)) * kBlock +
+              key % kBlock;
+          const uint4 w = __ldcg(reinterpret_cast<const uint4*>(P.vp + (row * D + d) * 2));
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t bits = e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16;
+            if ((bits & 0x7F800000u) == 0x7F800000u) sum[e] += __uint_as_float(bits);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (sum[e] != 0.f)
+            out[d + e] = f32_to_bf16_bits(bf16_bits_to_f32(out[d + e]) + sum[e]);
+      }
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ the pages
@@ -498,8 +515,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       scale = load_if(P.ks + id, scaled, id == -1 ? __int_as_float(0x7FC00000) : 1.f);
       vscale = load_if(P.vs + id, scaled, 1.f);
     };
-    // bf16: values of V that are not finite out of the operand, aside
-    auto set_aside = [&](int j) {
+    // bf16: values of V that are not finite out of the operand
+    auto leave_out = [&]() {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -508,21 +525,12 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         for (int e = 0; e < 4; ++e)
           odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
         if (!odd) continue;
-        const int key = j * kKeys + i * (64 / CPR) + row0, d0 = cc * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t bits = e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
-          if ((bits & 0x7F800000u) != 0x7F800000u) continue;
-          w[e / 2] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
-          const int k = atomicAdd(&S.odd_n, 1);
-          if (k < kOdd) {
-            S.odd_key[k] = key;
-            S.odd_dim[k] = d0 + e;
-            S.odd_val[k] = __uint_as_float(bits);
-          } else {
-            atomicMin(&S.odd_from, key);
-          }
+        for (int e = 0; e < 4; ++e) {
+          if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+          if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
         }
+        S.odd = 1;
         x[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         break;
       }
       // (some rows do not see all of a partly masked step's tokens)
-      if (!I8 && isv && j * kKeys + kKeys > common) set_aside(j);
+      if (!I8 && isv && j * kKeys + kKeys > common) leave_out();
       uint8_t* const dst = buf + b * L::kKV;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
