@@ -621,6 +621,8 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
     S.hist_w0[i] = S.hist_w1[i] = S.hist_w2[i] = 0;
   }
   if (tid < kSteps) S.pow2[tid] = P.pow2[tid];
+  // the other CTAs run, before anything is written into their shared memory
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_wait();
   const float T = P.temperature ? __ldcg(P.temperature + b) : 1.f;
   const int top_k = P.top_k ? __ldcg(P.top_k + b) : 0;
@@ -666,6 +668,7 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
     S.red2[warp] = lo;
     S.red3[warp] = cnt;
   }
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   __syncthreads();
   if (warp == 0) {  // to every rank
     hi = warp_max64(lane < NTHR / 32 ? S.red[lane] : 0);
