@@ -491,9 +491,9 @@ typedef struct qg_paged_kv {
  * rows' values of that head (0 below 2^-126). The rows before o are brought
  * to it, code <- rint(code * (s_old / s)) (half a step of s at most per
  * change), and the new rows get code = clamp(rint(x / s), -127, 127), both in
- * fp32 (all 0 where s is 0). Rows after the new ones stay as they are. A NaN or infinite value, or a NaN
- * s_old, makes s NaN, and with it every value of the block until a call
- * writes the block from its first row again.
+ * fp32 (all 0 where s is 0). Rows after the new ones stay as they are. A NaN
+ * or infinite value, or a NaN s_old, makes s NaN, and with it every value of
+ * the block until a call writes the block from its first row again.
  *
  * page_table device int32 [B][max_pages]; only entries of tokens that get
  *            rows are read. A page outside [0, num_pages): its K/V rows are
@@ -509,7 +509,8 @@ typedef struct qg_paged_kv {
  *            the types match and q_ld = H * head_dim.
  * Pages that get rows must not be shared by two sequences of the call.
  * Angles are formed in float64 and reduced there; sine and cosine are fp32.
- * q, k, v rows must start on 16 bytes; B, T, H >= 0, max_pages >= 0. */
+ * q, k, v rows must start on 16 bytes; 0 <= B <= 65536, 0 <= T <= 2^28,
+ * 0 <= H <= 8192, max_pages >= 0. */
 qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
                              const int32_t* kv_len, const int32_t* row_start, const void* q,
                              long long q_ld, const void* k, long long k_ld, const void* v,
@@ -522,7 +523,7 @@ qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* page_table, i
  * first[b] + i (first NULL: 0). k_out, v_out device [T][kv_heads * head_dim]
  * of out_dtype (either may be NULL). A token index outside
  * [0, max_pages * page_size) or a page outside [0, num_pages) gives NaN.
- * row_start as above, NULL: one row each. */
+ * row_start as above, NULL: one row each. B and T as above. */
 qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
                              const int32_t* first, const int32_t* row_start, void* k_out,
                              void* v_out, qg_dtype out_dtype, int B, int T, void* stream);
@@ -534,7 +535,7 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  * each row sees the cached tokens up to its own, which qg_paged_kv_append
  * has written before.
  * q          device [T][H * head_dim] of q_dtype.
- * out        device [T][H * head_dim] of out_dtype.
+ * out        device [T][H * head_dim] of out_dtype; must not overlap q.
  * kv_len     device int32 [B]. Outside [n_b, max_pages * page_size], and 0:
  *            zero rows (nothing is read). A page outside [0, num_pages)
  *            gives NaN to the rows that see its tokens. Tokens past
@@ -547,6 +548,9 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  * bf16 values, q) but for the softmax weights (fp16 with int8 pages, bf16
  * with bf16 pages); sums, maxima and scales in fp32. With an fp32 q or out,
  * q and the weights are carried in several 16-bit terms (22 bits or more).
+ * Prompts (head_dim <= 128, bf16 q and out, 32 or more row-head pairs of a
+ * KV head per sequence on average) run on tcgen05; the waits inside that
+ * kernel are bounded in time (1 s), and one that gives up makes its rows NaN.
  * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0, and
  * (T * H / 8 + B * kv_heads) * (max_pages * page_size / 128 + 1) < 2^31. */
 size_t qg_paged_attention_workspace_size(int head_dim);

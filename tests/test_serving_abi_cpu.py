@@ -67,6 +67,17 @@ def test_append_refusals():
     assert _append(row_start=FAKE, T=0)[0] == qg.QG_OK
 
 
+def test_more_sequences_than_a_call_takes():
+    """Every block looks through the sequences: past 65536 that would take
+    the GPU for minutes."""
+    B = (1 << 16) + 1
+    st, msg = _append(B=B, T=B)
+    assert st == qg.QG_ERR_UNSUPPORTED_SHAPE and "too large" in msg
+    st, _ = _status("qg_paged_kv_gather", ctypes.byref(_kv()), FAKE, 4, FAKE, None, FAKE, FAKE,
+                    qg.QG_F32, B, B, None)
+    assert st == qg.QG_ERR_UNSUPPORTED_SHAPE
+
+
 def test_gather_refusals():
     ref = ctypes.byref(_kv())
     g = lambda *a: _status("qg_paged_kv_gather", ref, *a, None)

@@ -578,7 +578,7 @@ extern "C" qg_status qg_paged_kv_append(const qg_paged_kv* kv, const int32_t* pa
   const int D = kv->head_dim, Hkv = kv->kv_heads;
   QG_REQUIRE(B >= 0 && T >= 0 && H >= 0 && H <= 8192, QG_ERR_UNSUPPORTED_SHAPE,
              "%s: B=%d T=%d H=%d", who, B, T, H);
-  QG_REQUIRE(B <= (1 << 24) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE, "%s: B=%d T=%d too large",
+  QG_REQUIRE(B <= (1 << 16) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE, "%s: B=%d T=%d too large",
              who, B, T);
   QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
              "%s: T=%d rows without row_start must be B=%d", who, T, B);
@@ -665,7 +665,7 @@ extern "C" qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* pa
   clear_error();
   const char* who = "qg_paged_kv_gather";
   if (qg_status s = pk::check_pool(who, kv, max_pages)) return s;
-  QG_REQUIRE(B >= 0 && T >= 0 && B <= (1 << 24) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE,
+  QG_REQUIRE(B >= 0 && T >= 0 && B <= (1 << 16) && T <= (1 << 28), QG_ERR_UNSUPPORTED_SHAPE,
              "%s: B=%d T=%d", who, B, T);
   QG_REQUIRE(row_start || T == B, QG_ERR_UNSUPPORTED_SHAPE,
              "%s: T=%d rows without row_start must be B=%d", who, T, B);
