@@ -360,3 +360,31 @@ def test_rows_of_values_that_are_not_finite():
     assert np.isposinf(last[:, 90:100]).all()
     before = g[-2, 2:]
     assert np.isneginf(before[:, 20:64]).all() and np.isnan(before[:, 64:80]).all()
+
+
+@pytest.mark.parametrize("case", [
+    ("int8", 128, 64, 4, 2, [40, 0, 33], [2100, 0, 35]),
+    ("int8", 64, 16, 16, 1, [9, 200], [2053, 200]),
+    ("bf16", 128, 32, 16, 16, [65], [1100]),
+    ("bf16", 64, 16, 6, 2, [50, 1], [2113, 700]),
+    ("bf16", 128, 128, 16, 1, [70, 5, 2], [1000, 5, 900]),
+], ids=lambda c: f"{c[0]}-d{c[1]}-h{c[3]}.{c[4]}-n{c[5]}-l{c[6]}")
+def test_few_prompt_rows_over_many_tokens(case):
+    """A tile's keys shared by up to eight blocks, some of them without any."""
+    kind, D, page, H, Hkv, n, lens = case
+    check(kind, D, page, H, Hkv, n, lens, BF, BF, 970, cap=max(lens) + 50, pad=5)
+
+
+def test_prompt_rows_of_a_wrong_length_beside_a_long_cache():
+    """kv_len below the sequence's rows: zero rows, the others as they are."""
+    D, H, Hkv, n = 128, 4, 2, [33, 64, 20]
+    lens = [2100, 64, 2090]
+    cache = Cache("int8", 3, Hkv, D, 64, 2200, lens, 980)
+    got, q = run(cache, n, [2100, 10, 2090], H, BF, BF, 981)
+    r0 = starts(n)
+    assert np.all(got[r0[1]:r0[2]] == 0.0)
+    for b in (0, 2):
+        k, v = cache.values(b, lens[b])
+        rows = slice(r0[b], r0[b + 1])
+        want, tol = reference(q[rows], k, v, H, Hkv, D, 1 / math.sqrt(D), "int8", False, True)
+        assert np.all(np.abs(got[rows] - want) <= tol)

@@ -52,13 +52,16 @@ constexpr int kScol = 128;         // S buffers at columns 128 and 192; O at 0
 template <int D>
 struct PromptSmem {
   static constexpr int kQ = kRows * D * 2, kKV = kKeys * D * 2;
-  static constexpr int kBytes = 1024 + kQ + 4 * kKV + 1536;
+  static constexpr int kTail = 2560;  // PromptShared
+  static constexpr int kBytes = 1024 + kQ + 4 * kKV + kTail;
 };
 
 struct PromptShared {  // behind the operands
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
   float scale[4][8];   // ring: a step's K and V scales (4 blocks of 16 tokens each)
   float unit[kRows];   // of each pair's q
+  float m[kRows], l[kRows];  // what a pair's keys gave (clusters)
+  float factor[kRows];       // of each CTA's part of the pairs written here
   uint32_t tmem;
   int abort;
   int odd;             // values of V that are not finite were left out
@@ -129,10 +132,107 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t panel) {
 }
 constexpr uint32_t kBisMnMajor = 1u << 16;  // instruction descriptor: B is MN-major
 
+// Clusters: another CTA's shared memory at the address of `p`.
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float remote_f32(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 remote_f32x4(const uint8_t* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Byte offset of 16-byte chunk c (8 dims) of a row in panels of 64 dims.
 template <int ROWS>
 __device__ __forceinline__ int at_chunk(int row, int c) {
   return (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// Byte offset of 4 dims (chunk c) of a pair's result: pairs 512 (256) bytes
+// apart, chunks exchanged by the pair so that neighbours' stores meet other
+// banks.
+template <int D>
+__device__ __forceinline__ int part_at(int pair, int c) {
+  return pair * (D * 4) + ((c ^ (pair & (D / 4 - 1))) << 4);
+}
+
+// A cluster's results of its tile: CTA z takes 128 / Z pairs from all of them
+// (a softmax's parts: each has its reference m, its weights' sum l, and its
+// output divided by l) and writes them out. Loads from the others' shared
+// memory take several hundred cycles: a thread's go out together. Returns
+// whether any CTA left V values out.
+template <int D, int Z, class F>
+__device__ __forceinline__ int join(PromptShared& S, const uint8_t* parts, int z, int first,
+                                    int cols, F out_at) {
+  constexpr int N = kRows / Z, C = D / 8;  // pairs, chunks of 8 dims
+  const int tid = threadIdx.x;
+  int odd = 0;
+  if (tid < N) {  // the pair's factors
+    float m[Z], l[Z], M = -FLT_MAX, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < Z; ++k) {
+      m[k] = remote_f32(&S.m[z * N + tid], k);
+      l[k] = remote_f32(&S.l[z * N + tid], k);
+    }
+#pragma unroll
+    for (int k = 0; k < Z; ++k) M = fmaxf(M, m[k]);
+#pragma unroll
+    for (int k = 0; k < Z; ++k) {
+      l[k] *= ex2(m[k] - M);
+      L += l[k];
+    }
+    const float f = L != 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int k = 0; k < Z; ++k) S.factor[k * N + tid] = l[k] * f;
+  }
+  {
+    int o[Z];
+#pragma unroll
+    for (int k = 0; k < Z; ++k) o[k] = __float_as_int(remote_f32((const float*)&S.odd, k));
+#pragma unroll
+    for (int k = 0; k < Z; ++k) odd |= o[k];
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int i = tid; i < N * C; i += kPThreads) {
+    const int pair = i / C, d = i % C;
+    float4 y[Z][2];
+#pragma unroll
+    for (int k = 0; k < Z; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        y[k][e] = remote_f32x4(parts + part_at<D>(z * N + pair, 2 * d + e), k);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < Z; ++k) {
+      const float a = S.factor[k * N + pair];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[4 * e] = fmaf(a, y[k][e].x, x[4 * e]);
+        x[4 * e + 1] = fmaf(a, y[k][e].y, x[4 * e + 1]);
+        x[4 * e + 2] = fmaf(a, y[k][e].z, x[4 * e + 2]);
+        x[4 * e + 3] = fmaf(a, y[k][e].w, x[4 * e + 3]);
+      }
+    }
+    if (first + z * N + pair < cols)
+      *reinterpret_cast<uint4*>(out_at(z * N + pair) + 8 * d) =
+          make_uint4(mm::pack_bf16(x[0], x[1]), mm::pack_bf16(x[2], x[3]),
+                     mm::pack_bf16(x[4], x[5]), mm::pack_bf16(x[6], x[7]));
+  }
+  return odd;
 }
 
 template <int D, bool I8>
@@ -178,18 +278,35 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
   // tokens that the last pair sees, and that all pairs see
   const int keys = it.len ? before + (min(first + kRows, cols) - 1) / P.G + 1 : 0;
   const int common = before + first / P.G + 1;
-  const int steps = (keys + kKeys - 1) / kKeys;
+  const int all = (keys + kKeys - 1) / kKeys;
+  // the steps of this CTA of the cluster: key0 / 64 of them lie before
+  const int Z = gridDim.z, z = blockIdx.z;
+  const int j0 = (int)((long long)all * z / Z), steps = (int)((long long)all * (z + 1) / Z) - j0;
+  const int key0 = j0 * kKeys;
 
   // softmax threads: their pair's place in q and out
   const int c = first + tid, ri = c / P.G;
   const bool real = tid < kRows && c < cols;
-  const long long at =
-      ((long long)(it.r0 + (real ? ri : 0)) * P.H + it.h * P.G + (real ? c - ri * P.G : 0)) * D;
-  uint16_t* out = reinterpret_cast<uint16_t*>(P.out) + at;
-  if (steps == 0) {
-    if (real)
+  const int at = real ? (it.r0 + ri) * P.H + it.h * P.G + (c - ri * P.G) : -1;  // (below 2^30)
+  uint16_t* out = reinterpret_cast<uint16_t*>(P.out) + (long long)(real ? at : 0) * D;
+  if (all == 0) {
+    if (real && z == 0)
       for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
     return;
+  }
+
+  // A softmax warp brings its own 32 pairs of q, whole rows at a time; the
+  // loads are under way while the barriers and tensor memory are set up.
+  constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a load
+  const int cc = lane % LPR;
+  uint4 x[LPR];
+  if (warp < 4 && steps) {
+#pragma unroll
+    for (int i = 0; i < LPR; ++i) {
+      const int from = __shfl_sync(0xffffffffu, at, i * RPI + lane / LPR);
+      x[i] = load16_if(reinterpret_cast<const uint8_t*>(P.q) + ((long long)from * D + cc * 8) * 2,
+                       from >= 0);
+    }
   }
 
   if (tid == 0) {
@@ -227,45 +344,38 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     // ------------------------------------------------------------ the rows
     const int lim = real ? before + ri + 1 : INT_MAX;  // tokens the pair sees
     float qf = P.scale_log2;
-    {
-      // q into shared memory, for int8 pages times a power of two, as fp16. A
-      // warp brings its own 32 pairs, whole rows at a time.
-      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a load
-      const int cc = lane % LPR;
+    if (steps) {
+      // q into shared memory, for int8 pages times a power of two, as fp16
+      if constexpr (I8) {
+        // two 16-bit maxima a word: magnitudes order as integers. Rows side by
+        // side, so that their exchanges overlap
+        uint32_t top[LPR];
 #pragma unroll
-      for (int i0 = 0; i0 < LPR; i0 += 8) {
-        uint4 x[8];
+        for (int i = 0; i < LPR; ++i)
+          top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                            __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int cq = first + 32 * warp + (i0 + i) * RPI + lane / LPR, rq = cq / P.G;
-          const bool in = cq < cols;
-          const long long from =
-              ((long long)(it.r0 + (in ? rq : 0)) * P.H + it.h * P.G + (in ? cq - rq * P.G : 0)) * D;
-          x[i] = load16_if(reinterpret_cast<const uint8_t*>(P.q) + 2 * (from + cc * 8), in);
-        }
+        for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 32 * warp + (i0 + i) * RPI + lane / LPR;
-          if constexpr (I8) {
-            // two 16-bit maxima: magnitudes order as integers
-            uint32_t top = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                                    __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+          for (int i = 0; i < LPR; ++i)
+            top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1)
-              top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float unit = q_unit(fmaxf(bf16_lo(top), bf16_hi(top)));
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < LPR; ++i) {
+          const float unit = q_unit(fmaxf(bf16_lo(top[i]), bf16_hi(top[i])));
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * unit, bf16_hi(w[e]) * unit);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (cc == 0) S.unit[row] = unit;
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(bf16_lo(w[e]) * unit, bf16_hi(w[e]) * unit);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          *reinterpret_cast<uint4*>(sq + at_chunk<kRows>(row, cc)) = x[i];
+          x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (cc == 0) S.unit[32 * warp + i * RPI + lane / LPR] = unit;
         }
       }
+#pragma unroll
+      for (int i = 0; i < LPR; ++i)
+        *reinterpret_cast<uint4*>(
+            sq + at_chunk<kRows>(32 * warp + i * RPI + lane / LPR, cc)) = x[i];
       __syncwarp();
       if constexpr (I8) qf /= S.unit[tid];
     }
@@ -288,8 +398,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         ks[i] = S.scale[j & 3][i] * qf;
         vs[i] = I8 ? S.scale[j & 3][4 + i] : 1.f;
       }
-      const bool part = j * kKeys + kKeys > common;
-      const int left = lim - j * kKeys;  // visible tokens of this step (or more, or none)
+      const bool part = key0 + j * kKeys + kKeys > common;
+      const int left = lim - key0 - j * kKeys;  // visible tokens of this step (or more, or none)
       // The row's largest score. A negative scale turns the order round.
       auto largest = [&]() {
         float top = -FLT_MAX;
@@ -419,20 +529,30 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       fence_before();
       mbar_arrive(&S.p_full[b]);
     }
-    if (ok && !wait_bar(&S.o_full, (uint32_t)(steps - 1) & 1u, abort)) ok = false;
+    if (ok && steps && !wait_bar(&S.o_full, (uint32_t)(steps - 1) & 1u, abort)) ok = false;
     if (!ok) *abort = 1;
     fence_after();
     const float f = l != 0.f ? (I8 ? r * (1.f / 2048.f) : 1.f) / l : 0.f;
+    const float lost = __int_as_float(0x7FC00000);
+    S.m[tid] = m;
+    S.l[tid] = ok ? l : lost;
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       uint32_t o[32];
-      tmem_ld32(lanes + d, o);
+      if (steps)
+        tmem_ld32(lanes + d, o);
+      else
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float x = __uint_as_float(o[i]) * f;
-        o[i] = __float_as_uint(ok ? x : __int_as_float(0x7FC00000));
-      }
-      if (real)
+        for (int i = 0; i < 32; ++i) o[i] = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        o[i] = __float_as_uint(ok ? __uint_as_float(o[i]) * f : lost);
+      if (Z > 1) {  // to where Q and K were: every product is done
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(smem + part_at<D>(tid, (d + i) / 4)) =
+              make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      } else if (real) {
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint4 w;
@@ -442,31 +562,6 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
           w.w = mm::pack_bf16(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
           *reinterpret_cast<uint4*>(out + d + i) = w;
         }
-    }
-    if (!I8 && S.odd && real) {  // (rare) what was left out, to the rows that see it
-#pragma unroll 1
-      for (int d = 0; d < D; d += 8) {
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int key = common / kKeys * kKeys; key < lim; ++key) {
-          const int blk = key / kBlock, pi = blk / P.bpp;
-          const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
-          if (page < 0 || page >= P.num_pages) continue;
-          const long long row =
-              ((long long)(page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)) * kBlock +
-              key % kBlock;
-          const uint4 w = __ldcg(reinterpret_cast<const uint4*>(P.vp + (row * D + d) * 2));
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t bits = e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16;
-            if ((bits & 0x7F800000u) == 0x7F800000u) sum[e] += __uint_as_float(bits);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (sum[e] != 0.f)
-            out[d + e] = f32_to_bf16_bits(bf16_bits_to_f32(out[d + e]) + sum[e]);
       }
     }
   } else if (warp < 8) {
@@ -485,12 +580,12 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     // before it is looked at; from it the block's place in the pool, -1 for a
     // bad page, -2 past the keys.
     auto page_of = [&](int base) {
-      const int blk = base + lane;
+      const int blk = key0 / kBlock + base + lane;
       return blk * kBlock < keys ? __ldcg(P.table + (long long)it.b * P.max_pages + blk / P.bpp)
                                  : -1;
     };
     auto place_of = [&](int base, int page) {
-      const int blk = base + lane;
+      const int blk = key0 / kBlock + base + lane;
       if (blk * kBlock >= keys) return -2;
       return page >= 0 && page < P.num_pages
                  ? (page * P.Hkv + it.h) * P.bpp + (blk - blk / P.bpp * P.bpp)
@@ -499,79 +594,126 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     // Thread t's chunk i: 64 / CPR rows further than chunk i - 1, the same
     // place in the row; 64 chunks never pass a block of 16 rows.
     const int row0 = t / CPR, cc = t % CPR;
-    uint4 x[R];
-    float scale = 1.f, vscale = 1.f;  // lanes 0-3 of warp 4; a bad page gives NaN scores
-    auto load = [&](int j, int places) {
-      const int from = j * 4 % 32;  // the step's blocks: lanes from .. from + 3
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int blk = __shfl_sync(0xffffffffu, places, from + i * 64 / (kBlock * CPR));
-        const bool in = blk >= 0 && (I8 || !isv || j * kKeys + i * (64 / CPR) + row0 < it.len);
-        x[i] = load16_if(pool + (long long)blk * (kBlock * D * ES) +
-                             (i * 64 % (kBlock * CPR) + t) * 16, in);
-      }
-      const int id = __shfl_sync(0xffffffffu, places, from + (lane & 3));
-      const bool scaled = I8 && warp == 4 && id >= 0;
-      scale = load_if(P.ks + id, scaled, id == -1 ? __int_as_float(0x7FC00000) : 1.f);
-      vscale = load_if(P.vs + id, scaled, 1.f);
-    };
-    // bf16: values of V that are not finite out of the operand
-    auto leave_out = [&]() {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        bool odd = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          odd |= (w[e] & 0x7F800000u) == 0x7F800000u || (w[e] & 0x7F80u) == 0x7F80u;
-        if (!odd) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-          if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-        }
-        S.odd = 1;
-        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    const auto wait_empty = [&](int j) {
+      return j < 2 || wait_bar(&empty[j & 1], (uint32_t)((j >> 1) + 1) & 1u, abort);
     };
     int page = page_of(0), places = place_of(0, page);
-    load(0, places);
-    for (int j = 0; j < steps; ++j) {
-      const int b = j & 1;
-      if (j >= 2 && !wait_bar(&empty[b], (uint32_t)((j >> 1) + 1) & 1u, abort)) {
-        ok = false;
-        break;
-      }
-      // (some rows do not see all of a partly masked step's tokens)
-      if (!I8 && isv && j * kKeys + kKeys > common) leave_out();
-      uint8_t* const dst = buf + b * L::kKV;
+    const auto look = [&](int j) {  // before step j's loads
+      if (j % 8 == 7) page = page_of(4 * (j + 1));
+      if (j % 8 == 0) places = place_of(4 * j, page);
+    };
+    if constexpr (I8) {
+      uint4 x[R];
+      float scale = 1.f, vscale = 1.f;  // lanes 0-3 of warp 4; a bad page gives NaN scores
+      auto load = [&](int j) {
+        const int from = j * 4 % 32;  // the step's blocks: lanes from .. from + 3
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int row = i * (64 / CPR) + row0;
-        if constexpr (I8) {
+        for (int i = 0; i < R; ++i) {
+          const int blk = __shfl_sync(0xffffffffu, places, from + i * 64 / (kBlock * CPR));
+          x[i] = load16_if(pool + (long long)blk * (kBlock * D) + (i * 64 % (kBlock * CPR) + t) * 16,
+                           blk >= 0);
+        }
+        const int id = __shfl_sync(0xffffffffu, places, from + (lane & 3));
+        const bool scaled = warp == 4 && id >= 0;
+        scale = load_if(P.ks + id, scaled, id == -1 ? __int_as_float(0x7FC00000) : 1.f);
+        vscale = load_if(P.vs + id, scaled, 1.f);
+      };
+      if (steps) load(0);
+      for (int j = 0; j < steps; ++j) {
+        const int b = j & 1;
+        if (!wait_empty(j)) {
+          ok = false;
+          break;
+        }
+        uint8_t* const dst = buf + b * L::kKV;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int row = i * (64 / CPR) + row0;
           const uint32_t w[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u,
                                  x[i].w ^ 0x80808080u};
           *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc)) =
               make_uint4(codes01(w[0]), codes23(w[0]), codes01(w[1]), codes23(w[1]));
           *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, 2 * cc + 1)) =
               make_uint4(codes01(w[2]), codes23(w[2]), codes01(w[3]), codes23(w[3]));
-        } else {
-          *reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(row, cc)) = x[i];
+        }
+        // A ring of four steps. The rows read a step's scales once its S is full,
+        // before V need be there, so K's warps bring V's scales too.
+        if (!isv && t < 4) {
+          S.scale[j & 3][t] = scale;
+          S.scale[j & 3][4 + t] = vscale;
+        }
+        fence_async();
+        mbar_arrive(&full[b]);
+        if (j + 1 < steps) {
+          look(j + 1);
+          load(j + 1);
         }
       }
-      // A ring of four steps. The rows read a step's scales once its S is full,
-      // before V need be there, so K's warps bring V's scales too.
-      if (!isv && t < 4) {
-        S.scale[j & 3][t] = scale;
-        S.scale[j & 3][4 + t] = vscale;
+    } else {
+      // bf16 values go to shared memory as they are, by asynchronous copies a
+      // step ahead (through registers the two steps in flight took 64 of them).
+      const uint32_t to = smem_u32(buf);
+      auto send = [&](int j) {
+        if (!wait_empty(j)) return false;
+        const int from = j * 4 % 32;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int blk = __shfl_sync(0xffffffffu, places, from + i * 64 / (kBlock * CPR));
+          const int row = i * (64 / CPR) + row0;
+          const bool in = blk >= 0 && (!isv || key0 + j * kKeys + row < it.len);
+          const uint8_t* p = pool + (long long)(in ? blk : 0) * (kBlock * D * ES) +
+                             (i * 64 % (kBlock * CPR) + t) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           to + (uint32_t)((j & 1) * L::kKV + at_chunk<kKeys>(row, cc))),
+                       "l"(p), "r"(in ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        // (the ring's place of step j - 4: its rows are done, or S of step j - 2
+        // would not have been issued)
+        const int id = __shfl_sync(0xffffffffu, places, from + (lane & 3));
+        if (!isv && t < 4) S.scale[j & 3][t] = id == -1 ? __int_as_float(0x7FC00000) : 1.f;
+        return true;
+      };
+      // values of V that are not finite out of the operand, each thread its own
+      auto leave_out = [&](uint8_t* dst) {
+#pragma unroll 1
+        for (int i = 0; i < R; ++i) {
+          uint4* const at =
+              reinterpret_cast<uint4*>(dst + at_chunk<kKeys>(i * (64 / CPR) + row0, cc));
+          const uint4 x = *at;
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool hi = (w[e] & 0x7F800000u) == 0x7F800000u, lo = (w[e] & 0x7F80u) == 0x7F80u;
+            odd |= hi || lo;
+            if (hi) w[e] &= 0xFFFFu;
+            if (lo) w[e] &= 0xFFFF0000u;
+          }
+          if (!odd) continue;
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
+          S.odd = 1;
+        }
+      };
+      if (steps) ok = send(0);
+      for (int j = 0; ok && j < steps; ++j) {
+        if (j + 1 < steps) {
+          look(j + 1);
+          if (!send(j + 1)) {
+            ok = false;
+            break;
+          }
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        // (some rows do not see all of a partly masked step's tokens)
+        if (isv && key0 + j * kKeys + kKeys > common) leave_out(buf + (j & 1) * L::kKV);
+        fence_async();
+        mbar_arrive(&full[j & 1]);
       }
-      fence_async();
-      mbar_arrive(&full[b]);
-      if (j + 1 < steps) {
-        if ((j + 1) % 8 == 7) page = page_of(4 * (j + 2));
-        if ((j + 1) % 8 == 0) places = place_of(4 * (j + 1), page);
-        load(j + 1, places);
-      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (!ok) *abort = 1;
   } else {
@@ -612,7 +754,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       }
       __syncwarp();
     };
-    if (wait(&S.q_full, 0)) issue_s(0);
+    if (wait(&S.q_full, 0) && steps) issue_s(0);
     for (int j = 0; ok && j < steps; ++j) {
       const int b = j & 1;
       if (j + 1 < steps) issue_s(j + 1);
@@ -643,22 +785,96 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     }
   }
   fence_before();
-  __syncthreads();
+  if (Z > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == 8) {
     __syncwarp();
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
+  // place of one of the tile's pairs in out
+  const auto out_at = [&](int pair) {
+    const int cp = first + pair, rp = cp / P.G;
+    return reinterpret_cast<uint16_t*>(P.out) +
+           ((long long)(it.r0 + rp) * P.H + it.h * P.G + (cp - rp * P.G)) * D;
+  };
+  int odd = S.odd;
+  const int mine = kRows / Z;  // pairs that this CTA writes
+  if (Z > 1) {
+    if (Z == 2)
+      odd = join<D, 2>(S, smem, z, first, cols, out_at);
+    else if (Z == 4)
+      odd = join<D, 4>(S, smem, z, first, cols, out_at);
+    else
+      odd = join<D, 8>(S, smem, z, first, cols, out_at);
+    cluster_sync();  // nobody ends while its shared memory is read
+  }
+  if (!I8 && odd) {  // (rare) V values that were left out, to the rows that see them
+    __syncthreads();
+    const int pair = z * mine + tid, seen = before + (first + pair) / P.G + 1;
+    if (tid >= mine || first + pair >= cols) return;
+    uint16_t* const o = out_at(pair);
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+      float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int key = common / kKeys * kKeys; key < seen; ++key) {
+        const int blk = key / kBlock, pi = blk / P.bpp;
+        const int page = __ldcg(P.table + (long long)it.b * P.max_pages + pi);
+        if (page < 0 || page >= P.num_pages) continue;
+        const long long row =
+            ((long long)(page * P.Hkv + it.h) * P.bpp + (blk - pi * P.bpp)) * kBlock + key % kBlock;
+        const uint4 w = __ldcg(reinterpret_cast<const uint4*>(P.vp + (row * D + d) * 2));
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t bits = e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16;
+          if ((bits & 0x7F800000u) == 0x7F800000u) sum[e] += __uint_as_float(bits);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (sum[e] != 0.f)
+          o[d + e] = f32_to_bf16_bits(bf16_bits_to_f32(o[d + e]) + sum[e]);
+    }
+  }
+}
+
+// CTAs of a cluster that share a tile's keys: as many as fit the GPU at once
+// (two an SM) with four steps each, should the sequences fill their pages.
+static int prompt_cluster(const Params& P) {
+  const long long tiles = ((long long)P.T * P.G / kRows + P.B / 2 + 1) * P.Hkv;
+  const long long steps = (long long)P.max_pages * P.bpp * kBlock / kKeys;
+  int z = 1;
+  while (z < 8 && tiles * 2 * z <= 2 * num_sms() && steps >= 8 * z) z *= 2;
+  return z;
 }
 
 template <int D, bool I8>
 static cudaError_t launch_prompt_kernel(const Params& P, cudaStream_t st) {
   const size_t smem = PromptSmem<D>::kBytes;
-  static_assert(sizeof(PromptShared) <= 1536, "PromptShared fits behind the operands");
+  static_assert(sizeof(PromptShared) <= PromptSmem<D>::kTail, "PromptShared fits behind the operands");
   ensure_smem((const void*)prompt_kernel<D, I8>, (int)smem);
   const long long slots = (long long)P.T * P.G / kRows + P.B;
-  return launch_pdl(prompt_kernel<D, I8>, dim3((unsigned)slots, P.Hkv), dim3(kPThreads), smem, st,
-                    true, P);
+  const int Z = prompt_cluster(P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)slots, P.Hkv, Z);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = Z;
+  cfg.attrs = attr;
+  cfg.numAttrs = Z > 1 ? 2 : 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<D, I8>, P);
 }
 
 cudaError_t launch_prompt(const Params& P, int D, bool i8, cudaStream_t st) {
