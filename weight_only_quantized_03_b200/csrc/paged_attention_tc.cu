@@ -248,32 +248,37 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
 
-  // The tile: slots as in the other kernels; the last ones (more keys) first.
-  const long long u = gridDim.x - 1 - blockIdx.x;
-  Item it = {-1, 0, 0, 0, 0, 0};
+  // The tile: long ones first, so that short ones fill the gaps at the end.
+  // The sequences (32 at a time) go by their length, a sequence's tiles from
+  // the last one back, heads side by side.
+  int slot = (int)(blockIdx.x / (unsigned)P.Hkv);
+  Item it = {-1, (int)blockIdx.x - slot * P.Hkv, 0, 0, 0, 0};
 #pragma unroll 1
   for (int b0 = 0; b0 < P.B && it.b < 0; b0 += 32) {
     Item mine = {-1, 0, 0, 0, 0, 0};
-    bool in = false;
-    if (b0 + lane < P.B) {
-      set_seq(P, mine, b0 + lane);
-      in = mine.n && u >= (long long)mine.r0 * P.G / kRows + mine.b &&
-           u <= (long long)(mine.r0 + mine.n) * P.G / kRows + mine.b;
+    if (b0 + lane < P.B) set_seq(P, mine, b0 + lane);
+    const int tiles = (mine.n * P.G + kRows - 1) / kRows;
+    int before = 0, all = 0;
+#pragma unroll 8
+    for (int o = 0; o < 32; ++o) {
+      const int ol = __shfl_sync(0xffffffffu, mine.len, o);
+      const int ot = __shfl_sync(0xffffffffu, tiles, o);
+      all += ot;
+      before += ol > mine.len || (ol == mine.len && o < lane) ? ot : 0;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const unsigned m = __ballot_sync(0xffffffffu, slot >= before && slot - before < tiles);
     if (m) {
       const int l = __ffs(m) - 1;
       it.b = __shfl_sync(0xffffffffu, mine.b, l);
       it.r0 = __shfl_sync(0xffffffffu, mine.r0, l);
       it.n = __shfl_sync(0xffffffffu, mine.n, l);
       it.len = __shfl_sync(0xffffffffu, mine.len, l);
+      it.ct = __shfl_sync(0xffffffffu, tiles - 1 - (slot - before), l);
     }
+    slot -= all;
   }
   if (it.b < 0) return;
-  it.ct = (int)(u - ((long long)it.r0 * P.G / kRows + it.b));
-  it.h = blockIdx.y;
   const int first = it.ct * kRows, cols = it.n * P.G;  // (row, head) pairs of the sequence
-  if (first >= cols) return;
   const int before = it.len - it.n;  // tokens cached before the rows
   // tokens that the last pair sees, and that all pairs see
   const int keys = it.len ? before + (min(first + kRows, cols) - 1) / P.G + 1 : 0;
@@ -860,7 +865,7 @@ static cudaError_t launch_prompt_kernel(const Params& P, cudaStream_t st) {
   const long long slots = (long long)P.T * P.G / kRows + P.B;
   const int Z = prompt_cluster(P);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)slots, P.Hkv, Z);
+  cfg.gridDim = dim3((unsigned)(slots * P.Hkv), 1, Z);
   cfg.blockDim = dim3(kPThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
