@@ -5,21 +5,33 @@
 // A CTA takes 128 (row, query head) pairs of one KV head of one sequence and
 // walks their keys 64 at a time: S = Q K^T and O += P V are tcgen05.mma with
 // M = 128, accumulators in tensor memory (O: head_dim columns, S: two buffers
-// of 64). Warps 4-7 bring K and V from the pages: int8 codes become fp16
-// (exact) on the way into shared memory, in the 128-byte swizzled layout, K
-// as the K-major operand and V, in the same [token][dim] order, as the
-// MN-major one. Warps 0-3 own a row a thread: no maximum or sum crosses
-// threads. They read S, form the weights with the lazy maximum of the decode
-// kernel and write them as 16-bit pairs over S, where the second product
-// reads them as its A operand. One thread of warp 8 issues the products; S of
-// the next keys is in flight while the rows work on the current ones.
+// of 64). Warps 4-7 bring K and V from the pages in the 128-byte swizzled
+// layout, K as the K-major operand and V, in the same [token][dim] order, as
+// the MN-major one: int8 codes become fp16 (exact) on the way through
+// registers, bf16 values come by asynchronous copies. Warps 0-3 own a row a
+// thread: no maximum or sum crosses threads. They read S, form the weights
+// with the lazy maximum of the decode kernel and write them as 16-bit pairs
+// over S, where the second product reads them as its A operand. One thread of
+// warp 8 issues the products; S of the next keys is in flight while the rows
+// work on the current ones.
 //
-// 96 KB of shared memory and 256 tensor-memory columns at head size 128, so
+// 99 KB of shared memory and 256 tensor-memory columns at head size 128, so
 // that an SM holds two CTAs and one's softmax meets the other's products.
-// What bounds it: a 64-key step is 640 cycles of tensor core (S reads both
-// operands from shared memory, 6 KB per 16 dims), and about 700 issue slots
-// per scheduler for two CTAs' conversions and weights. 128 keys a step at one
-// CTA an SM would halve S's operand reads, but leave each phase's waits bare.
+// What bounds it: a 64-key step takes a lone CTA 1900 cycles, of which the
+// rows' 64 weights a thread are 1400 and their way back to tensor memory 200;
+// two CTAs on an SM take about 2900 for a step each. The step's products are
+// 640 cycles of tensor core (S reads both operands from shared memory), and a
+// scheduler issues every other cycle. 4096 rows over 4096 tokens (16 query, 8
+// KV heads of 128): 390 TFLOP/s. Measured and slower: eight row warps with
+// half of a step's keys each (2053 rows of five users: 69 against 60 us), 256
+// pairs a CTA (80), and the line of all steps cut into equal pieces with a
+// merge behind (108: a step's scheduling and the pieces' parts cost more than
+// the balance gave).
+//
+// Balance: long tiles start first, and where the tiles do not fill the GPU a
+// cluster of up to eight CTAs shares a tile's keys; their results meet through
+// distributed shared memory (128 rows over 32768 tokens: 914 us with one CTA a
+// tile, 131 with eight).
 //
 // A value of V that is infinite or NaN at a token that some of the rows do
 // not see must not reach them as 0 * inf: it is left out of the operand, and
@@ -849,6 +861,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
 
 // CTAs of a cluster that share a tile's keys: as many as fit the GPU at once
 // (two an SM) with four steps each, should the sequences fill their pages.
+// Measured with 1, 2, 4 and 8 (us): 128 rows over 32768 tokens 914, 456, 235,
+// 137; 512 over 8192 151, 98, 69, 97; 2053 rows of five users 60, 71, 105, 226;
+// 300 rows over themselves 14, 16, 19, 39.
 static int prompt_cluster(const Params& P) {
   const long long tiles = ((long long)P.T * P.G / kRows + P.B / 2 + 1) * P.Hkv;
   const long long steps = (long long)P.max_pages * P.bpp * kBlock / kKeys;
