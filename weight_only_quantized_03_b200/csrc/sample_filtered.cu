@@ -823,7 +823,8 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
         many += kb.c;
       }
       if (top_p < 1.f) {
-        const Bin p0 = bin_at(true, share(top_p, z0)), p1 = bin_at(true, share(top_p, z1));
+        const Bin p0 = bin_at(true, share(top_p, z0));
+        const Bin p1 = z1 == z0 ? p0 : bin_at(true, share(top_p, z1));
         s0 = min(s0, p0.pw + 1);
         s1 = min(s1, p1.pw + p1.w);
         want(p0.at, p1.at);
