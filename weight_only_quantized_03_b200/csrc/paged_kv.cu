@@ -10,14 +10,22 @@
 // values of each row in registers, so the norm's sum, the rotation's partner
 // (D/2 away: another lane) and the block's maximum are warp shuffles, and
 // each value is read once and written once. The cosines and sines of the
-// block's tokens are formed once per CTA in shared memory and serve all
-// heads.
+// block's tokens and the norms' weights are brought into shared memory once
+// per CTA and serve all heads (the weights read for each head cost 4 of 36 us),
+// while the first rows are under way.
+//
+// What bounds it: a few rows, the chain launch, lengths, table, rows, stores
+// (32 sequences of one token, 16 + 2 x 8 heads of 128, with the read-back 6.3
+// us); prompts, latency at 64 registers a thread, a lane's 8 rows in turn: a
+// scheduler issues every other cycle (4099 int8 rows 22 us, 59 MB, 2.7 TB/s).
 //
 // The mapping of CTAs to (sequence, block) needs no host knowledge of the
 // lengths: n rows touch at most n/16 + 2 blocks, so slot ranges
 // [row_start[b]/16 + 2b, row_start[b+1]/16 + 2(b+1)) are wide enough for
 // every sequence and do not overlap.
 #include "paged_kv.cuh"
+
+#include "mma_sync.cuh"
 
 #include <algorithm>
 #include <cfloat>
@@ -51,53 +59,48 @@ struct AppendParams {
   double turns[kMaxHalf];  // angle of pair i at position 1, in units of pi
 };
 
-// EPL consecutive values of a row, fp32 or bf16, as fp32.
+// EPL consecutive values of a row, fp32 or bf16, as they come from memory.
 template <int EPL, bool XF32>
-__device__ __forceinline__ void load_vals(const uint8_t* p, float (&x)[EPL]) {
-  if constexpr (XF32) {
-    if constexpr (EPL == 2) {
-      const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
-      x[0] = t.x;
-      x[1] = t.y;
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPL; j += 4) {
-        const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + j / 4);
-        x[j] = t.x;
-        x[j + 1] = t.y;
-        x[j + 2] = t.z;
-        x[j + 3] = t.w;
-      }
-    }
-  } else {
-    uint32_t w[EPL / 2];
-    if constexpr (EPL == 2) {
+struct Raw {
+  static constexpr int N = XF32 ? EPL : EPL / 2;
+  uint32_t w[N];
+
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (N == 1) {
       w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
-    } else if constexpr (EPL == 4) {
+    } else if constexpr (N == 2) {
       const uint2 t = __ldcg(reinterpret_cast<const uint2*>(p));
       w[0] = t.x;
       w[1] = t.y;
     } else {
-      const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
-      w[0] = t.x;
-      w[1] = t.y;
-      w[2] = t.z;
-      w[3] = t.w;
-    }
 #pragma unroll
-    for (int j = 0; j < EPL / 2; ++j) {
-      x[2 * j] = bf16_lo(w[j]);
-      x[2 * j + 1] = bf16_hi(w[j]);
+      for (int j = 0; j < N; j += 4) {
+        const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p) + j / 4);
+        w[j] = t.x;
+        w[j + 1] = t.y;
+        w[j + 2] = t.z;
+        w[j + 3] = t.w;
+      }
     }
   }
-}
-
+  __device__ __forceinline__ void values(float (&x)[EPL]) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (XF32) {
+        x[j] = __uint_as_float(w[j]);
+      } else {
+        x[2 * j] = bf16_lo(w[j]);
+        x[2 * j + 1] = bf16_hi(w[j]);
+      }
+    }
+  }
+};
 template <int EPL>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&x)[EPL]) {
   uint32_t w[EPL / 2];
 #pragma unroll
   for (int j = 0; j < EPL / 2; ++j)
-    w[j] = (uint32_t)f32_to_bf16_bits(x[2 * j]) | ((uint32_t)f32_to_bf16_bits(x[2 * j + 1]) << 16);
+    w[j] = mm::pack_bf16(x[2 * j], x[2 * j + 1]);
   if constexpr (EPL == 2)
     *reinterpret_cast<uint32_t*>(p) = w[0];
   else if constexpr (EPL == 4)
@@ -182,12 +185,10 @@ __device__ __forceinline__ void lds(const float* p, float (&x)[EPL]) {
 // exchanges a lane holds one row's (row lane / 4), so that its root and
 // reciprocal are formed once, not on every lane, and 9 shuffles replace 40.
 template <int D, int NR>
-__device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const uint16_t* w, float eps,
+__device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const float* w, float eps,
                                           int lane) {
   constexpr int EPL = D / 32;
   float nw[EPL], ss[NR];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) nw[j] = bf16_bits_to_f32(__ldcg(w + lane * EPL + j));
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     ss[r] = 0.f;
@@ -206,6 +207,7 @@ __device__ __forceinline__ void norm_rows(float (&x)[NR][D / 32], const uint16_t
 #pragma unroll
   for (int o = 16 / NR; o > 0; o >>= 1) ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
   const float inv = 1.0f / sqrtf(ss[0] / (float)D + eps);
+  lds<EPL>(w + lane * EPL, nw);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const float f = __shfl_sync(0xffffffffu, inv, r * (32 / NR));
@@ -240,39 +242,12 @@ __device__ __forceinline__ void rotate_rows(float (&x)[NR][D / 32], const float*
   }
 }
 
-// Where a warp's rows of one head go.
-struct Task {
-  const uint8_t* src;     // the lane's values of the first row
-  long long ld;           // bytes between rows
-  const uint16_t* norm;   // or null
-  const float* cs;        // null: no rotation
-  const float* sn;
-  int rows;               // 1 .. NR
-};
-
-template <int D, bool XF32, int NR>
-__device__ __forceinline__ void take_rows(const Task& t, float (&x)[NR][D / 32], float eps,
-                                          int half, int lane) {
-  constexpr int EPL = D / 32;
+template <int D, int NR>
+__device__ __forceinline__ void put_query(const AppendParams& P, const float (&x)[NR][D / 32],
+                                          int rows, long long at) {
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) x[r][j] = 0.f;
-    if (r < t.rows) load_vals<EPL, XF32>(t.src + r * t.ld, x[r]);
-  }
-  if (t.norm) norm_rows<D, NR>(x, t.norm, eps, lane);
-  if (t.cs) rotate_rows<D, NR>(x, t.cs, t.sn, half, lane);
-}
-
-template <int D, bool XF32, int NR>
-__device__ __forceinline__ void query_task(const AppendParams& P, const Task& t, long long at,
-                                           int lane) {
-  float x[NR][D / 32];
-  take_rows<D, XF32, NR>(t, x, P.eps, P.half, lane);
-  __syncwarp();  // q_out may be q: every lane has its values
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    if (r >= t.rows) break;
+    if (r >= rows) break;
     if (P.q_bf16)
       store_bf16<D / 32>(reinterpret_cast<uint16_t*>(P.qo) + at + (long long)r * P.H * D, x[r]);
     else
@@ -283,17 +258,15 @@ __device__ __forceinline__ void query_task(const AppendParams& P, const Task& t,
 // K or V rows of one head into a page. int8: `o` rows of the block lie before
 // the block's new ones; `pair`: another warp has the block's other new rows
 // (the block's maximum meets in smax, barrier `bar`).
-template <int D, bool I8, bool XF32, int NR>
-__device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t, uint8_t* block,
-                                           int first, float* scale, int o, bool pair, int half,
-                                           unsigned* smax, int bar, int lane) {
+template <int D, bool I8, int NR>
+__device__ __forceinline__ void put_cache(const float (&x)[NR][D / 32], int rows, uint8_t* block,
+                                          int first, float* scale, int o, bool pair, int half,
+                                          unsigned* smax, int bar, int lane) {
   constexpr int EPL = D / 32;
-  float x[NR][EPL];
-  take_rows<D, XF32, NR>(t, x, P.eps, P.half, lane);
   if constexpr (!I8) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      if (r >= t.rows) break;
+      if (r >= rows) break;
       store_bf16<EPL>(reinterpret_cast<uint16_t*>(block) + (first + r) * D, x[r]);
     }
   } else {
@@ -305,7 +278,7 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
       unsigned m = 0;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) m = max(m, __float_as_uint(x[r][j]) & 0x7FFFFFFFu);
-      top = max(top, r < t.rows ? m : 0u);
+      top = max(top, r < rows ? m : 0u);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (pair) {
@@ -331,7 +304,7 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      if (r >= t.rows) break;
+      if (r >= rows) break;
       store_codes<EPL>(block + (first + r) * D + lane * EPL, x[r], inv);
     }
     if (half == 0) {
@@ -341,92 +314,143 @@ __device__ __forceinline__ void cache_task(const AppendParams& P, const Task& t,
   }
 }
 
-template <int D, bool I8, bool XF32>
-__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2)
-append_kernel(const __grid_constant__ AppendParams P) {
-  constexpr int EPL = D / 32, XB = XF32 ? 4 : 2, NR = 8;
-  __shared__ __align__(16) float cs[kBlock * D / 2];
-  __shared__ __align__(16) float sn[kBlock * D / 2];
-  __shared__ unsigned smax[kWarps];
-  __shared__ int s_b;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
+// A CTA's block of 16 tokens: its new rows, lo .. lo + nr - 1 of the sequence
+// (packed rows from `row`), the o rows of the block before them, its page.
+struct NewRows {
+  int first, lo, nr, o, page;
+  long long row;
+};
 
-  // the sequence whose slot range holds this CTA's slot
-  const int u = blockIdx.x;
-  int b = u;
-  if (P.row_start) {
-    if (tid == 0) s_b = -1;
-    __syncthreads();
-    for (int i = tid; i < P.B; i += kWarps * 32) {
-      const int lo = row_begin(P.row_start, i, P.T) / kBlock + 2 * i;
-      const int hi = row_begin(P.row_start, i + 1, P.T) / kBlock + 2 * (i + 1);
-      if (lo <= u && u < hi) s_b = i;
+// The (q, K or V; head) items of a block, up to NR rows of a head a warp.
+template <int D, bool I8, bool XF32, int NR>
+__device__ __forceinline__ void append_rows(const AppendParams& P, const NewRows& B, float* cs,
+                                            float* sn, float* norms, unsigned* smax) {
+  constexpr int EPL = D / 32, XB = XF32 ? 4 : 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // past NR rows two neighbouring warps share the head's block
+  const bool pair = B.nr > NR;
+  const int half = pair ? warp & 1 : 0, base = half * NR, rows = min(NR, B.nr - base);
+  const int items = 2 * P.Hkv + P.H, step = pair ? kWarps / 2 : kWarps;
+  Raw<EPL, XF32> raw[NR];
+  const auto fetch = [&](int it) {
+    const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
+    const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
+    const long long ld = isk ? P.k_ld : isv ? P.v_ld : P.q_ld;
+    const uint8_t* const p =
+        (isk ? P.k : isv ? P.v : P.q) + ((B.row + base) * ld + h * D + lane * EPL) * XB;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int j = 0; j < Raw<EPL, XF32>::N; ++j) raw[r].w[j] = 0;
+      if (r < rows) raw[r].load(p + r * ld * XB);
     }
-    __syncthreads();
-    b = s_b;
-    if (b < 0) return;
-  }
-  const int r0 = row_begin(P.row_start, b, P.T), n = row_begin(P.row_start, b + 1, P.T) - r0;
-  const int len = __ldcg(P.kv_len + b);
-  if (n < 1 || len < n || len > P.max_pages * P.page_size) return;
-  const int p0 = len - n;
-  const int first = (p0 / kBlock + (P.row_start ? u - (r0 / kBlock + 2 * b) : 0)) * kBlock;
-  if (first >= len) return;
-  const int lo = max(p0, first), hi = min(len, first + kBlock);
-  const int nr = hi - lo, o = lo - first;  // new rows, and rows of the block before them
-  const long long row = r0 + (lo - p0);
-  const int page = __ldcg(P.table + (long long)b * P.max_pages + first / P.page_size);
-  const bool in_pool = page >= 0 && page < P.num_pages;
+  };
+  int it = blockIdx.y * step + (pair ? warp >> 1 : warp);
+  if (it < items) fetch(it);  // under way while the angles are formed
 
   // cosines and sines of the new rows: the angle pos * theta^(-2i/rd) in units
   // of pi and its reduction to [-1, 1] in float64 (positions in the millions
   // keep the full fp32 accuracy), sincospi in fp32: within 2^-22 of the
-  // exact values, at a fraction of the cost of a float64 sincos.
-  for (int i = tid; i < nr * P.half; i += kWarps * 32) {
-    const int r = i / P.half, f = i - r * P.half;
-    const double t = (double)(lo + r) * P.turns[f];
-    sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn[i], &cs[i]);
+  // exact values, at a fraction of the cost of a float64 sincos. A thread
+  // keeps its pair, whose angle it reads once (each lane another one, which the
+  // constant cache gives in turn).
+  if (P.half) {
+    const int f = tid % P.half, every = kWarps * 32 / P.half;
+    const double turn = P.turns[f];
+    for (int r = tid / P.half; r < B.nr && tid < every * P.half; r += every) {
+      const double t = (double)(B.lo + r) * turn;
+      sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn[r * P.half + f], &cs[r * P.half + f]);
+    }
+  }
+  for (int i = tid; i < 2 * D; i += kWarps * 32) {  // K's norm weights, then q's
+    const uint16_t* const w = i < D ? P.kn : P.qn;
+    if (w) norms[i] = bf16_bits_to_f32(__ldcg(w + i % D));
   }
   __syncthreads();
 
-  // A warp has up to 8 rows of a head; past 8 new rows two neighbouring
-  // warps share the head's block.
-  const bool pair = nr > NR;
-  const int half = pair ? warp & 1 : 0, base = half * NR;
-  const int items = 2 * P.Hkv + P.H, step = pair ? kWarps / 2 : kWarps;
-  for (int it = blockIdx.y * step + (pair ? warp >> 1 : warp); it < items; it += gridDim.y * step) {
-    const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
-    const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
-    const long long ld = isk ? P.k_ld : isv ? P.v_ld : P.q_ld;
-    Task t;
-    t.src = (isk ? P.k : isv ? P.v : P.q) + ((row + base) * ld + h * D + lane * EPL) * XB;
-    t.ld = ld * XB;
-    t.norm = isk ? P.kn : isv ? nullptr : P.qn;
-    t.cs = isv || !P.half ? nullptr : cs + base * P.half;
-    t.sn = sn + base * P.half;
-    t.rows = min(NR, nr - base);
-    if (!isk && !isv) {
-      const long long at = (row + base) * P.H * D + h * D + lane * EPL;
-      if (nr == 1)
-        query_task<D, XF32, 1>(P, t, at, lane);
-      else
-        query_task<D, XF32, NR>(P, t, at, lane);
-      continue;
-    }
-    if (!in_pool) continue;
-    const long long hp = (long long)page * P.Hkv + h;
-    const int in_page = first % P.page_size;
+  const auto put = [&](const float (&x)[NR][EPL], bool isk, int h) {
+    const long long hp = (long long)B.page * P.Hkv + h;
+    const int in_page = B.first % P.page_size;
     uint8_t* block = (isk ? P.kp : P.vp) + (hp * P.page_size + in_page) * D * (I8 ? 1 : 2) +
                      (I8 ? 0 : lane * EPL * 2);
     float* scale =
         I8 ? (isk ? P.ks : P.vs) + hp * (P.page_size / kBlock) + in_page / kBlock : nullptr;
-    if (nr == 1)
-      cache_task<D, I8, XF32, 1>(P, t, block, o, scale, o, false, 0, nullptr, 0, lane);
-    else
-      cache_task<D, I8, XF32, NR>(P, t, block, o + base, scale, o, pair, half,
-                                  smax + (warp & ~1), 1 + (warp >> 1), lane);
+    put_cache<D, I8, NR>(x, rows, block, B.o + base, scale, B.o, pair, half, smax + (warp & ~1),
+                         1 + (warp >> 1), lane);
+  };
+  // the next item's rows are under way while this one's are put away, where
+  // registers hold both (fp32 rows of 128 spilled)
+  constexpr bool kAhead = NR == 1;
+  for (; it < items; it += gridDim.y * step) {
+    const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
+    const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
+    float x[NR][EPL];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) raw[r].values(x[r]);
+    if (!isv && (isk ? P.kn : P.qn)) norm_rows<D, NR>(x, isk ? norms : norms + D, P.eps, lane);
+    if (!isv && P.half) rotate_rows<D, NR>(x, cs + base * P.half, sn + base * P.half, P.half, lane);
+    // (q_out may be q: every lane has the values of this item's rows, and the
+    // next item's are another head's)
+    __syncwarp();
+    const int next = it + gridDim.y * step;
+    if (kAhead && next < items) fetch(next);
+    if (!isk && !isv)
+      put_query<D, NR>(P, x, rows, (B.row + base) * P.H * D + h * D + lane * EPL);
+    else if (B.page >= 0 && B.page < P.num_pages)
+      put(x, isk, h);
+    if (!kAhead && next < items) fetch(next);
   }
+}
+
+template <int D, bool I8, bool XF32>
+__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2)
+append_kernel(const __grid_constant__ AppendParams P) {
+  __shared__ __align__(16) float cs[kBlock * D / 2];
+  __shared__ __align__(16) float sn[kBlock * D / 2];
+  __shared__ __align__(16) float norms[2 * D];
+  __shared__ unsigned smax[kWarps];
+  __shared__ int s_b, s_r0, s_n, s_len;
+  const int tid = threadIdx.x;
+  pdl_wait();
+
+  // the sequence whose slot range holds this CTA's slot
+  const int u = blockIdx.x;
+  int b = u, r0 = u, n = 1, len;
+  if (P.row_start) {
+    int found = 0;
+    for (int i = tid; i < P.B; i += kWarps * 32) {
+      const int from = row_begin(P.row_start, i, P.T), to = row_begin(P.row_start, i + 1, P.T);
+      const int cached = __ldcg(P.kv_len + i);
+      if (u >= from / kBlock + 2 * i && u < to / kBlock + 2 * (i + 1)) {
+        found = 1;
+        s_b = i;
+        s_r0 = from;
+        s_n = to - from;
+        s_len = cached;
+      }
+    }
+    if (!__syncthreads_or(found)) return;
+    b = s_b;
+    r0 = s_r0;
+    n = s_n;
+    len = s_len;
+  } else {
+    len = __ldcg(P.kv_len + b);
+  }
+  if (n < 1 || len < n || len > P.max_pages * P.page_size) return;
+  const int p0 = len - n;
+  NewRows B;
+  B.first = (p0 / kBlock + (P.row_start ? u - (r0 / kBlock + 2 * b) : 0)) * kBlock;
+  if (B.first >= len) return;
+  B.lo = max(p0, B.first);
+  B.nr = min(len, B.first + kBlock) - B.lo;
+  B.o = B.lo - B.first;
+  B.row = r0 + (B.lo - p0);
+  B.page = __ldcg(P.table + (long long)b * P.max_pages + B.first / P.page_size);
+  if (B.nr == 1)
+    append_rows<D, I8, XF32, 1>(P, B, cs, sn, norms, smax);
+  else
+    append_rows<D, I8, XF32, 8>(P, B, cs, sn, norms, smax);
 }
 
 struct GatherParams {
@@ -443,9 +467,10 @@ struct GatherParams {
   int B, T, Hkv, page_size, max_pages, num_pages;
 };
 
-// A CTA reads kGatherRows rows; a thread takes 8 neighbouring values of K or
-// V, the same place in each row, so that its loads are independent.
-constexpr int kGatherRows = 4;
+// A CTA reads kGatherRows rows, a warp finding the page of each; a thread takes
+// 8 neighbouring values of K or V, the same place in each row, so that its
+// loads go out together.
+constexpr int kGatherRows = kWarps;
 
 template <int D, bool I8>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams P) {
@@ -453,24 +478,31 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   const int row0 = blockIdx.x * kGatherRows;
-  if (warp < kGatherRows) {  // a warp finds a row's sequence and page
+  {  // a warp finds a row's sequence and page
     const int row = row0 + warp;
-    int b = row < P.T ? row : -1;
+    int b = row < P.T ? row : -1, from = row, first = 0;
     if (P.row_start) {
       b = -1;
       for (int i0 = 0; i0 < P.B && b < 0; i0 += 32) {
         const int i = i0 + lane;
-        const bool in = i < P.B && row < P.T && row_begin(P.row_start, i, P.T) <= row &&
-                        row < row_begin(P.row_start, i + 1, P.T);
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (m) b = i0 + __ffs(m) - 1;
+        const int lo = i < P.B ? row_begin(P.row_start, i, P.T) : P.T;
+        const int hi = i < P.B ? row_begin(P.row_start, i + 1, P.T) : 0;
+        const int at = P.first && i < P.B ? __ldcg(P.first + i) : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, row < P.T && lo <= row && row < hi);
+        if (m) {
+          const int l = __ffs(m) - 1;
+          b = i0 + l;
+          from = __shfl_sync(0xffffffffu, lo, l);
+          first = __shfl_sync(0xffffffffu, at, l);
+        }
       }
+    } else if (P.first && b >= 0) {
+      first = __ldcg(P.first + b);
     }
     if (lane == 0) {
       int page = -2, off = 0;
       if (b >= 0) {
-        const long long t =
-            (long long)(P.first ? __ldcg(P.first + b) : 0) + (row - row_begin(P.row_start, b, P.T));
+        const long long t = (long long)first + (row - from);
         page = -1;
         if (t >= 0 && t < (long long)P.max_pages * P.page_size) {
           const int pi = (int)t / P.page_size;
@@ -492,35 +524,36 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherParams 
     if (!out) continue;
     const uint8_t* pages = isv ? P.vp : P.kp;
     const float* scales = isv ? P.vs : P.ks;
-    float x[kGatherRows][8];
+    Raw<I8 ? 4 : 8, false> raw[kGatherRows];  // 8 codes or values
+    float scale[kGatherRows];
 #pragma unroll
     for (int r = 0; r < kGatherRows; ++r) {
       const int page = s_page[r];
-      if (page < 0) {
+      scale[r] = __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[r][j] = __int_as_float(0x7FC00000);
-        continue;
-      }
+      for (int j = 0; j < (I8 ? 2 : 4); ++j) raw[r].w[j] = I8 ? 0 : 0x7FC07FC0u;
+      if (page < 0) continue;
       const long long hp = (long long)page * P.Hkv + h;
-      const long long from = (hp * P.page_size + s_off[r]) * D + d;
-      if constexpr (I8) {
-        int c[8];
-        load_codes<8>(pages + from, c);
-        const float s = __ldcg(scales + hp * (P.page_size / kBlock) + s_off[r] / kBlock);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[r][j] = (float)c[j] * s;
-      } else {
-        load_vals<8, false>(pages + from * 2, x[r]);
-      }
+      raw[r].load(pages + ((hp * P.page_size + s_off[r]) * D + d) * (I8 ? 1 : 2));
+      if (I8) scale[r] = __ldcg(scales + hp * (P.page_size / kBlock) + s_off[r] / kBlock);
     }
 #pragma unroll
     for (int r = 0; r < kGatherRows; ++r) {
       if (s_page[r] == -2) continue;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t w = raw[r].w[I8 ? j / 4 : j / 2];
+        if constexpr (I8)
+          x[j] = (float)(int8_t)(w >> (8 * (j & 3))) * scale[r];
+        else
+          x[j] = j & 1 ? bf16_hi(w) : bf16_lo(w);
+      }
       const long long to = ((long long)(row0 + r) * P.Hkv + h) * D + d;
       if (P.out_bf16)
-        store_bf16<8>(reinterpret_cast<uint16_t*>(out) + to, x[r]);
+        store_bf16<8>(reinterpret_cast<uint16_t*>(out) + to, x);
       else
-        store_f32<8>(reinterpret_cast<float*>(out) + to, x[r]);
+        store_f32<8>(reinterpret_cast<float*>(out) + to, x);
     }
   }
 }
