@@ -388,3 +388,42 @@ def test_prompt_rows_of_a_wrong_length_beside_a_long_cache():
         rows = slice(r0[b], r0[b + 1])
         want, tol = reference(q[rows], k, v, H, Hkv, D, 1 / math.sqrt(D), "int8", False, True)
         assert np.all(np.abs(got[rows] - want) <= tol)
+
+
+LONG = [
+    ("int8", 128, 64, 16, 8, [1, 1, 1], [513, 17, 1], BF, BF),
+    ("int8", 64, 32, 6, 2, [1, 3, 0, 1], [1000, 15, 0, 129], F32, BF),
+    ("int8", 256, 16, 8, 2, [1, 1], [700, 31], BF, BF),
+    ("int8", 128, 64, 16, 1, [1, 1], [300, 5], BF, BF),
+    ("bf16", 128, 16, 8, 1, [1], [2093], F32, F32),
+    ("bf16", 64, 48, 16, 16, [1, 1], [900, 3], BF, BF),
+    ("bf16", 256, 32, 8, 2, [2, 1], [700, 31], F32, BF),
+    ("bf16", 128, 64, 16, 8, [1] * 40, [1 + 29 * i for i in range(40)], BF, BF),
+]
+
+
+@pytest.mark.parametrize("case", LONG,
+                         ids=lambda c: f"{c[0]}-d{c[1]}-h{c[3]}.{c[4]}-n{len(c[5])}-l{c[6][0]}")
+def test_page_tables_far_longer_than_the_sequences(case):
+    """Room for 20000 tokens a sequence: the work is cut into pieces whose
+    parts a second launch merges, most of them of a chunk or two."""
+    kind, D, page, H, Hkv, n, lens, xt, ot = case
+    cap = 20000 if len(n) < 10 else 5000
+    check(kind, D, page, H, Hkv, n, lens, xt, ot, 990, cap=cap, pad=2)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_a_cluster_with_idle_blocks_and_empty_sequences(kind):
+    """Eight blocks an item and keys for one, several and all of them; a
+    sequence without rows and one of a wrong length."""
+    D, H, Hkv = 128, 4, 2
+    n, lens = [1, 0, 1, 1, 1], [1, 300, 130, 1000, 40]
+    cache = Cache(kind, 5, Hkv, D, 64, 1000, lens, 995)
+    got, q = run(cache, n, [1, 300, 130, 1000, 5000], H, BF, BF, 996)
+    r0 = starts(n)
+    assert np.all(got[3] == 0.0)
+    for b in (0, 2, 3):
+        k, v = cache.values(b, lens[b])
+        rows = slice(r0[b], r0[b + 1])
+        want, tol = reference(q[rows], k, v, H, Hkv, D, 1 / math.sqrt(D), kind, False, True)
+        assert np.all(np.abs(got[rows] - want) <= tol)

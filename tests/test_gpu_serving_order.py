@@ -32,7 +32,8 @@ def _pool(Hkv, D, tokens, page=64, seed=0):
 
 
 @pytest.mark.parametrize("B,Hkv,tokens", [
-    (37, 8, 16384),   # as many (sequence, head) items as pieces: none is cut
+    (74, 8, 8192),    # twice as many (sequence, head) items as pieces: none is cut
+    (37, 8, 16384),   # an item is a block
     (37, 8, 16320),
     (5, 8, 100),      # an item is one chunk
     (40, 1, 16384),   # some items cut

@@ -35,13 +35,15 @@
 // passes it by 2^kMargin, one vote per tile instead of the shuffles of a
 // maximum.
 //
-// Work split (kernel "split", decodes and short prompts). All (sequence, KV
-// head, column tile) items' key chunks form one line that is cut into equal
-// pieces, one per CTA, from the lengths on the device: ragged batches are
-// balanced, and the grid never depends on them. A CTA's 8 warps take a
-// piece's tiles in turn and merge in shared memory. An item inside one piece
-// is written out; the others' parts go to the workspace and a second small
-// launch merges them in order (results do not depend on scheduling).
+// Work split (decodes and short prompts). A CTA's 8 warps take its keys' tiles
+// in turn and merge in shared memory. Kernel "cluster", where equal shares are
+// good enough (see plan): an item, a (sequence, KV head, column tile), belongs
+// to a cluster of up to 8 CTAs, whose results meet through distributed shared
+// memory. Kernel "split": all items' key chunks form one line that is cut into
+// equal pieces, one per CTA, from the lengths on the device: ragged batches are
+// balanced, and the grid never depends on them. An item inside one piece is
+// written out; the others' parts go to the workspace and a second small launch
+// merges them in order. Results do not depend on scheduling in either.
 // Prompts with a bf16 q and out go to the tcgen05 kernel of
 // paged_attention_tc.cu.
 #include <cuda_fp16.h>
@@ -59,6 +61,7 @@ namespace pa {
 constexpr int kWarps = 8;            // split kernel
 constexpr int kChunk = kWarps * kBlock;
 constexpr int kMergeThreads = 512;
+constexpr int kSlack = 2;            // chunks (see plan)
 constexpr int kMaxPieces = 320;      // of the split kernel (two CTAs on each of 148 SMs)
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -554,6 +557,52 @@ __device__ __forceinline__ void store_out(const Params& P, const Item& it, int c
     reinterpret_cast<float*>(P.out)[at] = x;
 }
 
+// A warp's state to shared memory: weights summed over the lanes that share a
+// column, outputs in plain units.
+template <int D, bool I8, int NT>
+__device__ __forceinline__ void put_state(const State<D, NT>& S, float* so, float* sm, float* sl,
+                                          int cols, int warp, int lane) {
+  constexpr int NC = NT * 8;
+  const int g = lane >> 2, t = lane & 3;
+  const float u = o_unit<I8>(S.r);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = S.l[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int n = j * 8 + 2 * t + e;
+      if (n < cols) {
+        if (g == 0) {
+          sm[warp * NC + n] = S.m[j][e];
+          sl[warp * NC + n] = l;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(so + (warp * NC + n) * D + g * (D / 8) + 2 * i) =
+              make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
+      }
+    }
+  }
+}
+// The CTA's reference M, weights' sum L and output O at column n, dim d.
+template <int D, int NC>
+__device__ __forceinline__ void join_warps(const float* so, const float* sm, const float* sl, int n,
+                                           int d, float& M, float& L, float& O) {
+  M = sm[n];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) M = fmaxf(M, sm[k * NC + n]);
+  L = O = 0.f;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    const float a = ex2(sm[k * NC + n] - M);
+    L = fmaf(a, sl[k * NC + n], L);
+    O = fmaf(a, so[(k * NC + n) * D + d], O);
+  }
+}
+
 // ------------------------------------------------------------ split kernel --
 
 // A sequence's column tiles and the chunks of each of its items (at least
@@ -717,45 +766,14 @@ split_kernel(const __grid_constant__ Params P) {
       c1 = (int)min((unsigned)w.chunks, stop - pos);
       start(it, c0, c1);
     }
-    // the warps' states to shared memory: weights summed over the lanes that
-    // share a column, outputs in plain units
     const int cols = min(NC, cur.n * P.G - cur.ct * NC);  // of the tile, real ones
-    const float u = o_unit<I8>(S.r);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = S.l[j][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int n = j * 8 + 2 * walk.t + e;
-        if (n < cols) {
-          if (walk.g == 0) {
-            sm[warp * NC + n] = S.m[j][e];
-            sl[warp * NC + n] = l;
-          }
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            *reinterpret_cast<float2*>(so + (warp * NC + n) * D + walk.g * (D / 8) + 2 * i) =
-                make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
-        }
-      }
-    }
+    put_state<D, I8, NT>(S, so, sm, sl, cols, warp, lane);
     __syncthreads();
     float* part = P.part + (long long)(2 * blockIdx.x + first_part) * NC * (D + 2);
     for (int i = tid; i < cols * D; i += kWarps * 32) {
       const int n = i / D, d = i % D;
-      float M = sm[n];
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) M = fmaxf(M, sm[k * NC + n]);
-      float L = 0.f, O = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float a = ex2(sm[k * NC + n] - M);
-        L = fmaf(a, sl[k * NC + n], L);
-        O = fmaf(a, so[(k * NC + n) * D + d], O);
-      }
+      float M, L, O;
+      join_warps<D, NC>(so, sm, sl, n, d, M, L, O);
       if (whole) {
         store_out(P, cur, cur.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
       } else {
@@ -769,6 +787,131 @@ split_kernel(const __grid_constant__ Params P) {
     if (!more) return;
   }
 }
+
+// ---------------------------------------------------------- cluster kernel --
+
+__device__ __forceinline__ uint32_t remote(const float* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(a)
+      : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float ld_remote(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// An item a cluster: its Z CTAs take equal shares of the item's chunks and
+// join their results through distributed shared memory, so one launch does.
+// A column tile's slot: a sequence with x columns has at most x / NC + 1 tiles,
+// so slot ranges [begin G / NC + b, end G / NC + b + 1) do not overlap.
+constexpr int kMaxZ = 8;
+template <int D, bool I8, int QS, int PS>
+__global__ void __launch_bounds__(kWarps * 32, split_ctas(D, I8, 1))
+cluster_kernel(const __grid_constant__ Params P) {
+  constexpr int NT = 1, NC = 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);            // [kWarps][NC][D]
+  float* sm = so + kWarps * NC * D;                      // [kWarps][NC]
+  float* sl = sm + kWarps * NC;                          // [kWarps][NC]
+  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * NC);  // fragments of q
+  __shared__ float sf[NC];
+  __shared__ float pm[NC], pl[NC], po[NC * D];           // the CTA's result
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Z = P.pieces, z = blockIdx.x % Z, u = blockIdx.x / Z;
+  pdl_wait();
+  pdl_trigger();
+
+  Item it = {-1, 0, 0, 0, 0, 0};
+#pragma unroll 1
+  for (int b0 = 0; b0 < P.B && it.b < 0; b0 += 32) {
+    Item mine = {-1, 0, 0, 0, 0, 0};
+    if (b0 + lane < P.B) set_seq(P, mine, b0 + lane);
+    const int from = (int)((long long)mine.r0 * P.G / NC) + b0 + lane;
+    const int to = (int)((long long)(mine.r0 + mine.n) * P.G / NC) + b0 + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, mine.n && u >= from && u <= to);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      it.b = __shfl_sync(0xffffffffu, mine.b, l);
+      it.r0 = __shfl_sync(0xffffffffu, mine.r0, l);
+      it.n = __shfl_sync(0xffffffffu, mine.n, l);
+      it.len = __shfl_sync(0xffffffffu, mine.len, l);
+      it.ct = __shfl_sync(0xffffffffu, u - from, l);
+    }
+  }
+  if (it.b < 0) return;  // (the cluster's CTAs alike)
+  const SeqWork w(P, it, NC);
+  if (it.ct >= w.tiles) return;
+  it.h = blockIdx.y;
+
+  Walk<D, I8, NT, QS, PS> walk(P, lane);
+  StageQ<D, I8, NT, QS, NT * 8 / kWarps> qs;
+  walk.sq = sq;
+  State<D, NT> S;
+  const int c0 = (int)((long long)w.chunks * z / Z), c1 = (int)((long long)w.chunks * (z + 1) / Z);
+  qs.take(P, it, warp, kWarps, lane);
+  walk.len = it.len;
+  walk.begin(it, c0 * kWarps + warp, kWarps, min(c1 * kWarps, (it.len + kBlock - 1) / kBlock));
+  qs.put(P, sq, sf, warp, kWarps, lane);
+  set_limits<NT>(P, it, walk);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    walk.qf[j][0] = sf[j * 8 + 2 * walk.t];
+    walk.qf[j][1] = sf[j * 8 + 2 * walk.t + 1];
+  }
+  S.clear();
+  walk.run(S, it);
+  const int cols = min(NC, it.n * P.G - it.ct * NC);
+  put_state<D, I8, NT>(S, so, sm, sl, cols, warp, lane);
+  __syncthreads();
+  for (int i = tid; i < cols * D; i += kWarps * 32) {
+    const int n = i / D, d = i % D;
+    float M, L, O;
+    join_warps<D, NC>(so, sm, sl, n, d, M, L, O);
+    if (Z == 1) {
+      store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+    } else {
+      po[i] = O;
+      if (d == 0) {
+        pm[n] = M;
+        pl[n] = L;
+      }
+    }
+  }
+  if (Z == 1) return;
+  cluster_sync();
+  // CTA z writes its share of the outputs; a thread's remote loads go out
+  // together
+  for (int i = z * kWarps * 32 + tid; i < cols * D; i += Z * kWarps * 32) {
+    const int n = i / D, d = i % D;
+    float m[kMaxZ], l[kMaxZ], o[kMaxZ];
+#pragma unroll
+    for (int k = 0; k < kMaxZ; ++k) {
+      m[k] = k < Z ? ld_remote(&pm[n], k) : -FLT_MAX;
+      l[k] = k < Z ? ld_remote(&pl[n], k) : 0.f;
+      o[k] = k < Z ? ld_remote(&po[i], k) : 0.f;
+    }
+    float M = -FLT_MAX, L = 0.f, O = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxZ; ++k) M = fmaxf(M, m[k]);
+#pragma unroll
+    for (int k = 0; k < kMaxZ; ++k) {
+      const float a = ex2(m[k] - M);
+      L = fmaf(a, l[k], L);
+      O = fmaf(a, o[k], O);
+    }
+    store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+  }
+  cluster_sync();  // nobody ends while its shared memory is read
+}
+
+// ------------------------------------------------------------ merge kernel --
 
 // Items cut between pieces: one CTA per (column tile, head). A column tile's
 // slot: a sequence with x columns has at most x / NC + 1 tiles, so slot
@@ -862,8 +1005,36 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 
 // ---------------------------------------------------------------- launches --
 
+template <int D, bool I8, int QS, int PS>
+cudaError_t launch_cluster(const Params& P, int z, cudaStream_t st) {
+  constexpr int NC = 8;
+  const size_t smem = (size_t)kWarps * NC * (D + 2) * 4 + (size_t)NC * D * QS * 2;
+  const auto kernel = cluster_kernel<D, I8, QS, PS>;
+  ensure_smem((const void*)kernel, (int)smem);
+  Params Q = P;
+  Q.pieces = z;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)P.T * P.G / NC + P.B) * z), P.Hkv);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = z;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = z > 1 ? 2 : 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, Q);
+}
+
 template <int D, bool I8, int NT, int QS, int PS>
-cudaError_t launch_split(const Params& P, cudaStream_t st) {
+cudaError_t launch_split(const Params& P, int z, cudaStream_t st) {
+  if constexpr (NT == 1)
+    if (z) return launch_cluster<D, I8, QS, PS>(P, z, st);
   constexpr int NC = NT * 8;
   const size_t smem = (size_t)kWarps * NC * (D + 2) * 4 + (size_t)NC * D * QS * 2;
   ensure_smem((const void*)split_kernel<D, I8, NT, QS, PS>, (int)smem);
@@ -872,38 +1043,59 @@ cudaError_t launch_split(const Params& P, cudaStream_t st) {
   if (e != cudaSuccess || P.pieces == 1) return e;
   const long long slots = (long long)P.T * P.G / NC + P.B;
   // few items: their dims over several CTAs, so that a thread has few pieces
-  unsigned z = 1;
-  while (z * 2 <= D / 64 && slots * P.Hkv * z * 2 <= 2 * num_sms()) z *= 2;
-  return launch_pdl(merge_kernel<D, NT>, dim3((unsigned)slots, P.Hkv, z), dim3(kMergeThreads), 0,
+  unsigned parts = 1;  // of the dims
+  while (parts * 2 <= D / 64 && slots * P.Hkv * parts * 2 <= 2 * num_sms()) parts *= 2;
+  return launch_pdl(merge_kernel<D, NT>, dim3((unsigned)slots, P.Hkv, parts), dim3(kMergeThreads), 0,
                     st, true, P);
 }
 
-// How a call runs: column tiles of 8 side by side, pieces of the split kernel
-// (0: the prompt kernel).
+// How a call runs: column tiles of 8 side by side, and pieces of the split
+// kernel (0: the prompt kernel) or the CTAs that share an item (z > 0).
 struct Plan {
-  int nt, pieces;
+  int nt, pieces, z;
 };
 inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bool exact) {
   const long long G = H / Hkv;
-  if (D <= 128 && !exact && T * G >= 32LL * B) return {0, 0};
+  if (D <= 128 && !exact && T * G >= 32LL * B) return {0, 0, 0};
   const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
-  const long long items = ((long long)T * G / (8 * nt) + B) * Hkv;
+  // at most: a sequence of n rows has n G / (8 nt) column tiles, rounded up
+  const int NC = 8 * nt;
+  const long long items = std::min(T * G / NC + B, T * ((G + NC - 1) / NC)) * Hkv;
   const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
-  if (items > 0x7FFFFFFFLL / chunks) return {0, -1};  // the line has 31 bits
+  if (items > 0x7FFFFFFFLL / chunks) return {0, -1, 0};  // the line has 31 bits
   const long long most =
       std::min((long long)kMaxPieces, (long long)num_sms() * split_ctas(D, i8, nt));
-  return {nt, (int)std::max(1LL, std::min(most, items * chunks))};
+  // Clusters where an item's equal shares are little longer than the balanced
+  // pieces would be (should the sequences fill their pages): up to two chunks
+  // cost less than the second launch. Past 8 chunks a share only without a
+  // cluster, whose CTAs wait for the slowest. Measured against the line and its
+  // merge (us, 8 int8 KV heads of 128, 2 query heads each): 1 x 512 7.8 -> 6.5,
+  // 4 x 2048 13.4 -> 10.3, 32 x 2048 33.6 -> 30.4; shares four chunks longer, 8 x
+  // 8192, 29.1 -> 31; more CTAs than the GPU holds at once, 4 x 700 of 16 rows
+  // in all, 11.2 -> 14.8. (Rows of up to 32 columns a sequence, in tiles of 16,
+  // keep the line.)
+  // (nor where most sequences are empty: each CTA looks through them)
+  if (nt == 1 && items <= most && B <= 4 * T) {
+    // (one CTA an SM: clusters leave some of a GPC's SMs empty)
+    const long long room = split_ctas(D, i8, nt) == 1 ? most * 3 / 4 : most;
+    int z = 1;
+    while (z < kMaxZ && z < chunks && items * 2 * z <= room) z *= 2;
+    const long long share = (chunks + z - 1) / z;
+    if (share <= (items * chunks + most - 1) / most + kSlack && (z == 1 || share <= 8))
+      return {nt, 0, z};
+  }
+  return {nt, (int)std::max(1LL, std::min(most, items * chunks)), 0};
 }
 
 template <int D, bool I8>
 cudaError_t launch(const Params& P, const Plan& p, bool exact, cudaStream_t st) {
   constexpr int E = I8 ? 2 : 3;  // terms of fp32 q and weights
-  if (exact) return launch_split<D, I8, 1, E, E>(P, st);
+  if (exact) return launch_split<D, I8, 1, E, E>(P, p.z, st);
   if constexpr (D <= 128) {
-    if (p.pieces == 0) return launch_prompt(P, D, I8, st);
-    if (p.nt == 2) return launch_split<D, I8, 2, 1, 1>(P, st);
+    if (p.pieces == 0 && !p.z) return launch_prompt(P, D, I8, st);
+    if (p.nt == 2) return launch_split<D, I8, 2, 1, 1>(P, p.z, st);
   }
-  return launch_split<D, I8, 1, 1, 1>(P, st);
+  return launch_split<D, I8, 1, 1, 1>(P, p.z, st);
 }
 
 // The largest number of pieces times columns any call of the head size uses.
