@@ -211,9 +211,10 @@ def _raw_stream(stream, dev):
 
 
 def _dt(t):
-    if t.dtype == torch.float32:
+    dt = t.dtype
+    if dt is torch.float32:
         return QG_F32
-    if t.dtype == torch.bfloat16:
+    if dt is torch.bfloat16:
         return QG_BF16
     raise TypeError(f"unsupported dtype {t.dtype}")
 
@@ -385,18 +386,23 @@ def qg_sample_filtered(logits, u, out, temperature=None, top_k=None, top_p=None,
     if logits.dtype is not torch.float32:
         raise TypeError(f"logits must be float32, not {logits.dtype}")
     ld = _rows_of("logits", logits, V)
-    f32, i32 = torch.float32, torch.int32
-    for name, t, dt in (("u", u, f32), ("out", out, i32), ("temperature", temperature, f32),
-                        ("top_k", top_k, i32), ("top_p", top_p, f32), ("min_p", min_p, f32),
-                        ("kept", kept, i32), ("logprob", logprob, f32), ("logits", logits, None)):
-        if t is None:
-            continue
-        if dt is not None and (t.dtype is not dt or t.shape != (B,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dt} tensor of {B} values")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
-    _sample(logits.data_ptr(), ld, B, V, _p(temperature), _p(top_k), _p(top_p), _p(min_p),
-            u.data_ptr(), out.data_ptr(), _p(kept), _p(logprob), _raw_stream(stream, dev))
+    floats, ints = (u, temperature, top_p, min_p, logprob), (out, top_k, kept)
+    for some, dt in ((floats, torch.float32), (ints, torch.int32)):
+        for t in some:
+            if t is not None and (t.dtype is not dt or t.dim() != 1 or t.numel() != B
+                                  or not t.is_contiguous() or t.get_device() != dev):
+                _check_device(dev, ("u", u), ("out", out), ("temperature", temperature),
+                              ("top_k", top_k), ("top_p", top_p), ("min_p", min_p),
+                              ("kept", kept), ("logprob", logprob))
+                names = ("u", "temperature", "top_p", "min_p", "logprob", "out", "top_k", "kept")
+                name = [n for n, x in zip(names, floats + ints) if x is t][0]
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of {B} values")
+    if logits.get_device() != dev:
+        _check_device(dev, ("logits", logits))
+    st = _sample(logits.data_ptr(), ld, B, V, _p(temperature), _p(top_k), _p(top_p), _p(min_p),
+                 u.data_ptr(), out.data_ptr(), _p(kept), _p(logprob), _raw_stream(stream, dev))
+    if st:
+        raise QGError("qg_sample_filtered", st, last_error())
 
 
 def qg_decode_attention_static_scratch_capacity():
@@ -432,19 +438,10 @@ def qg_dequant_q4_0(blocks, out, stream=None):
 _PAGED_KV = struct.Struct("@PPPPiiiii").pack  # the fields of qg_paged_kv
 
 
-def _fast_call(name):
-    """``_call`` of one entry point, looked up once."""
-    fn = getattr(lib, name)
-
-    def call(*args):
-        st = fn(*args)
-        if st != QG_OK:
-            raise QGError(name, st, last_error())
-    return call
-
-
-_append, _gather, _attend, _sample = map(_fast_call, (
-    "qg_paged_kv_append", "qg_paged_kv_gather", "qg_paged_attention", "qg_sample_filtered"))
+_append, _gather = lib.qg_paged_kv_append, lib.qg_paged_kv_gather
+_attend, _sample = lib.qg_paged_attention, lib.qg_sample_filtered
+_f32, _bf16, _i32 = torch.float32, torch.bfloat16, torch.int32
+_TYPES = {_f32: QG_F32, _bf16: QG_BF16}
 
 
 def _check_device(dev, *named):
@@ -527,13 +524,18 @@ class PagedKV:
         if len(shape) != 2:
             raise ValueError("page_table must be [B, max_pages]")
         B, most = shape
-        _check_index(dev, "page_table", page_table, B * most)
-        if lens is not None:
+        if page_table.dtype is not _i32 or not page_table.is_contiguous() \
+                or page_table.get_device() != dev:
+            _check_index(dev, "page_table", page_table, B * most)
+        if lens is not None and (lens.dtype is not _i32 or lens.numel() != B
+                                 or not lens.is_contiguous() or lens.get_device() != dev):
             _check_index(dev, lens_name, lens, B)
-        if row_start is not None:
+        if row_start is None:
+            if T != B:
+                raise ValueError(f"{T} rows of {B} sequences need row_start")
+        elif row_start.dtype is not _i32 or row_start.numel() != B + 1 \
+                or not row_start.is_contiguous() or row_start.get_device() != dev:
             _check_index(dev, "row_start", row_start, B + 1)
-        elif T != B:
-            raise ValueError(f"{T} rows of {B} sequences need row_start")
         return B, most
 
 
@@ -550,22 +552,27 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
     dev = _current_device()
     D = kv.head_dim
     W = kv.kv_heads * D
-    T, dt = k.shape[0], k.dtype
+    dt = k.dtype
     if kv_len is None:
         raise ValueError("kv_len is needed")
-    B, most = kv._batch(page_table, kv_len, "kv_len", row_start, T, dev)
     k_ld, v_ld = _rows_of("k", k, W), _rows_of("v", v, W)
+    T = k.shape[0]
     if v.shape[0] != T or v.dtype is not dt:
         raise ValueError("v must have k's rows and type")
-    H, q_ld, qdt = 0, 0, QG_BF16
+    B, most = kv._batch(page_table, kv_len, "kv_len", row_start, T, dev)
+    H, q_ld, qdt, q_at, out_at = 0, 0, QG_BF16, None, None
     if q is not None:
-        Q = q.shape[-1]
-        if q.shape[0] != T or q.dtype is not dt or Q % D:
+        shape = q.shape
+        Q = shape[-1]
+        if shape[0] != T or q.dtype is not dt or Q % D:
             raise ValueError(f"q must be [{T}, H * {D}] of k's type")
         H, q_ld = Q // D, _rows_of("q", q, Q)
-        if q_out is None or q_out.shape != q.shape or not q_out.is_contiguous():
+        if q_out is None or q_out.shape != shape or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous with q's shape")
-        qdt = _dt(q_out)
+        qdt = _TYPES.get(q_out.dtype)
+        if qdt is None:
+            _dt(q_out)
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     for t in (k, v, q, q_out, q_norm, k_norm):
         if t is not None and t.get_device() != dev:
             _check_device(dev, ("k", k), ("v", v), ("q", q), ("q_out", q_out), ("q_norm", q_norm),
@@ -573,10 +580,17 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
     for w in (q_norm, k_norm):
         if w is not None and (w.numel() != D or w.element_size() != 2 or not w.is_contiguous()):
             raise ValueError(f"q_norm and k_norm must be {D} bf16 values")
-    _append(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(), _p(row_start), _p(q), q_ld,
-            k.data_ptr(), k_ld, v.data_ptr(), v_ld, _dt(k), _p(q_norm), _p(k_norm), eps, theta,
-            D if rotary_dim is None else rotary_dim, _p(q_out), qdt, B, T, H,
-            _raw_stream(stream, dev))
+    xdt = _TYPES.get(dt)
+    if xdt is None:
+        _dt(k)
+    st = _append(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(),
+                 None if row_start is None else row_start.data_ptr(), q_at, q_ld, k.data_ptr(),
+                 k_ld, v.data_ptr(), v_ld, xdt, None if q_norm is None else q_norm.data_ptr(),
+                 None if k_norm is None else k_norm.data_ptr(), eps, theta,
+                 D if rotary_dim is None else rotary_dim, out_at, qdt, B, T, H,
+                 _raw_stream(stream, dev))
+    if st:
+        raise QGError("qg_paged_kv_append", st, last_error())
 
 
 def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None, stream=None):
@@ -587,16 +601,26 @@ def qg_paged_kv_gather(kv, page_table, first, row_start, k_out=None, v_out=None,
     if one is None:
         return
     dev = _current_device()
-    T = one.shape[0]
+    shape, dt = one.shape, one.dtype
+    T = shape[0]
     B, most = kv._batch(page_table, first, "first", row_start, T, dev)
+    good = len(shape) == 2 and shape[1] == kv.kv_heads * kv.head_dim
     for t in (k_out, v_out):
-        if t is not None and (t.shape != (T, kv.kv_heads * kv.head_dim) or t.dtype is not one.dtype
-                              or not t.is_contiguous()):
-            raise ValueError(f"k_out and v_out must be contiguous [{T}, "
-                             f"{kv.kv_heads * kv.head_dim}] of one type")
-    _check_device(dev, ("k_out", k_out), ("v_out", v_out))
-    _gather(kv.c_kv, page_table.data_ptr(), most, _p(first), _p(row_start), _p(k_out),
-            _p(v_out), _dt(one), B, T, _raw_stream(stream, dev))
+        if t is not None:
+            if t is not one and t.shape != shape or t.dtype is not dt or not t.is_contiguous():
+                good = False
+            elif t.get_device() != dev:
+                _check_device(dev, ("k_out", k_out), ("v_out", v_out))
+    if not good:
+        raise ValueError(f"k_out and v_out must be contiguous [{T}, "
+                         f"{kv.kv_heads * kv.head_dim}] of one type")
+    st = _gather(kv.c_kv, page_table.data_ptr(), most, None if first is None else first.data_ptr(),
+                 None if row_start is None else row_start.data_ptr(),
+                 None if k_out is None else k_out.data_ptr(),
+                 None if v_out is None else v_out.data_ptr(), _dt(one), B, T,
+                 _raw_stream(stream, dev))
+    if st:
+        raise QGError("qg_paged_kv_gather", st, last_error())
 
 
 def qg_paged_attention_workspace_size(head_dim):
@@ -610,17 +634,22 @@ def qg_paged_attention(kv, page_table, kv_len, q, out, H, scale, ws, row_start=N
     counts the rows' own tokens; row_start int32 [B+1], or None for one row
     per sequence; ws of qg_paged_attention_workspace_size(D) bytes."""
     dev = _current_device()
-    T = q.shape[0]
+    shape = q.shape
+    T = shape[0]
     if kv_len is None:
         raise ValueError("kv_len is needed")
     B, most = kv._batch(page_table, kv_len, "kv_len", row_start, T, dev)
-    if q.shape != (T, H * kv.head_dim) or out.shape != q.shape or \
+    if len(shape) != 2 or shape[1] != H * kv.head_dim or out.shape != shape or \
             not (q.is_contiguous() and out.is_contiguous()):
         raise ValueError(f"q and out must be contiguous [T, {H} * {kv.head_dim}]")
-    _check_device(dev, ("q", q), ("out", out), ("ws", ws))
-    _attend(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(), _p(row_start),
-            q.data_ptr(), _dt(q), out.data_ptr(), _dt(out), B, T, H, scale, ws.data_ptr(),
-            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev:
+        _check_device(dev, ("q", q), ("out", out), ("ws", ws))
+    st = _attend(kv.c_kv, page_table.data_ptr(), most, kv_len.data_ptr(),
+                 None if row_start is None else row_start.data_ptr(), q.data_ptr(), _dt(q),
+                 out.data_ptr(), _dt(out), B, T, H, scale, ws.data_ptr(), ws.nbytes,
+                 _raw_stream(stream, dev))
+    if st:
+        raise QGError("qg_paged_attention", st, last_error())
 
 
 # ---------------------------------------------------------- decode step ----
