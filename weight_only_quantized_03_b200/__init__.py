@@ -482,17 +482,23 @@ class PagedKV:
             raise ValueError("k_pages and v_pages must be [num_pages, kv_heads, page_size, "
                              "head_dim] of one type")
         int8 = dtype is torch.int8
-        if not int8 and dtype is not torch.bfloat16:
+        if not int8 and dtype is not _bf16:
             raise TypeError(f"pages must be bfloat16 or int8, not {dtype}")
         P, Hkv, size, D = shape
         self.device_index = dev = k_pages.get_device()
-        for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if (s is not None) != int8:
-                raise ValueError(f"{name} goes with int8 pages only, and they need it")
-            if int8 and (s.dtype is not torch.float32 or s.shape != (P, Hkv, size // QG_KV_BLOCK)
-                         or not s.is_contiguous() or s.get_device() != dev):
-                raise ValueError(f"{name} must be contiguous fp32 "
-                                 f"[{P}, {Hkv}, {size // QG_KV_BLOCK}] on the pages' device")
+        ks = vs = 0
+        if int8:
+            blocks = (P, Hkv, size // QG_KV_BLOCK)
+            for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
+                if s is None:
+                    raise ValueError(f"{name} goes with int8 pages only, and they need it")
+                if s.dtype is not _f32 or s.shape != blocks or not s.is_contiguous() \
+                        or s.get_device() != dev:
+                    raise ValueError(f"{name} must be contiguous fp32 {list(blocks)} on the "
+                                     f"pages' device")
+            ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales and v_scales go with int8 pages only")
         if not (k_pages.is_contiguous() and v_pages.is_contiguous()
                 and v_pages.get_device() == dev):
             raise ValueError("k_pages and v_pages must be contiguous, on one device")
@@ -500,9 +506,7 @@ class PagedKV:
                                                                     v_scales)
         self.kv_heads, self.page_size, self.head_dim = Hkv, size, D
         # the C struct qg_paged_kv (read during a call only)
-        self.c_kv = _PAGED_KV(k_pages.data_ptr(), v_pages.data_ptr(),
-                              k_scales.data_ptr() if int8 else 0,
-                              v_scales.data_ptr() if int8 else 0, P, size, Hkv, D,
+        self.c_kv = _PAGED_KV(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, P, size, Hkv, D,
                               QG_KV_INT8 if int8 else QG_KV_BF16)
 
     @classmethod
