@@ -314,3 +314,37 @@ def test_append_on_a_side_stream_and_captured():
     for a, b, c in zip(*pools):
         np.testing.assert_array_equal(a, b)
         np.testing.assert_array_equal(a, c)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_append_of_prompts_in_place_and_apart_are_the_same(kind):
+    """q rotated onto itself, K and V slices of one projection: the same bits
+    as from tensors of their own, whole blocks and their ends."""
+    D, H, Hkv, page = 128, 6, 2, 32
+    n, before = [37, 0, 3, 16], [5, 9, 30, 0]
+    T, B = sum(n), len(n)
+    g = torch.Generator(device="cuda").manual_seed(77)
+    dt = torch.int8 if kind == "int8" else torch.bfloat16
+    x = torch.randn((T, (H + 2 * Hkv) * D), generator=g, device="cuda").bfloat16()
+    w = [(1 + 0.1 * torch.randn(D, generator=g, device="cuda")).bfloat16() for _ in range(2)]
+    table = torch.randperm(B * 4, generator=g, device="cuda").view(B, 4).int()
+    lens = dev(np.array([a + b for a, b in zip(n, before)], np.int32))
+    rs = dev(starts(n))
+    got = []
+    for apart in (False, True):
+        kv = qg.PagedKV.empty(B * 4, page, Hkv, D, dt)
+        for t in (kv.k_pages, kv.v_pages, kv.k_scales, kv.v_scales):
+            if t is not None:
+                t.zero_()
+        q, k, v = x.split((H * D, Hkv * D, Hkv * D), 1)
+        q = q.contiguous()
+        out = torch.zeros_like(q) if apart else q
+        if apart:
+            k, v = k.contiguous(), v.contiguous()
+        qg.qg_paged_kv_append(kv, table, lens, k, v, row_start=rs, q=q, q_out=out, q_norm=w[0],
+                              k_norm=w[1], theta=1e4, rotary_dim=96)
+        torch.cuda.synchronize()
+        got.append([out] + [t for t in (kv.k_pages, kv.v_pages, kv.k_scales, kv.v_scales)
+                            if t is not None])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert got[0][0].abs().max() > 0 and got[0][1].float().abs().max() > 0
