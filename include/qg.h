@@ -548,9 +548,10 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  * bf16 values, q) but for the softmax weights (fp16 with int8 pages, bf16
  * with bf16 pages); sums, maxima and scales in fp32. With an fp32 q or out,
  * q and the weights are carried in several 16-bit terms (22 bits or more).
- * Prompts (head_dim <= 128, bf16 q and out, 32 or more row-head pairs of a
- * KV head per sequence on average) run on tcgen05; the waits inside that
- * kernel are bounded in time (1 s), and one that gives up makes its rows NaN.
+ * Larger calls with head_dim <= 128, bf16 q and out and more than 8 row-head
+ * pairs of a KV head per sequence (prompts, mostly) run on tcgen05; the waits
+ * inside that kernel are bounded in time (1 s), and one that gives up makes its
+ * rows NaN.
  * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0, and
  * (T * H / 8 + B * kv_heads) * (max_pages * page_size / 128 + 1) < 2^31. */
 size_t qg_paged_attention_workspace_size(int head_dim);

@@ -44,7 +44,7 @@
 // balanced, and the grid never depends on them. An item inside one piece is
 // written out; the others' parts go to the workspace and a second small launch
 // merges them in order. Results do not depend on scheduling in either.
-// Prompts with a bf16 q and out go to the tcgen05 kernel of
+// Larger prompts with a bf16 q and out go to the tcgen05 kernel of
 // paged_attention_tc.cu.
 #include <cuda_fp16.h>
 
@@ -58,7 +58,8 @@
 namespace qg {
 namespace pa {
 
-constexpr int kWarps = 8;            // split kernel
+constexpr int kWarps = 8;            // of the cluster and split kernels
+constexpr int kCols = 8;             // (row, head) columns of a tile
 constexpr int kChunk = kWarps * kBlock;
 constexpr int kMergeThreads = 512;
 constexpr int kSlack = 2;            // chunks (see plan)
@@ -141,48 +142,45 @@ __device__ __forceinline__ void load_q(const Params& P, const Item& it, int c, i
 }
 
 // Where element (column n, dim d) of Q lies in the fragments' order
-// [k step][column tile][term][lane][4] of 16-bit values: a lane's 16 bytes
+// [k step][term][lane][4] of 16-bit values: a lane's 16 bytes
 // of a K row are neighbouring dims, four per k step.
-template <bool I8, int NT, int QS>
+template <bool I8, int QS>
 __device__ __forceinline__ int q_at(int n, int d, int term) {
   constexpr int PL = I8 ? 16 : 8;  // dims of a lane's 16 bytes
   const int t = d % (4 * PL) / PL, ks = d / (4 * PL) * (PL / 4) + d % PL / 4;
-  return (((ks * NT + n / 8) * QS + term) * 32 + (n % 8) * 4 + t) * 4 + d % 4;
+  return ((ks * QS + term) * 32 + (n % 8) * 4 + t) * 4 + d % 4;
 }
 
 // Stores a lane's neighbouring values of one column, split into QS terms.
-template <int D, bool I8, int NT, int QS>
+template <int D, bool I8, int QS>
 __device__ __forceinline__ void put_q(uint16_t* sq, int n, int lane, float (&x)[D / 32]) {
 #pragma unroll
   for (int s = 0; s < QS; ++s)
 #pragma unroll
     for (int e = 0; e < D / 32; e += 2)
-      *reinterpret_cast<uint32_t*>(sq + q_at<I8, NT, QS>(n, lane * (D / 32) + e, s)) =
+      *reinterpret_cast<uint32_t*>(sq + q_at<I8, QS>(n, lane * (D / 32) + e, s)) =
           take16<I8>(x[e], x[e + 1]);
 }
 
 // A warp's running state over the columns of its item.
-template <int D, int NT>
+template <int D>
 struct State {
-  float m[NT][2], l[NT][2];   // columns 8 nt + 2 t (+ 1): reference, this lane's weights
-  float o[D / 16][NT][4];     // dims g D/8 + 2 i (+ 1), columns 2 t (+ 1)
-  float r;                    // unit of o: the V scales seen are at most r
+  float m[2], l[2];        // columns 2 t (+ 1): reference, this lane's weights
+  float o[D / 16][4];      // dims g D/8 + 2 i (+ 1), columns 2 t (+ 1)
+  float r;                 // unit of o: the V scales seen are at most r
 
   __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -FLT_MAX;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      m[j][0] = m[j][1] = -FLT_MAX;
-      l[j][0] = l[j][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
-    }
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     r = FLT_MIN;
   }
 };
 
 // A warp's walk over tiles first, first + step, ... < end of one sequence
 // and KV head: page lookups 32 tiles at a time, K and V one tile ahead.
-template <int D, bool I8, int NT, int QS, int PS>
+template <int D, bool I8, int QS, int PS>
 struct Walk {
   static constexpr int ES = I8 ? 1 : 2;
   static constexpr int KC = D * ES / 64;        // 16-byte pieces of a lane per K row
@@ -190,9 +188,9 @@ struct Walk {
   static constexpr int VC = (VB + 15) / 16;
   const Params& P;
   const int lane, g, t;
-  int lim[NT][2];     // visible tokens of the lane's columns
+  int lim[2];     // visible tokens of the lane's columns
   int min_lim, len;   // of all the item's columns; cached tokens
-  float qf[NT][2];    // scale_log2 / 2^e of the lane's columns
+  float qf[2];    // scale_log2 / 2^e of the lane's columns
   const uint16_t* sq;
   uint4 kr[2][KC];
   uint4 vr[4][VC];
@@ -251,13 +249,10 @@ struct Walk {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
   }
 
-  __device__ __forceinline__ void scores(float (&s)[NT][4]) {
-    float rest[QS > 1 ? NT : 1][4];  // of q's lower terms (see weigh)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if constexpr (QS > 1) rest[j][0] = rest[j][1] = rest[j][2] = rest[j][3] = 0.f;
-    }
+  __device__ __forceinline__ void scores(float (&s)[4]) {
+    float rest[4];  // of q's lower terms (see weigh)
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+    if constexpr (QS > 1) rest[0] = rest[1] = rest[2] = rest[3] = 0.f;
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
 #pragma unroll
@@ -277,39 +272,32 @@ struct Walk {
         }
         const int step = c * (I8 ? 4 : 2) + u;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-          for (int e = 0; e < QS; ++e) {
-            const uint2 b = *reinterpret_cast<const uint2*>(
-                sq + (((step * NT + j) * QS + e) * 32 + lane) * 4);
-            mma<I8>(e ? rest[QS > 1 ? j : 0] : s[j], a0, a1, a2, a3, b.x, b.y);
-          }
+        for (int e = 0; e < QS; ++e) {
+          const uint2 b =
+              *reinterpret_cast<const uint2*>(sq + ((step * QS + e) * 32 + lane) * 4);
+          mma<I8>(e ? rest : s, a0, a1, a2, a3, b.x, b.y);
         }
       }
     }
     if constexpr (QS > 1) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] += rest[j][e];
+      for (int e = 0; e < 4; ++e) s[e] += rest[e];
     }
   }
 
   // bf16 pages, a tile that some columns see in part, with V values that are
   // not finite: 0 * NaN must not reach the columns that do not see them, so
   // the products are formed one by one (never taken with finite values).
-  static __device__ __forceinline__ void accumulate_seen(State<D, NT>& S, const float (&p)[NT][4],
+  static __device__ __forceinline__ void accumulate_seen(State<D>& S, const float (&p)[4],
                                                       const uint4 (&vr)[4][VC], int lane) {
     const int t = lane & 3;
 #pragma unroll 1
     for (int key = 0; key < kBlock; ++key) {
       const int slot = (key & 1) + 2 * (key >> 3), src = (lane & ~3) | ((key & 7) >> 1);
-      float w[NT][2];
+      float w[2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          w[j][e] = __shfl_sync(0xffffffffu, key < 8 ? p[j][e] : p[j][2 + e], (key & 7) * 4 + t);
+      for (int e = 0; e < 2; ++e)
+        w[e] = __shfl_sync(0xffffffffu, key < 8 ? p[e] : p[2 + e], (key & 7) * 4 + t);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t mine = slot == 0   ? word(vr[0][i / 4], i % 4)
@@ -318,18 +306,16 @@ struct Walk {
                                           : word(vr[3][i / 4], i % 4);
         const uint32_t x = __shfl_sync(0xffffffffu, mine, src);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (w[j][e] != 0.f) {
-              S.o[i][j][e] = fmaf(w[j][e], bf16_lo(x), S.o[i][j][e]);
-              S.o[i][j][2 + e] = fmaf(w[j][e], bf16_hi(x), S.o[i][j][2 + e]);
-            }
+        for (int e = 0; e < 2; ++e)
+          if (w[e] != 0.f) {
+            S.o[i][e] = fmaf(w[e], bf16_lo(x), S.o[i][e]);
+            S.o[i][2 + e] = fmaf(w[e], bf16_hi(x), S.o[i][2 + e]);
+          }
       }
     }
   }
 
-  __device__ __forceinline__ void weigh(State<D, NT>& S, float (&p)[NT][4], bool part) {
+  __device__ __forceinline__ void weigh(State<D>& S, float (&p)[4], bool part) {
     if constexpr (!I8) {
       if (part) {
         bool odd = false;
@@ -348,14 +334,12 @@ struct Walk {
         }
       }
     }
-    uint32_t b[NT][PS][2];
+    uint32_t b[PS][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < PS; ++e) {
-        b[j][e][0] = transpose8x8(take16<I8>(p[j][0], p[j][1]));
-        b[j][e][1] = transpose8x8(take16<I8>(p[j][2], p[j][3]));
-      }
+    for (int e = 0; e < PS; ++e) {
+      b[e][0] = transpose8x8(take16<I8>(p[0], p[1]));
+      b[e][1] = transpose8x8(take16<I8>(p[2], p[3]));
+    }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t a0, a1, a2, a3;
@@ -383,17 +367,14 @@ struct Walk {
       // by itself, smallest term first, and added to the running one with
       // rounding, which keeps a long cache's sum at fp32's accuracy (32749
       // tokens: 1.3e-6 off with the terms added to the running sum).
+      if constexpr (PS == 1) {
+        mma<I8>(S.o[i], a0, a1, a2, a3, b[0][0], b[0][1]);
+      } else {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (PS == 1) {
-          mma<I8>(S.o[i][j], a0, a1, a2, a3, b[j][0][0], b[j][0][1]);
-        } else {
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int e = PS - 1; e >= 0; --e) mma<I8>(t, a0, a1, a2, a3, b[e][0], b[e][1]);
 #pragma unroll
-          for (int e = PS - 1; e >= 0; --e) mma<I8>(t, a0, a1, a2, a3, b[j][e][0], b[j][e][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S.o[i][j][e] += t[e];
-        }
+        for (int e = 0; e < 4; ++e) S.o[i][e] += t[e];
       }
     }
   }
@@ -410,7 +391,7 @@ struct Walk {
     load_v(blk);
   }
 
-  __device__ __forceinline__ void run(State<D, NT>& S, const Item& it) {
+  __device__ __forceinline__ void run(State<D>& S, const Item& it) {
     if (tile >= end) return;
     int at = 0;  // the tile's place in the batch of lookups
     for (;;) {
@@ -420,27 +401,22 @@ struct Walk {
         lookup(it, tile + step);
       }
       const int next = __shfl_sync(0xffffffffu, blocks, at);
-      float p[NT][4];
+      float p[4];
       scores(p);
-      float f[NT][2];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        f[j][0] = qf[j][0] * ks;
-        f[j][1] = qf[j][1] * ks;
-      }
+      float f[2];
+      f[0] = qf[0] * ks;
+      f[1] = qf[1] * ks;
       if (more) load_k(next);
       // scores in log2 units, masked
       const int key0 = tile * kBlock + g;
       const bool part = tile * kBlock + kBlock > min_lim;
       bool over = false;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[j][e] *= f[j][e & 1];
-          if (part && key0 + 8 * (e >> 1) >= lim[j][e & 1]) p[j][e] = -INFINITY;
-          over |= p[j][e] > S.m[j][e & 1] + kMargin;
-        }
+      for (int e = 0; e < 4; ++e) {
+        p[e] *= f[e & 1];
+        if (part && key0 + 8 * (e >> 1) >= lim[e & 1]) p[e] = -INFINITY;
+        over |= p[e] > S.m[e & 1] + kMargin;
+      }
       const bool wider = I8 && fabsf(vs) > S.r && fabsf(vs) <= FLT_MAX;  // the same in all lanes
       if (__any_sync(0xffffffffu, over) || wider) {
         float down = 1.f;
@@ -450,43 +426,38 @@ struct Walk {
           down = S.r / r;
           S.r = r;
         }
+        float a[2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float a[2];
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(p[e], p[2 + e]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, S.m[e]);
+          a[e] = ex2(S.m[e] - x);
+          S.m[e] = x;
+          S.l[e] *= a[e];
+        }
+        a[0] *= down;
+        a[1] *= down;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(p[j][e], p[j][2 + e]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, S.m[j][e]);
-            a[e] = ex2(S.m[j][e] - x);
-            S.m[j][e] = x;
-            S.l[j][e] *= a[e];
-          }
-          a[0] *= down;
-          a[1] *= down;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            S.o[i][j][0] *= a[0];
-            S.o[i][j][1] *= a[1];
-            S.o[i][j][2] *= a[0];
-            S.o[i][j][3] *= a[1];
-          }
+        for (int i = 0; i < D / 16; ++i) {
+          S.o[i][0] *= a[0];
+          S.o[i][1] *= a[1];
+          S.o[i][2] *= a[0];
+          S.o[i][3] *= a[1];
         }
       }
       const float wv = I8 ? vs * (1.f / S.r) * 2048.f : 1.f;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = ex2(p[j][e] - S.m[j][e & 1]);
-          S.l[j][e & 1] += x;
-          // a token that the column does not see keeps weight 0 whatever the
-          // block's scale is
-          if constexpr (I8) p[j][e] = part && p[j][e] == -INFINITY ? 0.f : x * wv;
-          else p[j][e] = x;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float x = ex2(p[e] - S.m[e & 1]);
+        S.l[e & 1] += x;
+        // a token that the column does not see keeps weight 0 whatever the
+        // block's scale is
+        if constexpr (I8) p[e] = part && p[e] == -INFINITY ? 0.f : x * wv;
+        else p[e] = x;
+      }
       weigh(S, p, part);
       if (!more) break;
       tile += step;
@@ -501,47 +472,39 @@ __device__ __forceinline__ float o_unit(float r) {
   return I8 ? r * (1.f / 2048.f) : 1.f;
 }
 
-// q of the item's column tile into shared memory, a warp per column, with
-// the factor that turns a column's products into log2 units in sf. The loads
-// go out first (take), so that they overlap the first keys' ones.
-template <int D, bool I8, int NT, int QS, int PER>
-struct StageQ {  // columns first, first + step, ... (PER of them)
-  float x[PER][D / 32];
-  __device__ __forceinline__ void take(const Params& P, const Item& it, int first, int step,
-                                       int lane) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) load_q<D>(P, it, it.ct * NT * 8 + first + i * step, lane, x[i]);
+// q of the item's column tile into shared memory, a column a warp, with the
+// factor that turns a column's products into log2 units in sf. The loads go
+// out first (take), so that they overlap the first keys' ones.
+template <int D, bool I8, int QS>
+struct StageQ {
+  static_assert(kCols == kWarps, "a column a warp");
+  float x[D / 32];
+  __device__ __forceinline__ void take(const Params& P, const Item& it, int warp, int lane) {
+    load_q<D>(P, it, it.ct * kCols + warp, lane, x);
   }
-  __device__ __forceinline__ void put(const Params& P, uint16_t* sq, float* sf, int first, int step,
-                                      int lane) {
+  __device__ __forceinline__ void put(const Params& P, uint16_t* sq, float* sf, int warp, int lane) {
+    float unit = 1.f;
+    if constexpr (I8) {
+      float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int n = first + i * step;
-      float unit = 1.f;
-      if constexpr (I8) {
-        float top = 0.f;
+      for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(x[e]));
+      unit = q_unit(warp_max(top));
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(x[i][e]));
-        unit = q_unit(warp_max(top));
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) x[i][e] *= unit;
-      }
-      put_q<D, I8, NT, QS>(sq, n, lane, x[i]);
-      if (lane == 0) sf[n] = P.scale_log2 / unit;
+      for (int e = 0; e < D / 32; ++e) x[e] *= unit;
     }
+    put_q<D, I8, QS>(sq, warp, lane, x);
+    if (lane == 0) sf[warp] = P.scale_log2 / unit;
   }
 };
 
-template <int NT, class W>
+template <class W>
 __device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w) {
   int lo = 0x7FFFFFFF;
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      w.lim[j][e] = visible(P, it, it.ct * NT * 8 + j * 8 + 2 * w.t + e);
-      lo = min(lo, w.lim[j][e]);
-    }
+  for (int e = 0; e < 2; ++e) {
+    w.lim[e] = visible(P, it, it.ct * kCols + 2 * w.t + e);
+    lo = min(lo, w.lim[e]);
+  }
   lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
   w.min_lim = min(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
 }
@@ -559,47 +522,43 @@ __device__ __forceinline__ void store_out(const Params& P, const Item& it, int c
 
 // A warp's state to shared memory: weights summed over the lanes that share a
 // column, outputs in plain units.
-template <int D, bool I8, int NT>
-__device__ __forceinline__ void put_state(const State<D, NT>& S, float* so, float* sm, float* sl,
+template <int D, bool I8>
+__device__ __forceinline__ void put_state(const State<D>& S, float* so, float* sm, float* sl,
                                           int cols, int warp, int lane) {
-  constexpr int NC = NT * 8;
   const int g = lane >> 2, t = lane & 3;
   const float u = o_unit<I8>(S.r);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = S.l[j][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int n = j * 8 + 2 * t + e;
-      if (n < cols) {
-        if (g == 0) {
-          sm[warp * NC + n] = S.m[j][e];
-          sl[warp * NC + n] = l;
-        }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(so + (warp * NC + n) * D + g * (D / 8) + 2 * i) =
-              make_float2(S.o[i][j][e] * u, S.o[i][j][2 + e] * u);
+  for (int e = 0; e < 2; ++e) {
+    float l = S.l[e];
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    const int n = 2 * t + e;
+    if (n < cols) {
+      if (g == 0) {
+        sm[warp * kCols + n] = S.m[e];
+        sl[warp * kCols + n] = l;
       }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<float2*>(so + (warp * kCols + n) * D + g * (D / 8) + 2 * i) =
+            make_float2(S.o[i][e] * u, S.o[i][2 + e] * u);
     }
   }
 }
 // The CTA's reference M, weights' sum L and output O at column n, dim d.
-template <int D, int NC>
+template <int D>
 __device__ __forceinline__ void join_warps(const float* so, const float* sm, const float* sl, int n,
                                            int d, float& M, float& L, float& O) {
   M = sm[n];
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) M = fmaxf(M, sm[k * NC + n]);
+  for (int k = 1; k < kWarps; ++k) M = fmaxf(M, sm[k * kCols + n]);
   L = O = 0.f;
 #pragma unroll
   for (int k = 0; k < kWarps; ++k) {
-    const float a = ex2(sm[k * NC + n] - M);
-    L = fmaf(a, sl[k * NC + n], L);
-    O = fmaf(a, so[(k * NC + n) * D + d], O);
+    const float a = ex2(sm[k * kCols + n] - M);
+    L = fmaf(a, sl[k * kCols + n], L);
+    O = fmaf(a, so[(k * kCols + n) * D + d], O);
   }
 }
 
@@ -610,8 +569,8 @@ __device__ __forceinline__ void join_warps(const float* so, const float* sm, con
 // 2^31.
 struct SeqWork {
   int tiles, chunks;
-  __device__ __forceinline__ SeqWork(const Params& P, const Item& it, int NC) {
-    tiles = (it.n * P.G + NC - 1) / NC;
+  __device__ __forceinline__ SeqWork(const Params& P, const Item& it) {
+    tiles = (it.n * P.G + kCols - 1) / kCols;
     chunks = max(1, (it.len + kChunk - 1) / kChunk);
   }
   __device__ __forceinline__ unsigned total(int Hkv) const {
@@ -637,7 +596,7 @@ struct Cut {
 // Running sums over the sequences, 32 at a time (every warp by itself): f
 // gets a sequence (its item's n is 0 past the last one), its work, and the
 // chunks before it; returns all chunks.
-template <int NC, class F>
+template <class F>
 __device__ __forceinline__ unsigned each_seq(const Params& P, F f) {
   const int lane = threadIdx.x & 31;
   unsigned before = 0;
@@ -645,7 +604,7 @@ __device__ __forceinline__ unsigned each_seq(const Params& P, F f) {
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     Item it = {0, 0, 0, 0, 0, 0};
     if (b0 + lane < P.B) set_seq(P, it, b0 + lane);
-    const SeqWork w(P, it, NC);
+    const SeqWork w(P, it);
     const unsigned mine = w.total(P.Hkv);
     unsigned x = mine;
 #pragma unroll
@@ -662,20 +621,17 @@ __device__ __forceinline__ unsigned each_seq(const Params& P, F f) {
 // CTAs of the split kernel that an SM holds: two where a warp's keys, next
 // keys and sums fit 128 registers. (bf16 pages of head size 128 at two CTAs
 // spilled: 42.6 us against 37.8 for 32749 tokens in fp32.)
-constexpr int split_ctas(int D, bool i8, int nt) {
-  return nt == 1 && (D <= 64 || (i8 && D <= 128)) ? 2 : 1;
-}
+constexpr int split_ctas(int D, bool i8) { return D <= 64 || (i8 && D <= 128) ? 2 : 1; }
 
-template <int D, bool I8, int NT, int QS, int PS>
-__global__ void __launch_bounds__(kWarps * 32, split_ctas(D, I8, NT))
+template <int D, bool I8, int QS, int PS>
+__global__ void __launch_bounds__(kWarps * 32, split_ctas(D, I8))
 split_kernel(const __grid_constant__ Params P) {
-  constexpr int NC = NT * 8;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* so = reinterpret_cast<float*>(smem);            // [kWarps][NC][D]
-  float* sm = so + kWarps * NC * D;                      // [kWarps][NC]
-  float* sl = sm + kWarps * NC;                          // [kWarps][NC]
-  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * NC);  // fragments of q
-  __shared__ float sf[NC];
+  float* so = reinterpret_cast<float*>(smem);            // [kWarps][kCols][D]
+  float* sm = so + kWarps * kCols * D;                      // [kWarps][kCols]
+  float* sl = sm + kWarps * kCols;                          // [kWarps][kCols]
+  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * kCols);  // fragments of q
+  __shared__ float sf[kCols];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();  // the merge may find its items meanwhile
@@ -703,7 +659,7 @@ split_kernel(const __grid_constant__ Params P) {
   if (P.B <= 32) {
     Item mine;
     unsigned before, len;
-    piece(each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
+    piece(each_seq(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
       mine = i;
       before = b;
       len = l;
@@ -711,39 +667,36 @@ split_kernel(const __grid_constant__ Params P) {
     if (pos >= stop) return;
     settle(mine, before, len);
   } else {
-    piece(each_seq<NC>(P, [](const Item&, const SeqWork&, unsigned, unsigned) {}));
+    piece(each_seq(P, [](const Item&, const SeqWork&, unsigned, unsigned) {}));
     if (pos >= stop) return;
-    each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
+    each_seq(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned l) {
       settle(i, b, l);
     });
   }
-  SeqWork w(P, it, NC);
+  SeqWork w(P, it);
   // (head, column tile) of the sequence, and the item's first chunk here
   int unit = (int)(rest / (unsigned)w.chunks);
   int c0 = (int)rest - unit * w.chunks;
   it.h = unit / w.tiles;
   it.ct = unit - it.h * w.tiles;
 
-  Walk<D, I8, NT, QS, PS> walk(P, lane);
-  StageQ<D, I8, NT, QS, NT * 8 / kWarps> qs;
+  Walk<D, I8, QS, PS> walk(P, lane);
+  StageQ<D, I8, QS> qs;
   walk.sq = sq;
-  State<D, NT> S;
+  State<D> S;
   const auto start = [&](const Item& i, int first, int last) {  // chunks [first, last)
-    qs.take(P, i, warp, kWarps, lane);
+    qs.take(P, i, warp, lane);
     walk.len = i.len;
     walk.begin(i, first * kWarps + warp, kWarps, min(last * kWarps, (i.len + kBlock - 1) / kBlock));
   };
   int c1 = (int)min((unsigned)w.chunks, c0 + (stop - pos));
   start(it, c0, c1);
   for (;;) {
-    qs.put(P, sq, sf, warp, kWarps, lane);
-    set_limits<NT>(P, it, walk);
+    qs.put(P, sq, sf, warp, lane);
+    set_limits(P, it, walk);
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      walk.qf[j][0] = sf[j * 8 + 2 * walk.t];
-      walk.qf[j][1] = sf[j * 8 + 2 * walk.t + 1];
-    }
+    walk.qf[0] = sf[2 * walk.t];
+    walk.qf[1] = sf[2 * walk.t + 1];
     S.clear();
     walk.run(S, it);
     // the next item's first keys and q go out before this one is put away
@@ -758,7 +711,7 @@ split_kernel(const __grid_constant__ Params P) {
           if (it.b + 1 >= P.B) return;  // (unless row starts decrease)
           set_seq(P, it, it.b + 1);
         } while (it.n == 0);
-        w = SeqWork(P, it, NC);
+        w = SeqWork(P, it);
       }
       it.h = unit / w.tiles;
       it.ct = unit - it.h * w.tiles;
@@ -766,21 +719,21 @@ split_kernel(const __grid_constant__ Params P) {
       c1 = (int)min((unsigned)w.chunks, stop - pos);
       start(it, c0, c1);
     }
-    const int cols = min(NC, cur.n * P.G - cur.ct * NC);  // of the tile, real ones
-    put_state<D, I8, NT>(S, so, sm, sl, cols, warp, lane);
+    const int cols = min(kCols, cur.n * P.G - cur.ct * kCols);  // of the tile, real ones
+    put_state<D, I8>(S, so, sm, sl, cols, warp, lane);
     __syncthreads();
-    float* part = P.part + (long long)(2 * blockIdx.x + first_part) * NC * (D + 2);
+    float* part = P.part + (long long)(2 * blockIdx.x + first_part) * kCols * (D + 2);
     for (int i = tid; i < cols * D; i += kWarps * 32) {
       const int n = i / D, d = i % D;
       float M, L, O;
-      join_warps<D, NC>(so, sm, sl, n, d, M, L, O);
+      join_warps<D>(so, sm, sl, n, d, M, L, O);
       if (whole) {
-        store_out(P, cur, cur.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+        store_out(P, cur, cur.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
       } else {
-        part[2 * NC + i] = O;
+        part[2 * kCols + i] = O;
         if (d == 0) {
           part[n] = M;
-          part[NC + n] = L;
+          part[kCols + n] = L;
         }
       }
     }
@@ -808,20 +761,19 @@ __device__ __forceinline__ void cluster_sync() {
 
 // An item a cluster: its Z CTAs take equal shares of the item's chunks and
 // join their results through distributed shared memory, so one launch does.
-// A column tile's slot: a sequence with x columns has at most x / NC + 1 tiles,
-// so slot ranges [begin G / NC + b, end G / NC + b + 1) do not overlap.
+// A column tile's slot: a sequence with x columns has at most x / kCols + 1 tiles,
+// so slot ranges [begin G / kCols + b, end G / kCols + b + 1) do not overlap.
 constexpr int kMaxZ = 8;
 template <int D, bool I8, int QS, int PS>
-__global__ void __launch_bounds__(kWarps * 32, split_ctas(D, I8, 1))
+__global__ void __launch_bounds__(kWarps * 32, split_ctas(D, I8))
 cluster_kernel(const __grid_constant__ Params P) {
-  constexpr int NT = 1, NC = 8;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* so = reinterpret_cast<float*>(smem);            // [kWarps][NC][D]
-  float* sm = so + kWarps * NC * D;                      // [kWarps][NC]
-  float* sl = sm + kWarps * NC;                          // [kWarps][NC]
-  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * NC);  // fragments of q
-  __shared__ float sf[NC];
-  __shared__ float pm[NC], pl[NC], po[NC * D];           // the CTA's result
+  float* so = reinterpret_cast<float*>(smem);            // [kWarps][kCols][D]
+  float* sm = so + kWarps * kCols * D;                      // [kWarps][kCols]
+  float* sl = sm + kWarps * kCols;                          // [kWarps][kCols]
+  uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * kCols);  // fragments of q
+  __shared__ float sf[kCols];
+  __shared__ float pm[kCols], pl[kCols], po[kCols * D];           // the CTA's result
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Z = P.pieces, z = blockIdx.x % Z, u = blockIdx.x / Z;
   pdl_wait();
@@ -832,8 +784,8 @@ cluster_kernel(const __grid_constant__ Params P) {
   for (int b0 = 0; b0 < P.B && it.b < 0; b0 += 32) {
     Item mine = {-1, 0, 0, 0, 0, 0};
     if (b0 + lane < P.B) set_seq(P, mine, b0 + lane);
-    const int from = (int)((long long)mine.r0 * P.G / NC) + b0 + lane;
-    const int to = (int)((long long)(mine.r0 + mine.n) * P.G / NC) + b0 + lane;
+    const int from = (int)((long long)mine.r0 * P.G / kCols) + b0 + lane;
+    const int to = (int)((long long)(mine.r0 + mine.n) * P.G / kCols) + b0 + lane;
     const unsigned m = __ballot_sync(0xffffffffu, mine.n && u >= from && u <= to);
     if (m) {
       const int l = __ffs(m) - 1;
@@ -845,37 +797,34 @@ cluster_kernel(const __grid_constant__ Params P) {
     }
   }
   if (it.b < 0) return;  // (the cluster's CTAs alike)
-  const SeqWork w(P, it, NC);
+  const SeqWork w(P, it);
   if (it.ct >= w.tiles) return;
   it.h = blockIdx.y;
 
-  Walk<D, I8, NT, QS, PS> walk(P, lane);
-  StageQ<D, I8, NT, QS, NT * 8 / kWarps> qs;
+  Walk<D, I8, QS, PS> walk(P, lane);
+  StageQ<D, I8, QS> qs;
   walk.sq = sq;
-  State<D, NT> S;
+  State<D> S;
   const int c0 = (int)((long long)w.chunks * z / Z), c1 = (int)((long long)w.chunks * (z + 1) / Z);
-  qs.take(P, it, warp, kWarps, lane);
+  qs.take(P, it, warp, lane);
   walk.len = it.len;
   walk.begin(it, c0 * kWarps + warp, kWarps, min(c1 * kWarps, (it.len + kBlock - 1) / kBlock));
-  qs.put(P, sq, sf, warp, kWarps, lane);
-  set_limits<NT>(P, it, walk);
+  qs.put(P, sq, sf, warp, lane);
+  set_limits(P, it, walk);
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    walk.qf[j][0] = sf[j * 8 + 2 * walk.t];
-    walk.qf[j][1] = sf[j * 8 + 2 * walk.t + 1];
-  }
+  walk.qf[0] = sf[2 * walk.t];
+  walk.qf[1] = sf[2 * walk.t + 1];
   S.clear();
   walk.run(S, it);
-  const int cols = min(NC, it.n * P.G - it.ct * NC);
-  put_state<D, I8, NT>(S, so, sm, sl, cols, warp, lane);
+  const int cols = min(kCols, it.n * P.G - it.ct * kCols);
+  put_state<D, I8>(S, so, sm, sl, cols, warp, lane);
   __syncthreads();
   for (int i = tid; i < cols * D; i += kWarps * 32) {
     const int n = i / D, d = i % D;
     float M, L, O;
-    join_warps<D, NC>(so, sm, sl, n, d, M, L, O);
+    join_warps<D>(so, sm, sl, n, d, M, L, O);
     if (Z == 1) {
-      store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+      store_out(P, it, it.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
     } else {
       po[i] = O;
       if (d == 0) {
@@ -906,7 +855,7 @@ cluster_kernel(const __grid_constant__ Params P) {
       L = fmaf(a, l[k], L);
       O = fmaf(a, o[k], O);
     }
-    store_out(P, it, it.ct * NC + n, d, D, L != 0.f ? O / L : 0.f);
+    store_out(P, it, it.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
   }
   cluster_sync();  // nobody ends while its shared memory is read
 }
@@ -914,11 +863,10 @@ cluster_kernel(const __grid_constant__ Params P) {
 // ------------------------------------------------------------ merge kernel --
 
 // Items cut between pieces: one CTA per (column tile, head). A column tile's
-// slot: a sequence with x columns has at most x / NC + 1 tiles, so slot
-// ranges [begin G / NC + b, end G / NC + b + 1) do not overlap.
-template <int D, int NT>
+// slot: a sequence with x columns has at most x / kCols + 1 tiles, so slot
+// ranges [begin G / kCols + b, end G / kCols + b + 1) do not overlap.
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Params P) {
-  constexpr int NC = NT * 8;
   __shared__ float acc[kMergeThreads];
   const int tid = threadIdx.x, lane = tid & 31;
   // (the split kernel's CTAs have passed their own wait, so what came before
@@ -926,10 +874,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const int u = blockIdx.x;
   Item it = {-1, 0, 0, 0, 0, 0};
   unsigned before = 0;
-  const unsigned N = each_seq<NC>(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned) {
+  const unsigned N = each_seq(P, [&](const Item& i, const SeqWork&, unsigned b, unsigned) {
     const int end = i.r0 + i.n;
-    const bool in = i.n && u >= (int)((long long)i.r0 * P.G / NC + i.b) &&
-                    u <= (int)((long long)end * P.G / NC + i.b);
+    const bool in = i.n && u >= (int)((long long)i.r0 * P.G / kCols + i.b) &&
+                    u <= (int)((long long)end * P.G / kCols + i.b);
     const unsigned m = __ballot_sync(0xffffffffu, in);
     if (!m) return;
     const int l = __ffs(m) - 1;
@@ -945,8 +893,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     pdl_wait();
     return;
   }
-  const SeqWork w(P, it, NC);
-  it.ct = u - (int)((long long)it.r0 * P.G / NC + it.b);
+  const SeqWork w(P, it);
+  it.ct = u - (int)((long long)it.r0 * P.G / kCols + it.b);
   it.h = blockIdx.y;
   if (it.ct >= w.tiles) {
     pdl_wait();
@@ -960,10 +908,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const int p1 = (int)min(cut.piece_of(begin + w.chunks - 1), (unsigned)last);
   pdl_wait();
   if (p0 >= p1) return;  // written by its piece
-  const int np = p1 - p0 + 1, cols = min(NC, it.n * P.G - it.ct * NC);
+  const int np = p1 - p0 + 1, cols = min(kCols, it.n * P.G - it.ct * kCols);
   // part of piece p0 + p: it begins the item in its second slot
   auto part = [&](int p) {
-    return P.part + (long long)(2 * (p0 + p) + (p == 0)) * NC * (D + 2);
+    return P.part + (long long)(2 * (p0 + p) + (p == 0)) * kCols * (D + 2);
   };
   // A thread an output, a warp within one column (of this CTA's share of the
   // dims); few outputs: several groups of warps share the pieces.
@@ -976,20 +924,20 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     if (grp < groups) {
       // lane p: piece p's factor
       const float m = lane < np ? __ldcg(part(lane) + n) : -FLT_MAX;
-      const float l = lane < np ? __ldcg(part(lane) + NC + n) : 0.f;
+      const float l = lane < np ? __ldcg(part(lane) + kCols + n) : 0.f;
       float M = m;
       for (int p = 32 + lane; p < np; p += 32) M = fmaxf(M, __ldcg(part(p) + n));
       M = warp_max(M);
       float a = lane < np ? ex2(m - M) : 0.f, L = a * l;
       for (int p = 32 + lane; p < np; p += 32)
-        L = fmaf(ex2(__ldcg(part(p) + n) - M), __ldcg(part(p) + NC + n), L);
+        L = fmaf(ex2(__ldcg(part(p) + n) - M), __ldcg(part(p) + kCols + n), L);
       L = warp_sum(L);
       for (int p = grp, from = 0; p < np; from += 32) {
         if (from) a = from + lane < np ? ex2(__ldcg(part(from + lane) + n) - M) : 0.f;
         const int to = min(np, from + 32);
 #pragma unroll 8
         for (; p < to; p += groups)
-          O = fmaf(__shfl_sync(0xffffffffu, a, p - from), __ldcg(part(p) + 2 * NC + n * D + d), O);
+          O = fmaf(__shfl_sync(0xffffffffu, a, p - from), __ldcg(part(p) + 2 * kCols + n * D + d), O);
       }
       O = L != 0.f ? O / L : 0.f;
     }
@@ -999,7 +947,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       if (grp == 0)
         for (int g = 1; g < groups; ++g) O += acc[g * width + i];
     }
-    if (grp == 0) store_out(P, it, it.ct * NC + n, d, D, O);
+    if (grp == 0) store_out(P, it, it.ct * kCols + n, d, D, O);
   }
 }
 
@@ -1007,14 +955,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 
 template <int D, bool I8, int QS, int PS>
 cudaError_t launch_cluster(const Params& P, int z, cudaStream_t st) {
-  constexpr int NC = 8;
-  const size_t smem = (size_t)kWarps * NC * (D + 2) * 4 + (size_t)NC * D * QS * 2;
+  const size_t smem = (size_t)kWarps * kCols * (D + 2) * 4 + (size_t)kCols * D * QS * 2;
   const auto kernel = cluster_kernel<D, I8, QS, PS>;
   ensure_smem((const void*)kernel, (int)smem);
   Params Q = P;
   Q.pieces = z;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)P.T * P.G / NC + P.B) * z), P.Hkv);
+  cfg.gridDim = dim3((unsigned)(((long long)P.T * P.G / kCols + P.B) * z), P.Hkv);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1031,40 +978,45 @@ cudaError_t launch_cluster(const Params& P, int z, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, Q);
 }
 
-template <int D, bool I8, int NT, int QS, int PS>
-cudaError_t launch_split(const Params& P, int z, cudaStream_t st) {
-  if constexpr (NT == 1)
-    if (z) return launch_cluster<D, I8, QS, PS>(P, z, st);
-  constexpr int NC = NT * 8;
-  const size_t smem = (size_t)kWarps * NC * (D + 2) * 4 + (size_t)NC * D * QS * 2;
-  ensure_smem((const void*)split_kernel<D, I8, NT, QS, PS>, (int)smem);
-  cudaError_t e = launch_pdl(split_kernel<D, I8, NT, QS, PS>, dim3(P.pieces), dim3(kWarps * 32),
+template <int D, bool I8, int QS, int PS>
+cudaError_t launch_split(const Params& P, cudaStream_t st) {
+  const size_t smem = (size_t)kWarps * kCols * (D + 2) * 4 + (size_t)kCols * D * QS * 2;
+  ensure_smem((const void*)split_kernel<D, I8, QS, PS>, (int)smem);
+  cudaError_t e = launch_pdl(split_kernel<D, I8, QS, PS>, dim3(P.pieces), dim3(kWarps * 32),
                              smem, st, true, P);
   if (e != cudaSuccess || P.pieces == 1) return e;
-  const long long slots = (long long)P.T * P.G / NC + P.B;
+  const long long slots = (long long)P.T * P.G / kCols + P.B;
   // few items: their dims over several CTAs, so that a thread has few pieces
   unsigned parts = 1;  // of the dims
   while (parts * 2 <= D / 64 && slots * P.Hkv * parts * 2 <= 2 * num_sms()) parts *= 2;
-  return launch_pdl(merge_kernel<D, NT>, dim3((unsigned)slots, P.Hkv, parts), dim3(kMergeThreads), 0,
+  return launch_pdl(merge_kernel<D>, dim3((unsigned)slots, P.Hkv, parts), dim3(kMergeThreads), 0,
                     st, true, P);
 }
 
-// How a call runs: column tiles of 8 side by side, and pieces of the split
-// kernel (0: the prompt kernel) or the CTAs that share an item (z > 0).
+// How a call runs: by the prompt kernel, by z CTAs an item, or in pieces of the
+// line (-1: it has over 31 bits).
 struct Plan {
-  int nt, pieces, z;
+  bool prompt;
+  int z, pieces;
 };
 inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bool exact) {
   const long long G = H / Hkv;
-  if (D <= 128 && !exact && T * G >= 32LL * B) return {0, 0, 0};
-  const int nt = T * G > 8LL * B && D <= 128 && !exact ? 2 : 1;
-  // at most: a sequence of n rows has n G / (8 nt) column tiles, rounded up
-  const int NC = 8 * nt;
-  const long long items = std::min(T * G / NC + B, T * ((G + NC - 1) / NC)) * Hkv;
+  // at most: a sequence of n rows has n G / 8 column tiles, rounded up
+  const long long items = std::min(T * G / kCols + B, T * ((G + kCols - 1) / kCols)) * Hkv;
   const long long chunks = std::max(1LL, (cap + kChunk - 1) / kChunk);
-  if (items > 0x7FFFFFFFLL / chunks) return {0, -1, 0};  // the line has 31 bits
   const long long most =
-      std::min((long long)kMaxPieces, (long long)num_sms() * split_ctas(D, i8, nt));
+      std::min((long long)kMaxPieces, (long long)num_sms() * split_ctas(D, i8));
+  const long long even = (items * chunks + most - 1) / most;  // chunks a piece
+  // More than 8 columns a sequence: its keys are read once for each 8, or once
+  // for 128 by the prompt kernel, which takes some 14 us before it has to stream
+  // (8 KV heads, int8 of 128 unless stated, this against that, us: 4 x 12 rows
+  // over 1000 tokens 14 / 17, 16 rows 19 / 17; 4 x 8 rows of bf16 heads of 64
+  // over 4000 15 / 20, 24 rows 26 / 21; 16 x 6 rows over 2000 38 / 33; 1 x 64 over
+  // 32768 169 / 131). Two column tiles a warp in place of one were slower than
+  // both (4 x 12 rows 19, 16 x 6 rows 50).
+  if (D <= 128 && !exact && T * G > kCols * (long long)B && (items > num_sms() || even > 14))
+    return {true, 0, 0};
+  if (items > 0x7FFFFFFFLL / chunks) return {false, 0, -1};
   // Clusters where an item's equal shares are little longer than the balanced
   // pieces would be (should the sequences fill their pages): up to two chunks
   // cost less than the second launch. Past 8 chunks a share only without a
@@ -1072,30 +1024,26 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bo
   // merge (us, 8 int8 KV heads of 128, 2 query heads each): 1 x 512 7.8 -> 6.5,
   // 4 x 2048 13.4 -> 10.3, 32 x 2048 33.6 -> 30.4; shares four chunks longer, 8 x
   // 8192, 29.1 -> 31; more CTAs than the GPU holds at once, 4 x 700 of 16 rows
-  // in all, 11.2 -> 14.8. (Rows of up to 32 columns a sequence, in tiles of 16,
-  // keep the line.)
+  // in all, 11.2 -> 14.8.
   // (nor where most sequences are empty: each CTA looks through them)
-  if (nt == 1 && items <= most && B <= 4 * T) {
+  if (items <= most && B <= 4 * T) {
     // (one CTA an SM: clusters leave some of a GPC's SMs empty)
-    const long long room = split_ctas(D, i8, nt) == 1 ? most * 3 / 4 : most;
+    const long long room = split_ctas(D, i8) == 1 ? most * 3 / 4 : most;
     int z = 1;
     while (z < kMaxZ && z < chunks && items * 2 * z <= room) z *= 2;
     const long long share = (chunks + z - 1) / z;
-    if (share <= (items * chunks + most - 1) / most + kSlack && (z == 1 || share <= 8))
-      return {nt, 0, z};
+    if (share <= even + kSlack && (z == 1 || share <= 8)) return {false, z, 0};
   }
-  return {nt, (int)std::max(1LL, std::min(most, items * chunks)), 0};
+  return {false, 0, (int)std::max(1LL, std::min(most, items * chunks))};
 }
 
 template <int D, bool I8>
 cudaError_t launch(const Params& P, const Plan& p, bool exact, cudaStream_t st) {
   constexpr int E = I8 ? 2 : 3;  // terms of fp32 q and weights
-  if (exact) return launch_split<D, I8, 1, E, E>(P, p.z, st);
-  if constexpr (D <= 128) {
-    if (p.pieces == 0 && !p.z) return launch_prompt(P, D, I8, st);
-    if (p.nt == 2) return launch_split<D, I8, 2, 1, 1>(P, p.z, st);
-  }
-  return launch_split<D, I8, 1, 1, 1>(P, p.z, st);
+  if (p.prompt) return launch_prompt(P, D, I8, st);
+  if (exact)
+    return p.z ? launch_cluster<D, I8, E, E>(P, p.z, st) : launch_split<D, I8, E, E>(P, st);
+  return p.z ? launch_cluster<D, I8, 1, 1>(P, p.z, st) : launch_split<D, I8, 1, 1>(P, st);
 }
 
 // The largest number of pieces times columns any call of the head size uses.

@@ -20,6 +20,13 @@
 // order of the atomics, so results are the same each time, and a border is
 // where float64 puts it up to 2^-45 a candidate. fp32 weights would move
 // borders by 2^-24 of the total, more than a rare token's whole weight.
+//
+// What bounds it: one row, the chain of phases (151936 values over 16 CTAs, 46
+// thousand cycles: reading 6, weights and histogram 11, its sums through
+// distributed shared memory 7, border bins 5, collection 8, sort and search 6);
+// full batches, four shared-memory atomics and a float64 exp a value (32 rows
+// of 151936 over 128 CTAs, 52 us: 20 of them). 30 us a row, 160 rows of 2048
+// 12.9.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -960,11 +967,17 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
   }
 }
 
-// CTAs per row: as many as leave each a slice worth a CTA, and fit the GPU
-// for the whole batch; more where a slice would not fit shared memory.
+// CTAs per row: as many as leave each a slice worth a CTA (4096 values: with
+// 1024, 4 rows of 4000 took 16.7 us in place of 13.2) and fit the GPU at once
+// for the whole batch; more where a slice would not fit shared memory. Clusters
+// of 8 and 16 leave some of a GPC's SMs empty (rows of 151936: 6 with 16 CTAs
+// each 34 us, with 8 41, 8 with 16 51, with 8 41; 18 with 8 54, with 4 50).
 inline int cluster_for(int B, int V) {
   int c = 1;
-  while (c < kMaxCluster && V / (2 * c) >= 4096 && (long long)B * 2 * c <= num_sms()) c *= 2;
+  const auto fits = [&](int n) {
+    return (long long)B * n <= num_sms() * (n == 16 ? 6 : n == 8 ? 7 : 8) / 8;
+  };
+  while (c < kMaxCluster && V / (2 * c) >= 4096 && fits(2 * c)) c *= 2;
   while (c < kMaxCluster && (V + c - 1) / c > kResident) c *= 2;
   return c;
 }
@@ -1046,7 +1059,8 @@ extern "C" qg_status qg_sample_filtered(const float* logits, long long ld, int B
   for (int i = 0; i < sf::kSteps; ++i) P.pow2[i] = pow2.v[i];
   cudaStream_t st = (cudaStream_t)stream;
   // a slice of a few thousand values: fewer threads, whose barriers cost less
-  // and of which an SM takes two blocks
+  // and of which an SM takes two blocks (160 rows of 2048: 21.4 us with 512
+  // threads, 12.9 with 256)
   const cudaError_t e = P.slice > 4096 ? sf::launch<512>(P, C, B, st) : sf::launch<256>(P, C, B, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
