@@ -427,3 +427,68 @@ def test_a_cluster_with_idle_blocks_and_empty_sequences(kind):
         rows = slice(r0[b], r0[b + 1])
         want, tol = reference(q[rows], k, v, H, Hkv, D, 1 / math.sqrt(D), kind, False, True)
         assert np.all(np.abs(got[rows] - want) <= tol)
+
+
+# Room for far more tokens than there are: the tcgen05 kernel, eight blocks a
+# tile, whatever the number of rows.
+ROOM = 20000
+
+
+@pytest.mark.parametrize("case", [
+    ("int8", 128, 64, 4, 2, [40, 0, 33], [2100, 0, 35]),
+    ("int8", 64, 16, 16, 1, [9, 200], [2053, 200]),
+    ("int8", 128, 16, 12, 4, [1, 14, 30], [1, 300, 64]),
+    ("bf16", 128, 32, 16, 16, [65], [1100]),
+    ("bf16", 64, 16, 6, 2, [50, 1], [2113, 700]),
+    ("bf16", 128, 128, 16, 1, [70, 5, 2], [1000, 5, 900]),
+    ("int8", 128, 64, 16, 8, [5] * 40, [5 + 31 * i for i in range(40)]),
+], ids=lambda c: f"{c[0]}-d{c[1]}-h{c[3]}.{c[4]}-n{c[5][:3]}-l{c[6][:3]}")
+def test_prompt_rows_with_room_for_many_tokens(case):
+    kind, D, page, H, Hkv, n, lens = case
+    check(kind, D, page, H, Hkv, n, lens, BF, BF, 1010,
+          cap=ROOM if len(n) < 10 else 6000, pad=5)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("q_scale", [1e-3, 30.0])
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_flat_and_peaked_scores_of_prompt_rows(kind, q_scale, room):
+    check(kind, 128, 64, 16, 4, [150], [1200], BF, BF, 1020, q_scale=q_scale, cap=room or 1200)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_prompt_rows_over_blocks_of_very_different_scales(kind, room):
+    D, Hkv, L, n = 128, 2, 640, 300
+    cache = Cache(kind, 1, Hkv, D, 64, room or L, [L], 1030)
+    if kind == "int8":
+        rng = np.random.default_rng(2)
+        cache.vs *= (2.0 ** rng.integers(-30, 10, cache.vs.shape)).astype(np.float32)
+        cache.vs[cache.table[0, 3], 0, 1] = 0.0
+        cache.ks *= (2.0 ** rng.integers(-6, 2, cache.ks.shape)).astype(np.float32)
+        cache.ks[cache.table[0, 5], 1, 2] *= -1.0
+    got, q = run(cache, [n], [L], 8, BF, BF, 1031)
+    k, v = cache.values(0, L)
+    want, tol = reference(q, k, v, 8, Hkv, D, 1 / math.sqrt(D), kind, False, True)
+    assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_bad_pages_and_lengths_among_prompt_rows(kind):
+    """Rows that see a page outside the pool are NaN, a wrong length gives
+    zero rows, the others are untouched."""
+    n, lens = [33, 20, 70, 9], [130, 20, 90, 40]
+    cache = Cache(kind, 4, 2, 128, 64, ROOM, lens, 1040)
+    good = cache.table.copy()
+    cache.table[0, 2] = cache.k.shape[0]        # tokens 128 and 129: the last two rows
+    cache.table[2, 2] = -1                      # past its length: never read
+    got, q = run(cache, n, [130, 20, 90, 5], 8, BF, BF, 1041)
+    cache.table = good
+    r0 = starts(n)
+    assert np.isnan(got[31:33]).all() and np.all(got[r0[3]:] == 0.0)
+    for b, rows in ((0, slice(0, 31)), (1, slice(33, 53)), (2, slice(53, 123))):
+        k, v = cache.values(b, lens[b])
+        want, tol = reference(q[r0[b]:r0[b + 1]], k, v, 8, 2, 128, 1 / math.sqrt(128), kind, False,
+                              True)
+        m = rows.stop - rows.start
+        assert np.all(np.abs(got[rows] - want[:m]) <= tol[:m])

@@ -73,7 +73,8 @@ def test_a_prompt_before_products_on_tensor_memory(T, N):
     D, H, Hkv, B = 128, 16, 8, 2
     K = H * D
     kv, g = _pool(Hkv, D, 4096, seed=1)
-    table = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32)
+    # (room for many more tokens, so that the few rows take that kernel too)
+    table = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32).repeat(1, 13)
     n = [T - 7, 7]
     rs, lens = dev(starts(n)), dev(np.array([2000, 900], np.int32))
     w, s, b = (dev(a) for a in qg_synth.affine8_packed(N, K, 7))
