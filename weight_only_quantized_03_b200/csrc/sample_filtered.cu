@@ -967,8 +967,9 @@ __global__ void __launch_bounds__(NTHR, 512 / NTHR) sample_kernel(const __grid_c
   }
 }
 
-// CTAs per row: as many as leave each a slice worth a CTA (4096 values: with
-// 1024, 4 rows of 4000 took 16.7 us in place of 13.2) and fit the GPU at once
+// CTAs per row: as many as leave each a slice worth a CTA (2048 values: with
+// 4096, 16 rows of 16000 took 23.5 us in place of 20.9; with 1024, 4 rows of 4000
+// 16.7 in place of 13.1) and fit the GPU at once
 // for the whole batch; more where a slice would not fit shared memory. Clusters
 // of 8 and 16 leave some of a GPC's SMs empty (rows of 151936: 6 with 16 CTAs
 // each 34 us, with 8 41, 8 with 16 51, with 8 41; 18 with 8 54, with 4 50).
@@ -977,7 +978,7 @@ inline int cluster_for(int B, int V) {
   const auto fits = [&](int n) {
     return (long long)B * n <= num_sms() * (n == 16 ? 6 : n == 8 ? 7 : 8) / 8;
   };
-  while (c < kMaxCluster && V / (2 * c) >= 4096 && fits(2 * c)) c *= 2;
+  while (c < kMaxCluster && V / (2 * c) >= 2048 && fits(2 * c)) c *= 2;
   while (c < kMaxCluster && (V + c - 1) / c > kResident) c *= 2;
   return c;
 }
@@ -1058,10 +1059,12 @@ extern "C" qg_status qg_sample_filtered(const float* logits, long long ld, int B
   while (((unsigned long long)V << P.frac) > (1ull << 62)) --P.frac;
   for (int i = 0; i < sf::kSteps; ++i) P.pow2[i] = pow2.v[i];
   cudaStream_t st = (cudaStream_t)stream;
-  // a slice of a few thousand values: fewer threads, whose barriers cost less
-  // and of which an SM takes two blocks (160 rows of 2048: 21.4 us with 512
-  // threads, 12.9 with 256)
-  const cudaError_t e = P.slice > 4096 ? sf::launch<512>(P, C, B, st) : sf::launch<256>(P, C, B, st);
+  // Short slices, and more CTAs than SMs: fewer threads, whose barriers cost less
+  // and of which an SM takes two blocks (512 and 256 threads, us: 160 rows of 2048
+  // 21.4, 12.9; 250 rows of 6000 32.1, 26.2; one CTA an SM, 64 rows of 8000, 20.0,
+  // 22.9).
+  const bool few = P.slice <= 4096 || (P.slice <= 8192 && (long long)B * C > num_sms());
+  const cudaError_t e = few ? sf::launch<256>(P, C, B, st) : sf::launch<512>(P, C, B, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     set_error("%s: CUDA launch failed: %s", who, cudaGetErrorString(e));
