@@ -190,3 +190,14 @@ def test_batches_beyond_one_wave_and_same_bits_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(out.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B,V", [(170, 6000), (149, 8192), (8, 151936), (2, 8190), (300, 4095)])
+def test_batches_and_slices_at_the_ends_of_the_rules(B, V):
+    """Two blocks an SM, clusters of 8 in place of 16, slices of 2047 values;
+    random rows, and rows of a few distinct values."""
+    rng = np.random.default_rng(V + 7 * B)
+    l = (rng.standard_normal((B, V)) * 2).astype(np.float32)
+    if V < 50000:
+        l[::3] = np.round(l[::3] * 2) / 2
+    check(l, **params(rng, B, V))
