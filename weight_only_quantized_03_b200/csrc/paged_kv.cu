@@ -16,8 +16,8 @@
 //
 // What bounds it: a few rows, the chain launch, lengths, table, rows, stores
 // (32 sequences of one token, 16 + 2 x 8 heads of 128, with the read-back 6.3
-// us); prompts, latency at 64 registers a thread, a lane's 8 rows in turn: a
-// scheduler issues every other cycle (4099 int8 rows 22 us, 59 MB, 2.7 TB/s).
+// us); prompts, latency and issue, a lane's 8 rows in turn (16000 int8 rows of
+// 8 users 88 us with the read-back, 3.7 TB/s).
 //
 // The mapping of CTAs to (sequence, block) needs no host knowledge of the
 // lengths: n rows touch at most n/16 + 2 blocks, so slot ranges
@@ -379,8 +379,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, const NewRows
                          1 + (warp >> 1), lane);
   };
   // the next item's rows are under way while this one's are put away, where
-  // registers hold both (fp32 rows of 128 spilled)
-  constexpr bool kAhead = NR == 1;
+  // registers hold both
+  constexpr bool kAhead = NR == 1 || !XF32;
   for (; it < items; it += gridDim.y * step) {
     const bool isk = it < P.Hkv, isv = !isk && it < 2 * P.Hkv;
     const int h = isk ? it : isv ? it - P.Hkv : it - 2 * P.Hkv;
@@ -402,8 +402,14 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, const NewRows
   }
 }
 
+// CTAs an SM: bf16 rows of 128 take 80 registers with the next item's rows
+// ahead (us with three CTAs so, three without, four: 16000 int8 rows of 8 users
+// 88, 94, 107; 600 rows 11.3, 11.5, 12.6); fp32 rows are faster as four at 64
+// (4099 rows 37.6 against 41.2).
+constexpr int append_ctas(int D, bool xf32) { return D > 128 ? 2 : xf32 ? 4 : 3; }
+
 template <int D, bool I8, bool XF32>
-__global__ void __launch_bounds__(kWarps * 32, D <= 128 ? 4 : 2)
+__global__ void __launch_bounds__(kWarps * 32, append_ctas(D, XF32))
 append_kernel(const __grid_constant__ AppendParams P) {
   __shared__ __align__(16) float cs[kBlock * D / 2];
   __shared__ __align__(16) float sn[kBlock * D / 2];
