@@ -62,6 +62,7 @@ constexpr int kWarps = 8;            // of the cluster and split kernels
 constexpr int kCols = 8;             // (row, head) columns of a tile
 constexpr int kChunk = kWarps * kBlock;
 constexpr int kMergeThreads = 512;
+constexpr int kItem = 2;             // chunks' worth of an item's other work (see SeqWork)
 constexpr int kSlack = 2;            // chunks (see plan)
 constexpr int kMaxPieces = 320;      // of the split kernel (two CTAs on each of 148 SMs)
 
@@ -509,11 +510,13 @@ __device__ __forceinline__ void set_limits(const Params& P, const Item& it, W& w
   w.min_lim = min(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
 }
 
-__device__ __forceinline__ void store_out(const Params& P, const Item& it, int c, int d, int D,
-                                          float x) {
+// Where column c of the item goes: its (row, query head) in out.
+__device__ __forceinline__ int out_row(const Params& P, const Item& it, int c) {
   const int i = c / P.G;
-  if (i >= it.n) return;
-  const long long at = ((long long)(it.r0 + i) * P.H + it.h * P.G + c % P.G) * D + d;
+  return (it.r0 + i) * P.H + it.h * P.G + (c - i * P.G);  // (below 2^30)
+}
+__device__ __forceinline__ void store_out(const Params& P, int row, int d, int D, float x) {
+  const long long at = (long long)row * D + d;
   if (P.out_bf16)
     reinterpret_cast<uint16_t*>(P.out)[at] = f32_to_bf16_bits(x);
   else
@@ -564,21 +567,30 @@ __device__ __forceinline__ void join_warps(const float* so, const float* sm, con
 
 // ------------------------------------------------------------ split kernel --
 
-// A sequence's column tiles and the chunks of each of its items (at least
-// one, so that empty ones are written). The host keeps a call's chunks below
-// 2^31.
+// A sequence's column tiles, the chunks of each of its items (at least one, so
+// that empty ones are written), and an item's length on the line: its chunks
+// behind kItem units for what it costs besides (q, the warps' join, the store):
+// without them pieces of many short items took several times as long as the
+// others (600 fp32 rows of 5 users over up to 2000 int8 tokens 164 us, with one
+// unit 107, two 91, four 96). The host keeps a call's units below 2^31.
 struct SeqWork {
   int tiles, chunks;
   __device__ __forceinline__ SeqWork(const Params& P, const Item& it) {
     tiles = (it.n * P.G + kCols - 1) / kCols;
     chunks = max(1, (it.len + kChunk - 1) / kChunk);
   }
+  __device__ __forceinline__ int units() const { return chunks + kItem; }
   __device__ __forceinline__ unsigned total(int Hkv) const {
-    return (unsigned)tiles * Hkv * chunks;
+    return (unsigned)tiles * Hkv * units();
   }
 };
+// Blocks of 16 tokens that the item's last column sees.
+__device__ __forceinline__ int seen_blocks(const Params& P, const Item& it) {
+  const int rows = min(it.n, ((it.ct + 1) * kCols - 1) / P.G + 1);
+  return (max(0, it.len - it.n + rows) + kBlock - 1) / kBlock;
+}
 
-// The line of N chunks cut into pieces: the first `rem` have q + 1 chunks,
+// The line of N units cut into pieces: the first `rem` have q + 1 units,
 // the others q.
 struct Cut {
   unsigned q, rem;
@@ -632,6 +644,7 @@ split_kernel(const __grid_constant__ Params P) {
   float* sl = sm + kWarps * kCols;                          // [kWarps][kCols]
   uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * kCols);  // fragments of q
   __shared__ float sf[kCols];
+  __shared__ int rows[2][kCols];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();  // the merge may find its items meanwhile
@@ -675,8 +688,8 @@ split_kernel(const __grid_constant__ Params P) {
   }
   SeqWork w(P, it);
   // (head, column tile) of the sequence, and the item's first chunk here
-  int unit = (int)(rest / (unsigned)w.chunks);
-  int c0 = (int)rest - unit * w.chunks;
+  int unit = (int)(rest / (unsigned)w.units());
+  int c0 = (int)rest - unit * w.units();
   it.h = unit / w.tiles;
   it.ct = unit - it.h * w.tiles;
 
@@ -687,12 +700,15 @@ split_kernel(const __grid_constant__ Params P) {
   const auto start = [&](const Item& i, int first, int last) {  // chunks [first, last)
     qs.take(P, i, warp, lane);
     walk.len = i.len;
-    walk.begin(i, first * kWarps + warp, kWarps, min(last * kWarps, (i.len + kBlock - 1) / kBlock));
+    walk.begin(i, first * kWarps + warp, kWarps, min(last * kWarps, seen_blocks(P, i)));
   };
-  int c1 = (int)min((unsigned)w.chunks, c0 + (stop - pos));
-  start(it, c0, c1);
+  int c1 = (int)min((unsigned)w.units(), c0 + (stop - pos));
+  start(it, max(0, c0 - kItem), max(0, c1 - kItem));
+  int turn = 0;
   for (;;) {
     qs.put(P, sq, sf, warp, lane);
+    turn ^= 1;  // (slower warps may still store the item before)
+    if (tid < kCols) rows[turn][tid] = out_row(P, it, it.ct * kCols + tid);
     set_limits(P, it, walk);
     __syncthreads();
     walk.qf[0] = sf[2 * walk.t];
@@ -701,7 +717,7 @@ split_kernel(const __grid_constant__ Params P) {
     walk.run(S, it);
     // the next item's first keys and q go out before this one is put away
     const Item cur = it;
-    const bool first_part = c0 == 0, whole = c0 == 0 && c1 == w.chunks;
+    const bool first_part = c0 == 0, whole = c0 == 0 && c1 == w.units();
     pos += c1 - c0;
     const bool more = pos < stop;
     if (more) {
@@ -716,8 +732,8 @@ split_kernel(const __grid_constant__ Params P) {
       it.h = unit / w.tiles;
       it.ct = unit - it.h * w.tiles;
       c0 = 0;
-      c1 = (int)min((unsigned)w.chunks, stop - pos);
-      start(it, c0, c1);
+      c1 = (int)min((unsigned)w.units(), stop - pos);
+      start(it, 0, max(0, c1 - kItem));
     }
     const int cols = min(kCols, cur.n * P.G - cur.ct * kCols);  // of the tile, real ones
     put_state<D, I8>(S, so, sm, sl, cols, warp, lane);
@@ -728,7 +744,7 @@ split_kernel(const __grid_constant__ Params P) {
       float M, L, O;
       join_warps<D>(so, sm, sl, n, d, M, L, O);
       if (whole) {
-        store_out(P, cur, cur.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
+        store_out(P, rows[turn][n], d, D, L != 0.f ? O / L : 0.f);
       } else {
         part[2 * kCols + i] = O;
         if (d == 0) {
@@ -773,6 +789,7 @@ cluster_kernel(const __grid_constant__ Params P) {
   float* sl = sm + kWarps * kCols;                          // [kWarps][kCols]
   uint16_t* sq = reinterpret_cast<uint16_t*>(sl + kWarps * kCols);  // fragments of q
   __shared__ float sf[kCols];
+  __shared__ int rows[kCols];
   __shared__ float pm[kCols], pl[kCols], po[kCols * D];           // the CTA's result
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Z = P.pieces, z = blockIdx.x % Z, u = blockIdx.x / Z;
@@ -808,8 +825,9 @@ cluster_kernel(const __grid_constant__ Params P) {
   const int c0 = (int)((long long)w.chunks * z / Z), c1 = (int)((long long)w.chunks * (z + 1) / Z);
   qs.take(P, it, warp, lane);
   walk.len = it.len;
-  walk.begin(it, c0 * kWarps + warp, kWarps, min(c1 * kWarps, (it.len + kBlock - 1) / kBlock));
+  walk.begin(it, c0 * kWarps + warp, kWarps, min(c1 * kWarps, seen_blocks(P, it)));
   qs.put(P, sq, sf, warp, lane);
+  if (tid < kCols) rows[tid] = out_row(P, it, it.ct * kCols + tid);
   set_limits(P, it, walk);
   __syncthreads();
   walk.qf[0] = sf[2 * walk.t];
@@ -824,7 +842,7 @@ cluster_kernel(const __grid_constant__ Params P) {
     float M, L, O;
     join_warps<D>(so, sm, sl, n, d, M, L, O);
     if (Z == 1) {
-      store_out(P, it, it.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
+      store_out(P, rows[n], d, D, L != 0.f ? O / L : 0.f);
     } else {
       po[i] = O;
       if (d == 0) {
@@ -855,7 +873,7 @@ cluster_kernel(const __grid_constant__ Params P) {
       L = fmaf(a, l[k], L);
       O = fmaf(a, o[k], O);
     }
-    store_out(P, it, it.ct * kCols + n, d, D, L != 0.f ? O / L : 0.f);
+    store_out(P, rows[n], d, D, L != 0.f ? O / L : 0.f);
   }
   cluster_sync();  // nobody ends while its shared memory is read
 }
@@ -900,12 +918,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     pdl_wait();
     return;
   }
-  const unsigned begin = before + (unsigned)(it.h * w.tiles + it.ct) * w.chunks;
+  const unsigned begin = before + (unsigned)(it.h * w.tiles + it.ct) * w.units();
   const Cut cut(N, P.pieces);
   // (within the workspace even if row starts decrease)
   const int last = P.pieces - 1;
   const int p0 = (int)min(cut.piece_of(begin), (unsigned)last);
-  const int p1 = (int)min(cut.piece_of(begin + w.chunks - 1), (unsigned)last);
+  const int p1 = (int)min(cut.piece_of(begin + w.units() - 1), (unsigned)last);
   pdl_wait();
   if (p0 >= p1) return;  // written by its piece
   const int np = p1 - p0 + 1, cols = min(kCols, it.n * P.G - it.ct * kCols);
@@ -947,7 +965,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       if (grp == 0)
         for (int g = 1; g < groups; ++g) O += acc[g * width + i];
     }
-    if (grp == 0) store_out(P, it, it.ct * kCols + n, d, D, O);
+    if (grp == 0) store_out(P, out_row(P, it, it.ct * kCols + n), d, D, O);
   }
 }
 
@@ -1016,7 +1034,7 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bo
   // both (4 x 12 rows 19, 16 x 6 rows 50).
   if (D <= 128 && !exact && T * G > kCols * (long long)B && (items > num_sms() || even > 14))
     return {true, 0, 0};
-  if (items > 0x7FFFFFFFLL / chunks) return {false, 0, -1};
+  if (items > 0x7FFFFFFFLL / (chunks + kItem)) return {false, 0, -1};
   // Clusters where an item's equal shares are little longer than the balanced
   // pieces would be (should the sequences fill their pages): up to two chunks
   // cost less than the second launch. Past 8 chunks a share only without a
