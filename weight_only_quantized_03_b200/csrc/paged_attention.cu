@@ -1026,13 +1026,15 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bo
       std::min((long long)kMaxPieces, (long long)num_sms() * split_ctas(D, i8));
   const long long even = (items * chunks + most - 1) / most;  // chunks a piece
   // More than 8 columns a sequence: its keys are read once for each 8, or once
-  // for 128 by the prompt kernel, which takes some 14 us before it has to stream
-  // (8 KV heads, int8 of 128 unless stated, this against that, us: 4 x 12 rows
-  // over 1000 tokens 14 / 17, 16 rows 19 / 17; 4 x 8 rows of bf16 heads of 64
-  // over 4000 15 / 20, 24 rows 26 / 21; 16 x 6 rows over 2000 38 / 33; 1 x 64 over
-  // 32768 169 / 131). Two column tiles a warp in place of one were slower than
-  // both (4 x 12 rows 19, 16 x 6 rows 50).
-  if (D <= 128 && !exact && T * G > kCols * (long long)B && (items > num_sms() || even > 14))
+  // for 128 by the prompt kernel, which takes some 14 us before it has to stream.
+  // The first where a piece has few chunks, and few items or long ones (8 KV
+  // heads, int8 of 128 unless stated, this against that, us: 4 x 12 rows over 1000
+  // tokens 14 / 17, 1 x 100 over 700 15 / 19, 16 x 6 over 2000 26 / 33, 12 rows each
+  // 36 / 34; 4 x 12 rows of bf16 over 3000 19 / 30; 1 x 64 over 32768 179 / 135; 1 x
+  // 300 over 300 27 / 15, 30 x 6 over 300 26 / 19). Two column tiles a warp in
+  // place of one were slower than both (4 x 12 rows 19, 16 x 6 rows 50).
+  if (D <= 128 && !exact && T * G > kCols * (long long)B &&
+      !(even <= 21 && (items <= num_sms() || chunks >= 6)))
     return {true, 0, 0};
   if (items > 0x7FFFFFFFLL / (chunks + kItem)) return {false, 0, -1};
   // Clusters where an item's equal shares are little longer than the balanced
