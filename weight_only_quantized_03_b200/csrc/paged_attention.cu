@@ -690,6 +690,12 @@ split_kernel(const __grid_constant__ Params P) {
   // (head, column tile) of the sequence, and the item's first chunk here
   int unit = (int)(rest / (unsigned)w.units());
   int c0 = (int)rest - unit * w.units();
+  int left = c0 + (int)(stop - pos);  // units from the item's beginning to the piece's end
+  // A cut before an item's first chunk moves to the item's beginning.
+  if (c0 <= kItem) {
+    c0 = 0;
+    if (left <= kItem) return;
+  }
   it.h = unit / w.tiles;
   it.ct = unit - it.h * w.tiles;
 
@@ -702,7 +708,7 @@ split_kernel(const __grid_constant__ Params P) {
     walk.len = i.len;
     walk.begin(i, first * kWarps + warp, kWarps, min(last * kWarps, seen_blocks(P, i)));
   };
-  int c1 = (int)min((unsigned)w.units(), c0 + (stop - pos));
+  int c1 = min(w.units(), left);
   start(it, max(0, c0 - kItem), max(0, c1 - kItem));
   int turn = 0;
   for (;;) {
@@ -718,8 +724,8 @@ split_kernel(const __grid_constant__ Params P) {
     // the next item's first keys and q go out before this one is put away
     const Item cur = it;
     const bool first_part = c0 == 0, whole = c0 == 0 && c1 == w.units();
-    pos += c1 - c0;
-    const bool more = pos < stop;
+    left -= w.units();
+    const bool more = left > kItem;
     if (more) {
       if (++unit == w.tiles * P.Hkv) {
         unit = 0;
@@ -732,7 +738,7 @@ split_kernel(const __grid_constant__ Params P) {
       it.h = unit / w.tiles;
       it.ct = unit - it.h * w.tiles;
       c0 = 0;
-      c1 = (int)min((unsigned)w.units(), stop - pos);
+      c1 = min(w.units(), left);
       start(it, 0, max(0, c1 - kItem));
     }
     const int cols = min(kCols, cur.n * P.G - cur.ct * kCols);  // of the tile, real ones
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const Cut cut(N, P.pieces);
   // (within the workspace even if row starts decrease)
   const int last = P.pieces - 1;
-  const int p0 = (int)min(cut.piece_of(begin), (unsigned)last);
+  const int p0 = (int)min(cut.piece_of(begin + kItem), (unsigned)last);
   const int p1 = (int)min(cut.piece_of(begin + w.units() - 1), (unsigned)last);
   pdl_wait();
   if (p0 >= p1) return;  // written by its piece
