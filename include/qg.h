@@ -464,7 +464,8 @@ qg_status qg_sample(const float* logits, int B, int V, const int32_t* past, int 
  * row_start NULL means one row each (T = B). Rows outside every sequence (a
  * padded batch) are neither read nor written. Row starts and lengths are
  * read on the device; row starts must not decrease and are clamped to
- * [0, T].
+ * [0, T] (where they do decrease, rows may come out wrong or stay as they
+ * were; nothing outside the T rows is touched).
  * ---------------------------------------------------------------------- */
 #define QG_KV_BLOCK 16
 typedef enum qg_kv_dtype { QG_KV_BF16 = 0, QG_KV_INT8 = 1 } qg_kv_dtype;

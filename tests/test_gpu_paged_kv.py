@@ -348,3 +348,42 @@ def test_append_of_prompts_in_place_and_apart_are_the_same(kind):
                             if t is not None])
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert got[0][0].abs().max() > 0 and got[0][1].float().abs().max() > 0
+
+
+def _matching_sequences(rs, T):
+    """Sequences whose range of block slots holds a slot, by the rule of
+    csrc/paged_kv.cu: {slot: [(first row, rows), ...]} where it is several."""
+    c = [min(max(r, 0), T) for r in rs]
+    out = {}
+    for u in range(T // BLOCK + 2 * (len(rs) - 1)):
+        m = [(c[i], c[i + 1] - c[i]) for i in range(len(rs) - 1)
+             if c[i] // BLOCK + 2 * i <= u < c[i + 1] // BLOCK + 2 * (i + 1)]
+        if len(m) > 1:
+            out[u] = m
+    return out
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_append_with_row_starts_that_decrease_stays_within_its_rows(kind):
+    """Slots that two sequences claim: a mix of one's first row and the
+    other's rows would reach past the call's rows."""
+    T, rs = 200, [0, 200, 50, 60, 190, 200]
+    claims = _matching_sequences(rs, T)
+    assert max(r + n for m in claims.values() for r, _ in m for _, n in m) > T
+    D, Hkv, H, page, B = 64, 2, 2, 32, 5
+    cache = Cache(kind, B, Hkv, D, page, 256, [0] * B, 500)
+    kv, table = cache.upload(qg)
+    x = torch.randn((2 * T, (H + 2 * Hkv) * D), device="cuda")
+    q, k, v = (a[:T] for a in x.split((H * D, Hkv * D, Hkv * D), 1))
+    out = torch.full((2 * T, H * D), 77.0, device="cuda")
+    lens = dev(np.array([200, 10, 10, 130, 10], np.int32))
+    qg.qg_paged_kv_append(kv, table, lens, k, v, row_start=dev(np.array(rs, np.int32)), q=q,
+                          q_out=out[:T])
+    torch.cuda.synchronize()
+    assert bool((out[T:] == 77.0).all())
+    assert not bool(torch.isnan(out).any())
+    # the pages of nobody (two spare ones) are as they were
+    spare = np.setdiff1d(np.arange(cache.k.shape[0]), cache.table)
+    got = cache.download(kv)
+    np.testing.assert_array_equal(got[0][spare], cache.k[spare])
+    np.testing.assert_array_equal(got[2][spare], cache.v[spare])

@@ -435,7 +435,9 @@ append_kernel(const __grid_constant__ AppendParams P) {
         s_len = cached;
       }
     }
-    if (!__syncthreads_or(found)) return;
+    // (two threads with a sequence: row starts that decrease, and what they
+    // stored is a mix of both; the block is dropped)
+    if (__syncthreads_count(found) != 1) return;
     b = s_b;
     r0 = s_r0;
     n = s_n;
