@@ -201,3 +201,29 @@ def test_batches_and_slices_at_the_ends_of_the_rules(B, V):
     if V < 50000:
         l[::3] = np.round(l[::3] * 2) / 2
     check(l, **params(rng, B, V))
+
+
+@pytest.mark.parametrize("B,V", [(3, 151936), (148, 5000), (300, 3000)])
+def test_collections_of_many_calls_side_by_side(B, V):
+    """Rows whose members come from every CTA of a cluster and every warp of a
+    CTA, on two streams at once, many times: the same tokens each time. (A
+    CTA's count of members and their place in the list are words of their own:
+    threads read the first while the other is set.)"""
+    rng = np.random.default_rng(B + V)
+    l = (rng.standard_normal((B, V)) * 2).astype(np.float32)
+    p = dict(u=rng.random(B).astype(np.float32), top_k=rng.integers(20, 200, B),
+             top_p=np.full(B, 0.95), temperature=np.full(B, 1.1))
+    want, kept = check(l, **p)
+    ld = dev(l)
+    args = {k: dev(np.asarray(v, np.int32 if k == "top_k" else np.float32)) for k, v in p.items()}
+    u = args.pop("u")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = torch.full((2, 40, 2, B), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(40):
+        for s, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                qg.qg_sample_filtered(ld, u, outs[s, i, 0], kept=outs[s, i, 1], **args)
+    torch.cuda.synchronize()
+    got = outs.cpu().numpy()
+    assert np.all(got[:, :, 0] == want) and np.all(got[:, :, 1] == kept)

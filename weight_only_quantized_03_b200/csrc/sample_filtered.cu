@@ -87,7 +87,7 @@ struct Shared {
   unsigned red3[32];
   double pow2[kSteps];
   u64 mine[kList];                       // this CTA's members of a collection
-  unsigned mine_n;
+  unsigned mine_n, mine_at;              // how many, and where they go in rank 0's list
   int path;                              // rank 0: how the row goes on
   u64 list_key[kList], list_w[kList];    // rank 0's list: sorted keys, running weights
   // rank 0: the cluster's counts and weights by bin, and what lies before
@@ -386,9 +386,9 @@ struct Work {
       });
       __syncthreads();
       const unsigned m = S.mine_n;
-      if (tid == 0) S.mine_n = add_u32(remote(&S.list_n, 0), m);
+      if (tid == 0) S.mine_at = add_u32(remote(&S.list_n, 0), m);
       __syncthreads();
-      const unsigned at = S.mine_n + tid;
+      const unsigned at = S.mine_at + tid;
       if (tid < (int)min(m, (unsigned)NTHR) && at < NTHR)
         st_u64(remote(&S.list_key[at], 0), S.mine[tid]);
     } else if (c.op == kMinMax) {  // of the bin's keys
