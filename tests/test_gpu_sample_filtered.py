@@ -227,3 +227,23 @@ def test_collections_of_many_calls_side_by_side(B, V):
     torch.cuda.synchronize()
     got = outs.cpu().numpy()
     assert np.all(got[:, :, 0] == want) and np.all(got[:, :, 1] == kept)
+
+
+@pytest.mark.parametrize("V", [1 << 22, (1 << 21) + 12345, (1 << 20) + 17])
+def test_crowded_rows_of_the_largest_vocabularies(V):
+    """A slice of more than 65536 values in one bin, whose weights' lower
+    pieces add up past 32 bits: one larger logit and the rest equal (a floor,
+    or a finite mask within reach), and a few crowded values. The weights are
+    no round numbers; each is rounded to 2^-40 of the largest, 2^-41 / 1e-4 of
+    the smallest one here, which moves a border by at most 0.02 candidates."""
+    B = 4
+    l = np.zeros((B, V), np.float32)
+    l[0, 17] = 6.5
+    l[1, V // 2:] = -0.375
+    l[1, V - 3] = 9.25
+    l[2] = -3.0 + np.random.default_rng(V).integers(0, 3, V) * 2.0 ** -12
+    l[2, 5] = 4.5
+    l[3, V // 3] = 6.5
+    u = np.array([0.9, 0.7, 0.4, 0.9], np.float32)
+    check(l, u)
+    check(l, u, top_p=[0.9, 0.65, 0.97, 1.0], top_k=[0, 0, 0, V - 5], min_p=[0, 0, 0, 1e-3])

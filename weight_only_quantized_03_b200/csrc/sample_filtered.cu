@@ -42,6 +42,7 @@ constexpr int kFine = 1536;         // bins for the values whose weight is not 0
 constexpr int kList = 512;          // members that rank 0 can hold at most (one a thread)
 constexpr int kMaxCluster = 16;
 constexpr int kResident = 37984;    // values of a slice that shared memory holds
+constexpr int kSumRoom = 65536;     // 16-bit pieces whose sum 32 bits hold
 constexpr int kSteps = 64;          // entries of the table of 2^(i / kSteps)
 
 typedef unsigned long long u64;
@@ -94,9 +95,10 @@ struct Shared {
   // each group of 32 bins (the whole at the end)
   u64 tot_w[kBins], sup_w[kBins / 32 + 1];
   unsigned tot_c[kBins], sup_c[kBins / 32 + 1];
-  // this CTA's histogram: counts, and weights in three pieces of 16 bits, whose
-  // sums over a slice fit 32 bits: atomics that return nothing (a 64-bit one
-  // costs several, and two halves would need the carry back)
+  // this CTA's histogram: counts, and weights in pieces of 16, 16 and 12 bits,
+  // whose sums over kSumRoom values fit 32 bits (see each_adding): atomics that
+  // return nothing (a 64-bit one costs several, and two halves would need the
+  // carry back)
   unsigned hist_c[kBins], hist_w0[kBins], hist_w1[kBins], hist_w2[kBins];
 };
 // Inside one bin (rank 0, rare): lies over the list.
@@ -260,19 +262,46 @@ struct Work {
   int begin, n;
   unsigned rank, C;
 
-  // f(four values, index of the first) for the slice, the indexes NTHR apart;
-  // -inf past its end. Four at once, so that f can form what it needs of all
-  // of them before it branches: their chains hide each other's latency.
+  // f(four values, index of the first) for places first .. last - 1 of the
+  // slice, the indexes NTHR apart; -inf past them. Four at once, so that f can
+  // form what it needs of all of them before it branches: their chains hide each
+  // other's latency.
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each(F f, int first, int last) const {
     const float* const from = P.resident ? data : row + begin;
-    const int len = n, first = begin;  // (in registers, whatever f does to memory)
+    const int at = begin;  // (in registers, whatever f does to memory)
 #pragma unroll 1
-    for (int i = threadIdx.x; i < len; i += 4 * NTHR) {
+    for (int i = first + threadIdx.x; i < last; i += 4 * NTHR) {
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = i + e * NTHR < len ? from[i + e * NTHR] : -INFINITY;
-      f(v, first + i);
+      for (int e = 0; e < 4; ++e) v[e] = i + e * NTHR < last ? from[i + e * NTHR] : -INFINITY;
+      f(v, at + i);
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    each(f, 0, n);
+  }
+
+  // The whole slice for an f that adds weights to the histogram. A piece's sum
+  // holds 65536 members of one bin; a slice of more (V past 2^20) goes in parts
+  // of half as many, after each of which the sums' upper halves move up.
+  template <class F>
+  __device__ __forceinline__ void each_adding(F f) const {
+    const int part = n <= kSumRoom ? kSumRoom : kSumRoom / 2;
+#pragma unroll 1
+    for (int at = 0; at < n; at += part) {
+      each(f, at, min(n, at + part));
+      if (n > part) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += NTHR) {
+          const unsigned lo = S.hist_w0[i], mid = S.hist_w1[i] + (lo >> 16);
+          S.hist_w0[i] = lo & 0xFFFFu;
+          S.hist_w1[i] = mid & 0xFFFFu;
+          S.hist_w2[i] += mid >> 16;
+        }
+        __syncthreads();
+      }
     }
   }
 
@@ -335,7 +364,7 @@ struct Work {
   // The slice's weights (and, with `count`, counts) into the histogram.
   __device__ __forceinline__ void weigh(const Row& R, double min_p, bool count) const {
     unsigned above = 0;
-    each([&](const float (&v)[4], int) {
+    each_adding([&](const float (&v)[4], int) {
       int b[4];
       u64 w[4];
       double y[4];
@@ -427,7 +456,7 @@ struct Work {
         S.hist_w0[i] = S.hist_w1[i] = S.hist_w2[i] = 0;
       }
       __syncthreads();
-      each([&](const float (&v)[4], int i) {
+      each_adding([&](const float (&v)[4], int i) {
 #pragma unroll 1
         for (int e = 0; e < 4; ++e) {
           const float x = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
