@@ -1,0 +1,88 @@
+"""qg_paged_attention on int8 pages: what a row does not see (later blocks,
+their scales, the padding behind the last token) must not reach it, and scales
+of 0 and very small ones keep their bits. Rows go to the prompt kernel with one
+CTA a tile (many KV heads) and with clusters (room for many tokens), and few
+rows to the other kernels.
+
+Tolerance: ``test_gpu_paged_attention.reference`` over the tokens that the rows
+of a check see, so that its terms in max|V| are theirs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import qg_synth
+from oracle import qg_oracle as O
+from tests.gpu_util import dev, host64
+from tests.paged_util import Cache, bf16_bits, starts
+from tests.test_gpu_paged_attention import ROOM, reference
+
+pytestmark = pytest.mark.gpu
+
+qg = pytest.importorskip("weight_only_quantized_03_b200")
+
+BF = torch.bfloat16
+# query and KV heads, room for tokens: tiles of 128 rows, of 64 rows, clusters
+FORMS = [(8, 8, 0), (16, 8, 0), (2, 2, ROOM), (4, 2, ROOM)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def attend(cache, q, n, lens, H, scale):
+    """(out, q as bf16) of the rows q."""
+    D = cache.D
+    q = O.bf16_bits_to_f64(bf16_bits(q))
+    kv, table = cache.upload(qg)
+    qd = torch.from_numpy(q).to(BF).cuda()
+    out = torch.full_like(qd, 55.0)
+    ws = torch.empty(qg.qg_paged_attention_workspace_size(D), dtype=torch.uint8, device="cuda")
+    qg.qg_paged_attention(kv, table, dev(np.array(lens, np.int32)), qd, out, H, scale, ws,
+                          row_start=dev(starts(n)))
+    return host64(out), q
+
+
+def check(cache, got, q, n, lens, H, scale, splits=()):
+    """Rows of each sequence against the oracle; `splits`: tokens at which a
+    sequence's rows are checked apart, by what they see."""
+    r0 = starts(n)
+    for b in range(len(n)):
+        k, v = cache.values(b, lens[b])
+        first = lens[b] - n[b]  # the first row's token
+        ends = [t for t in splits if first < t < lens[b]] + [lens[b]]
+        at = first
+        for end in ends:
+            rows = slice(r0[b] + at - first, r0[b] + end - first)
+            want, tol = reference(q[rows], k[:, :end], v[:, :end], H, cache.Hkv, cache.D, scale,
+                                  "int8", False, True)
+            err = np.abs(got[rows] - want)
+            assert np.all(err <= tol), (b, at, end, float((err / tol).max()))
+            at = end
+
+
+def _rows(H, D, T, seed):
+    return qg_synth.gaussian((T, H * D), 1.0, seed)
+
+
+@pytest.mark.parametrize("small", [0.0, 2.0 ** -126, 1e-30])
+@pytest.mark.parametrize("H,Hkv,room", FORMS)
+def test_a_block_of_small_keys_that_rows_do_not_see(H, Hkv, room, small):
+    """Blocks of K with scale 0 (what an append of zeros stores) or a very
+    small one, behind rows whose own scores lie far below 0: their softmax
+    goes by the scores that they see."""
+    D, L = 128, 300
+    cache = Cache("int8", 1, Hkv, D, 64, room or L, [L], 1100)
+    cache.k = np.where(cache.k < 0, cache.k, -1 - np.maximum(cache.k, 0).clip(0, 126)).astype(np.int8)
+    blocks = [2, 6, 11, 13, 17]
+    for j in blocks:
+        p, r = cache.place(0, 16 * j)
+        if small == 0.0:
+            cache.k[p, :, r:r + 16] = 0
+        cache.ks[p, :, r // 16] = small
+    q = np.abs(_rows(H, D, L, 1101)) * 3.0
+    got, q = attend(cache, q, [L], [L], H, 0.5)
+    check(cache, got, q, [L], [L], H, 0.5, splits=[16 * j for j in blocks])

@@ -417,7 +417,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       }
       const bool part = key0 + j * kKeys + kKeys > common;
       const int left = lim - key0 - j * kKeys;  // visible tokens of this step (or more, or none)
-      // The row's largest score. A negative scale turns the order round.
+      // The row's largest score. A negative scale turns the order round. Blocks
+      // that the row does not see at all stay out: under a scale of 0 (zeros
+      // appended) or near it the least score would become one near 0.
       auto largest = [&]() {
         float top = -FLT_MAX;
 #pragma unroll
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
               if (32 * h + 16 * q + i >= left) y = -FLT_MAX;
               x[i & 3] = fmaxf(x[i & 3], y);
             }
-            top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * fabsf(k));
+            const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * fabsf(k);
+            if (32 * h + 16 * q < left) top = fmaxf(top, y);
           }
         }
         return top;
