@@ -86,3 +86,24 @@ def test_a_block_of_small_keys_that_rows_do_not_see(H, Hkv, room, small):
     q = np.abs(_rows(H, D, L, 1101)) * 3.0
     got, q = attend(cache, q, [L], [L], H, 0.5)
     check(cache, got, q, [L], [L], H, 0.5, splits=[16 * j for j in blocks])
+
+
+@pytest.mark.parametrize("H,Hkv,room", FORMS)
+@pytest.mark.parametrize("v_scale", [1.0])
+def test_values_of_zero(H, Hkv, room, v_scale):
+    """Blocks of V with scale 0: the first ones (a whole step, and more than
+    one), every block of a head, and the last ones; the others with ordinary and
+    with the smallest scales."""
+    D, L = 128, 300
+    cache = Cache("int8", 1, Hkv, D, 64, room or L, [L], 1120)
+    cache.vs *= np.float32(v_scale)
+    for h, (lo, hi) in ((0, (0, 80)), (1, (0, 304))):
+        for t in range(lo, min(hi, L), 16):
+            p, r = cache.place(0, t)
+            cache.v[p, h, r:r + 16] = 0
+            cache.vs[p, h, r // 16] = 0.0
+    q = _rows(H, D, L, 1121)
+    got, q = attend(cache, q, [L], [L], H, 1 / math.sqrt(D))
+    G = H // Hkv
+    assert np.all(got.reshape(L, H, D)[:, G:2 * G] == 0.0)
+    check(cache, got, q, [L], [L], H, 1 / math.sqrt(D), splits=[80])

@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
           tmem_ld32(sc + 32 * h, s);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float k = ks[2 * h + q], w = I8 ? vs[2 * h + q] * inv : 1.f;
+            const float k = ks[2 * h + q], w = I8 ? vs[2 * h + q] * inv * 2048.f : 1.f;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               float y[2];
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       };
       auto form = [&]() {
-        const float inv = I8 ? 2048.f / r : 1.f;
+        const float inv = I8 ? 1.f / r : 1.f;  // (finite from the least r, 2^-126, on)
         if (part)
           weights(std::true_type(), inv);
         else
