@@ -5,7 +5,9 @@ CTA a tile (many KV heads) and with clusters (room for many tokens), and few
 rows to the other kernels.
 
 Tolerance: ``test_gpu_paged_attention.reference`` over the tokens that the rows
-of a check see, so that its terms in max|V| are theirs."""
+of a check see, so that its terms in max|V| are theirs; and 2^-134, half of bf16's
+step below 2^-126 (its least numbers are multiples of 2^-133), which rounding by
+2^-8 |o| does not count."""
 import math
 
 import numpy as np
@@ -59,7 +61,7 @@ def check(cache, got, q, n, lens, H, scale, splits=()):
             rows = slice(r0[b] + at - first, r0[b] + end - first)
             want, tol = reference(q[rows], k[:, :end], v[:, :end], H, cache.Hkv, cache.D, scale,
                                   "int8", False, True)
-            err = np.abs(got[rows] - want)
+            err, tol = np.abs(got[rows] - want), tol + 2.0 ** -134
             assert np.all(err <= tol), (b, at, end, float((err / tol).max()))
             at = end
 
@@ -88,8 +90,23 @@ def test_a_block_of_small_keys_that_rows_do_not_see(H, Hkv, room, small):
     check(cache, got, q, [L], [L], H, 0.5, splits=[16 * j for j in blocks])
 
 
+@pytest.mark.parametrize("v_scale", [1e-6, 1e-9, 1e-13])
 @pytest.mark.parametrize("H,Hkv,room", FORMS)
-@pytest.mark.parametrize("v_scale", [1.0])
+def test_small_values_with_lengths_that_end_inside_a_step(H, Hkv, room, v_scale):
+    """What lies behind the last token does not set the unit of V."""
+    D = 128
+    lens = [17, 1, 65, 70, 33, 130, 48, 200] * (3 if not room else 1)
+    n = [x if i % 3 else min(x, 20) for i, x in enumerate(lens)]
+    cache = Cache("int8", len(n), Hkv, D, 64, room or 200, lens, 1110)
+    cache.vs *= np.float32(v_scale)
+    q = _rows(H, D, sum(n), 1111)
+    got, q = attend(cache, q, n, lens, H, 1 / math.sqrt(D))
+    assert np.abs(got).max() > 0
+    check(cache, got, q, n, lens, H, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("H,Hkv,room", FORMS)
+@pytest.mark.parametrize("v_scale", [1.0, 2.0 ** -116])
 def test_values_of_zero(H, Hkv, room, v_scale):
     """Blocks of V with scale 0: the first ones (a whole step, and more than
     one), every block of a head, and the last ones; the others with ordinary and

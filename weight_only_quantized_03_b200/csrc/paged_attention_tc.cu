@@ -552,7 +552,8 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     if (ok && steps && !wait_bar(&S.o_full, (uint32_t)(steps - 1) & 1u, abort)) ok = false;
     if (!ok) *abort = 1;
     fence_after();
-    const float f = l != 0.f ? (I8 ? r * (1.f / 2048.f) : 1.f) / l : 0.f;
+    // (V's unit apart from 1 / l: as one factor they would lose bits below 2^-126)
+    const float f = l != 0.f ? 1.f / l : 0.f, unit = I8 ? r * (1.f / 2048.f) : 1.f;
     const float lost = __int_as_float(0x7FC00000);
     S.m[tid] = m;
     S.l[tid] = ok ? l : lost;
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         for (int i = 0; i < 32; ++i) o[i] = 0;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        o[i] = __float_as_uint(ok ? __uint_as_float(o[i]) * f : lost);
+        o[i] = __float_as_uint(ok ? __uint_as_float(o[i]) * f * unit : lost);
       if (Z > 1) {  // to where Q and K were: every product is done
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         const int id = __shfl_sync(0xffffffffu, places, from + (lane & 3));
         const bool scaled = warp == 4 && id >= 0;
         scale = load_if(P.ks + id, scaled, id == -1 ? __int_as_float(0x7FC00000) : 1.f);
-        vscale = load_if(P.vs + id, scaled, 1.f);
+        vscale = load_if(P.vs + id, scaled, 0.f);  // (no block: nothing sets the unit of V)
       };
       if (steps) load(0);
       for (int j = 0; j < steps; ++j) {
