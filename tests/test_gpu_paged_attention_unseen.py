@@ -124,3 +124,38 @@ def test_values_of_zero(H, Hkv, room, v_scale):
     G = H // Hkv
     assert np.all(got.reshape(L, H, D)[:, G:2 * G] == 0.0)
     check(cache, got, q, [L], [L], H, 1 / math.sqrt(D), splits=[80])
+
+
+@pytest.mark.parametrize("H,Hkv,room", FORMS)
+def test_a_block_of_large_values_that_rows_do_not_see(H, Hkv, room):
+    """V of a later block is 2^30 times as large: rows before it keep the
+    bits that they would have without it."""
+    D, L = 128, 300
+    cache = Cache("int8", 1, Hkv, D, 64, room or L, [L], 1130)
+    blocks = [3, 7, 10, 15]
+    for i, j in enumerate(blocks):
+        p, r = cache.place(0, 16 * j)
+        cache.vs[p, :, r // 16] *= np.float32(2.0 ** (20 + 10 * i))
+    q = _rows(H, D, L, 1131)
+    got, q = attend(cache, q, [L], [L], H, 1 / math.sqrt(D))
+    check(cache, got, q, [L], [L], H, 1 / math.sqrt(D), splits=[16 * j for j in blocks])
+
+
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_few_rows_over_such_blocks(n):
+    """The kernels for few rows: the same contents."""
+    D, L, H, Hkv = 128, 300, 4, 2
+    cache = Cache("int8", 2, Hkv, D, 64, L, [L, 17], 1140)
+    for j, (ks, vs) in {1: (0.0, 2.0 ** 30), 17: (2.0 ** -126, 0.0), 18: (0.0, 2.0 ** 20)}.items():
+        p, r = cache.place(0, 16 * j)
+        cache.ks[p, :, r // 16] = ks
+        if ks == 0.0:
+            cache.k[p, :, r:r + 16] = 0
+        cache.vs[p, :, r // 16] *= np.float32(vs)
+        if vs == 0.0:
+            cache.v[p, :, r:r + 16] = 0
+    cache.vs[cache.table[1, 0], :, :2] *= np.float32(1e-9)
+    m = [n, min(n, 17)]
+    q = _rows(H, D, sum(m), 1141)
+    got, q = attend(cache, q, m, [L, 17], H, 1 / math.sqrt(D))
+    check(cache, got, q, m, [L, 17], H, 1 / math.sqrt(D), splits=[16 * 17, 16 * 18])

@@ -489,13 +489,15 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         else
           weights(std::false_type(), inv);
       };
+      // V's largest scale among the blocks that the row sees: a later block's
+      // must not cost it bits
       float vtop = 0.f;
       if constexpr (I8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (fabsf(vs[i]) <= FLT_MAX) vtop = fmaxf(vtop, fabsf(vs[i]));
+          if (16 * i < left && fabsf(vs[i]) <= FLT_MAX) vtop = fmaxf(vtop, fabsf(vs[i]));
       }
-      const bool wider = I8 && vtop > r;  // the same in all threads
+      const bool wider = I8 && vtop > r;
       // Every warp waits for every product once, in order (a parity tells a
       // phase only from its neighbours): here if O has to be rescaled, else at
       // the end of the step, when it has long been done.
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
       // The weights are formed with the reference as it is; only if one of a
       // warp's rows has outgrown it (or V's unit grows, or there is none yet)
       // the largest scores are looked for, and the weights formed again.
-      bool again = j == 0 || wider;
+      bool again = j == 0 || (I8 && __any_sync(0xffffffffu, wider));
       if (!again) {
         form();
         again = __any_sync(0xffffffffu, most > (float)(1 << (int)kMargin));
