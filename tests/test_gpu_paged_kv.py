@@ -387,3 +387,66 @@ def test_append_with_row_starts_that_decrease_stays_within_its_rows(kind):
     got = cache.download(kv)
     np.testing.assert_array_equal(got[0][spare], cache.k[spare])
     np.testing.assert_array_equal(got[2][spare], cache.v[spare])
+
+
+def _codes32(codes, s_old, o, x):
+    """kv_block_append as include/qg.h states it in fp32: (codes, scale) of a
+    block [16, D] after rows x (fp32 values) at place o."""
+    f = np.float32
+    codes, s_old = codes.copy(), f(s_old) if o else f(0)
+    s = max(s_old, np.abs(x).max() / f(127))
+    s = s if s >= f(2.0 ** -126) else f(0)
+    n = len(x)
+    if s == 0:
+        codes[:o + n] = 0
+        return codes, s
+    if s != s_old:
+        codes[:o] = np.rint(codes[:o].astype(f) * (s_old / s))
+    codes[o:o + n] = np.clip(np.rint(x / s), -127, 127)
+    return codes, s
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_codes_are_the_fp32_quotients(xt, D):
+    """Without norm and rotation every step is one fp32 operation, so codes
+    and scales are equal, also where x / s lies at a tie between two codes or
+    next to one: half the largest value and other odd multiples of s / 2."""
+    Hkv, page, n = 3, 32, [40, 1, 16, 9, 8, 5, 3]
+    lens = [45, 1, 16, 25, 31, 37, 8]
+    dt = torch.float32 if xt == "f32" else torch.bfloat16
+    f32 = lambda a: torch.from_numpy(a).to(dt).float().numpy()
+    rng = np.random.default_rng(D)
+    cache = Cache("int8", len(n), Hkv, D, page, 64, np.array(lens) - n, 600)
+    cache.ks *= np.float32(0.3)
+    x = f32(rng.standard_normal((sum(n), 2 * Hkv, D)).astype(np.float32) * 1.5)
+    # near ties: (k + 1/2) s for the scale of a row's own largest value
+    s = np.abs(x).max(-1, keepdims=True) / np.float32(127)
+    k = rng.integers(-127, 127, x.shape).astype(np.float32) + np.float32(0.5)
+    near = f32(k * s) if xt == "f32" else f32(np.sign(k) * np.abs(x).max(-1, keepdims=True) / 2)
+    near = np.nextafter(near, np.float32(9) * rng.integers(-1, 2, x.shape).astype(np.float32)) \
+        if xt == "f32" else near
+    x = np.where((rng.random(x.shape) < 0.5) & (np.abs(near) < np.abs(x).max(-1, keepdims=True)),
+                 near, x).astype(np.float32)
+    kv, table = cache.upload(qg)
+    xd = torch.from_numpy(x.reshape(sum(n), -1)).to(dt).cuda()
+    qg.qg_paged_kv_append(kv, table, dev(np.array(lens, np.int32)), xd[:, :Hkv * D],
+                          xd[:, Hkv * D:], row_start=dev(starts(n)), rotary_dim=0)
+    got, r0 = cache.download(kv), starts(n)
+    ties = 0
+    for which, (pages, scales) in enumerate(((cache.k, cache.ks), (cache.v, cache.vs))):
+        for b in range(len(n)):
+            p0 = lens[b] - n[b]
+            rows = x[r0[b]:r0[b + 1], which * Hkv:(which + 1) * Hkv]
+            for t0 in range(p0 // BLOCK * BLOCK, lens[b], BLOCK):
+                lo, hi = max(t0, p0), min(t0 + BLOCK, lens[b])
+                p, r = cache.place(b, t0)
+                for h in range(Hkv):
+                    want, s = _codes32(pages[p, h, r:r + BLOCK], scales[p, h, r // BLOCK],
+                                       lo - t0, rows[lo - p0:hi - p0, h])
+                    q = rows[lo - p0:hi - p0, h] / s
+                    ties += int((np.abs(np.abs(q - np.rint(q)) - 0.5) < 1e-4).sum())
+                    assert got[2 * which + 1][p, h, r // BLOCK] == s, (which, b, t0, h)
+                    np.testing.assert_array_equal(got[2 * which][p, h, r:hi - t0 + r],
+                                                  want[:hi - t0], err_msg=str((which, b, t0, h)))
+    assert ties > 20

@@ -137,15 +137,40 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int (&c)[EPL]) {
   for (int j = 0; j < EPL; ++j) c[j] = (int)(int8_t)(w[j >> 2] >> (8 * (j & 3)));
 }
 
-// EPL codes x * f: the sum with 1.5 * 2^23 rounds the product to the nearest
-// integer, whose low byte is the code. |x * f| is at most 127 but for
-// roundings (f = 1 / scale, and the scale is a normal number), so nothing is
-// clamped; f = 0 gives 0 (and any code under a NaN scale).
+// The sum with 1.5 * 2^23 rounds a value to the nearest integer, ties to even;
+// its low byte is the code.
+__device__ __forceinline__ float rounded(float y) { return __fadd_rn(y, 12582912.f); }
+
+// EPL codes rint(y) (y times the scales' ratio, rounded to fp32).
 template <int EPL>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[EPL], float f) {
-  uint32_t c[EPL];
+__device__ __forceinline__ void times_codes(const float (&y)[EPL], float ratio,
+                                            uint32_t (&c)[EPL]) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) c[j] = __float_as_uint(fmaf(x[j], f, 12582912.f));
+  for (int j = 0; j < EPL; ++j) c[j] = __float_as_uint(rounded(__fmul_rn(y[j], ratio)));
+}
+// EPL codes rint(x / s), the quotient rounded to fp32. |x| <= 127 s but for
+// roundings, so nothing is clamped. below and above are 1 / s times 1 -+ 2^-22:
+// with u = 2^-24, |x| above >= |x / s| (1 + 4u) (1 - u)^2 > |x / s| (1 + u), so the
+// rounded quotient lies between x below and x above, and where these round to one
+// integer it is the code. Only else, next to a tie, a value is divided (4099 int8
+// prompt rows: 31.2 us with x * (1 / s), 34.7 with a division for each value, 32.4
+// so). below = above = 0 (scale 0) gives 0; under a NaN scale any code.
+template <int EPL>
+__device__ __forceinline__ void quotient_codes(const float (&x)[EPL], float s, float below,
+                                               float above, uint32_t (&c)[EPL]) {
+  uint32_t tie = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    c[j] = __float_as_uint(fmaf(x[j], below, 12582912.f));
+    tie |= c[j] ^ __float_as_uint(fmaf(x[j], above, 12582912.f));
+  }
+  if (tie) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) c[j] = __float_as_uint(rounded(__fdiv_rn(x[j], s)));
+  }
+}
+template <int EPL>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&c)[EPL]) {
   if constexpr (EPL == 2) {
     *reinterpret_cast<uint16_t*>(p) = (uint16_t)__byte_perm(c[0], c[1], 0x40);
   } else {
@@ -291,6 +316,7 @@ __device__ __forceinline__ void put_cache(const float (&x)[NR][D / 32], int rows
     if (top >= 0x7F800000u || s_old != s_old) s = __int_as_float(0x7FC00000);
     if (s < FLT_MIN) s = 0.f;
     const float inv = s > 0.f ? 1.f / s : 0.f;  // (false for a NaN scale)
+    const float below = inv * (1.f - 0x1p-22f), above = inv * (1.f + 0x1p-22f);
     if (half == 0 && o > 0 && s != s_old) {  // the block's earlier rows to the new scale
       const float ratio = s > 0.f ? s_old / s : 0.f;
       for (int r = 0; r < o; ++r) {
@@ -299,13 +325,17 @@ __device__ __forceinline__ void put_cache(const float (&x)[NR][D / 32], int rows
         float y[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) y[j] = (float)c[j];
-        store_codes<EPL>(block + r * D + lane * EPL, y, ratio);
+        uint32_t w[EPL];
+        times_codes<EPL>(y, ratio, w);
+        store_codes<EPL>(block + r * D + lane * EPL, w);
       }
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       if (r >= rows) break;
-      store_codes<EPL>(block + (first + r) * D + lane * EPL, x[r], inv);
+      uint32_t w[EPL];
+      quotient_codes<EPL>(x[r], s, below, above, w);
+      store_codes<EPL>(block + (first + r) * D + lane * EPL, w);
     }
     if (half == 0) {
       __syncwarp();  // every lane has read s_old
