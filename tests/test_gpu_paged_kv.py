@@ -450,3 +450,29 @@ def test_append_codes_are_the_fp32_quotients(xt, D):
                     np.testing.assert_array_equal(got[2 * which][p, h, r:hi - t0 + r],
                                                   want[:hi - t0], err_msg=str((which, b, t0, h)))
     assert ties > 20
+
+
+@pytest.mark.parametrize("which", ["q_norm", "k_norm"])
+def test_append_refuses_norm_weights_of_another_type(which):
+    """A refused call leaves the cache as it was; bf16 bits as int16 are the
+    same weights."""
+    D = 64
+    cache = Cache("int8", 1, 1, D, 16, 16, [3], 700)
+    kv, table = cache.upload(qg)
+    x = torch.randn((1, 3 * D), device="cuda")
+    w = (1 + 0.1 * torch.randn(D, device="cuda"))
+    lens, out = dev(np.array([4], np.int32)), torch.zeros((1, D), device="cuda")
+    call = lambda w: qg.qg_paged_kv_append(kv, table, lens, x[:, D:2 * D], x[:, 2 * D:],
+                                           q=x[:, :D], q_out=out, **{which: w})
+    for bad in (w.half(), w, w[:32].bfloat16()):
+        with pytest.raises(ValueError, match="64 bf16 values"):
+            call(bad)
+    for a, b in zip(cache.download(kv), (cache.k, cache.ks, cache.v, cache.vs)):
+        np.testing.assert_array_equal(a, b)
+    call(w.bfloat16())
+    first = [out.clone()] + [torch.from_numpy(a) for a in cache.download(kv)]
+    kv, _ = cache.upload(qg)
+    call(w.bfloat16().view(torch.int16))
+    again = [out] + [torch.from_numpy(a) for a in cache.download(kv)]
+    assert all(torch.equal(a.cpu().nan_to_num(7.5), b.cpu().nan_to_num(7.5))
+               if a.is_floating_point() else torch.equal(a, b) for a, b in zip(first, again))

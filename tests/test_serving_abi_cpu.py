@@ -163,3 +163,14 @@ def test_sample_filtered_refusals():
         st, msg = call(**kw)
         assert st == code and word in msg, (kw, st, msg)
     assert call(B=0, logits=None)[0] == qg.QG_OK
+
+
+def test_norm_weights_are_bf16():
+    """fp16 weights have two bytes as well, but other bits: refused."""
+    for good in (torch.ones(64).bfloat16(), torch.ones(64).bfloat16().view(torch.int16),
+                 torch.ones(64).bfloat16().view(torch.uint16)):
+        qg._check_norm(good, 64)
+    for bad in (torch.ones(64).half(), torch.ones(64), torch.ones(32).bfloat16(),
+                torch.ones(128).bfloat16()[::2]):
+        with pytest.raises(ValueError, match="64 bf16 values"):
+            qg._check_norm(bad, 64)

@@ -470,6 +470,16 @@ def _rows_of(name, t, width):
                      f"{tuple(shape)} with strides {t.stride()}")
 
 
+_BF16_BITS = (_bf16, torch.int16, torch.uint16)  # bf16 values, or their bits
+
+
+def _check_norm(w, D):
+    """A norm weight of D bf16 values (float16 has another meaning per bit)."""
+    if w.dtype not in _BF16_BITS or w.numel() != D or not w.is_contiguous():
+        raise ValueError(f"q_norm and k_norm must be contiguous, {D} bf16 values (or their bits as "
+                         f"int16), not {w.dtype} {tuple(w.shape)}")
+
+
 class PagedKV:
     """A pool of K/V pages of one layer (``qg_paged_kv``): ``k_pages`` and
     ``v_pages`` [num_pages, kv_heads, page_size, head_dim], bfloat16, or int8
@@ -550,6 +560,7 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
     to the pages of ``kv`` (a PagedKV) and write the rotated q to q_out
     [T, H*D] (fp32 or bf16; q itself if the types match). Rows of q, k and v
     (fp32 or bf16, one type) may lie apart, as slices of one projection do.
+    q_norm and k_norm: D bf16 values (or their bits as int16).
     page_table int32 [B, max_pages]; kv_len int32 [B] counts the new rows;
     row_start int32 [B+1], or None for one row per sequence. ``rotary_dim``
     None: the whole head."""
@@ -582,8 +593,8 @@ def qg_paged_kv_append(kv, page_table, kv_len, k, v, row_start=None, q=None, q_o
             _check_device(dev, ("k", k), ("v", v), ("q", q), ("q_out", q_out), ("q_norm", q_norm),
                           ("k_norm", k_norm))
     for w in (q_norm, k_norm):
-        if w is not None and (w.numel() != D or w.element_size() != 2 or not w.is_contiguous()):
-            raise ValueError(f"q_norm and k_norm must be {D} bf16 values")
+        if w is not None:
+            _check_norm(w, D)
     xdt = _TYPES.get(dt)
     if xdt is None:
         _dt(k)
