@@ -247,3 +247,24 @@ def test_crowded_rows_of_the_largest_vocabularies(V):
     u = np.array([0.9, 0.7, 0.4, 0.9], np.float32)
     check(l, u)
     check(l, u, top_p=[0.9, 0.65, 0.97, 1.0], top_k=[0, 0, 0, V - 5], min_p=[0, 0, 0, 1e-3])
+
+
+@pytest.mark.parametrize("V", [300, 5000, 151936])
+def test_a_min_p_below_the_weights_resolution(V):
+    """min-p keeps every weight of at least min_p, also those that the sums
+    round to 0: from 2^-40 down to the least positive float, with the other
+    filters off and on, over values whose weights reach far below it."""
+    rng = np.random.default_rng(V + 3)
+    B = 10
+    l = (rng.standard_normal((B, V)) * 30).astype(np.float32)
+    l[8, 3] = np.inf
+    l[9, rng.random(V) < 0.3] = -np.inf
+    min_p = np.array([1e-12, 3e-14, 1e-15, 1e-20, 1e-30, 1e-37, 1e-40, 1.5e-45, 1e-20, 1e-20],
+                     np.float32)
+    assert 0 < min_p.min() < 2.0 ** -148
+    u = rng.random(B).astype(np.float32)
+    for k in (0, 60, V - 7):
+        for p in (1.0, 0.97):
+            check(l, u, top_k=np.full(B, k), top_p=np.full(B, p), min_p=min_p)
+    check(l, u, temperature=np.full(B, 0.05), min_p=min_p)
+    check(l, u, temperature=np.full(B, np.inf), min_p=min_p)

@@ -203,7 +203,7 @@ struct Row {
     const double x = ((double)v - (double)top) * per_unit;  // (the difference is exact)
     return v == top ? 0.0 : x;
   }
-  // 2^(x / 64 + up) for x <= 0 down to -64 (frac + 2): table-driven (Tang, "Table-driven
+  // 2^(x / 64 + up) for x <= 0, the result above 2^-1022: table-driven (Tang, "Table-driven
   // implementation of the exponential function", 1989): x = n + f with n an
   // integer, 2^(n / 64) from the table of 64 and the exponent, e^(f ln2 / 64)
   // by its series up to the fifth power (the next term is below 2^-54).
@@ -221,8 +221,10 @@ struct Row {
     const double y = fma(s, p, s);
     return __hiloint2double(__double2hiint(y) + (((k >> 6) + up) << 20), __double2loint(y));
   }
+  // A candidate's weight for min-p, whose least positive value is 2^-149: as it
+  // is down to 2^-1020, also where it is 0 in fixed point.
   __device__ __forceinline__ double weight(float v) const {
-    return weighs(v) ? power(steps(v), 0) : 0.0;
+    return power(fmax(steps(v), -1020.0 * kSteps), 0);
   }
   // Whether v's weight can be more than 0.
   __device__ __forceinline__ bool weighs(float v) const {
@@ -364,6 +366,8 @@ struct Work {
   // The slice's weights (and, with `count`, counts) into the histogram.
   __device__ __forceinline__ void weigh(const Row& R, double min_p, bool count) const {
     unsigned above = 0;
+    // (a weight of at least this is not 0 in fixed point)
+    const double least = __hiloint2double((1023 - R.frac) << 20, 0);
     each_adding([&](const float (&v)[4], int) {
       int b[4];
       u64 w[4];
@@ -378,11 +382,18 @@ struct Work {
         if (count && v[e] > -INFINITY) atomicAdd(&S.hist_c[b[e]], 1u);
         if (w[e]) add_weight(S, b[e], w[e]);
       }
-      if (min_p > 0.0)  // (scaling by 2^frac is exact: this is power(x, 0) >= min_p)
+      if (min_p >= least) {  // (scaling by 2^frac is exact: this is power(x, 0) >= min_p)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           above += w[e] && __hiloint2double(__double2hiint(y[e]) - (R.frac << 20),
                                             __double2loint(y[e])) >= min_p;
+      } else if (min_p > 0.0) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const float x = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+          above += x > -INFINITY && R.weight(x) >= min_p;
+        }
+      }
     });
     if (min_p > 0.0) push_above(above);
   }
