@@ -554,7 +554,7 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  * inside that kernel are bounded in time (1 s), and one that gives up makes its
  * rows NaN.
  * Shape rules: H % kv_heads == 0, T * H <= 2^30, B <= 65536, scale > 0, and
- * (T * H / 8 + B * kv_heads) * (max_pages * page_size / 128 + 1) < 2^31. */
+ * (T * H / 8 + B * kv_heads) * (max_pages * page_size / 128 + 3) < 2^31. */
 size_t qg_paged_attention_workspace_size(int head_dim);
 qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* page_table, int max_pages,
                              const int32_t* kv_len, const int32_t* row_start, const void* q,

@@ -174,3 +174,22 @@ def test_norm_weights_are_bf16():
                 torch.ones(128).bfloat16()[::2]):
         with pytest.raises(ValueError, match="64 bf16 values"):
             qg._check_norm(bad, 64)
+
+
+@pytest.mark.parametrize("B,T,H,Hkv,pages", [(54606, 16777284, 8, 2, 84), (40555, 33554509, 8, 2, 41),
+                                             (1, 1 << 27, 8, 8, 6), (1, 1000, 16, 8, 1 << 18),
+                                             (65536, 65536, 64, 64, 340), (3, 70, 2, 2, 1 << 19)])
+def test_attention_takes_what_the_header_allows(B, T, H, Hkv, pages):
+    """The rule on rows, heads and pages, at fp32 (where no call goes to the
+    kernel that it does not bound), with q missing: a call within the rule is
+    refused for that, one beyond for its sizes."""
+    kv = _kv(kv_heads=Hkv, page_size=192)
+    room = lambda pages: (T * H // 8 + B * Hkv) * (pages * 192 // 128 + 3)
+    most = next(p for p in range(pages, -1, -1) if room(p) < 1 << 31)
+    call = lambda pages: _attend(kv, row_start=FAKE, B=B, T=T, H=H, max_pages=pages, q=None,
+                                 qdt=qg.QG_F32)
+    st, msg = call(most)
+    assert st == qg.QG_ERR_INVALID_ARGUMENT and "q or out" in msg, (st, msg)
+    if 2 * room(most) > 1 << 31 and 192 * (2 * most + 8) < 0x7FFFFFFF - 65536:
+        st, msg = call(2 * most + 8)
+        assert st == qg.QG_ERR_UNSUPPORTED_SHAPE and "too many" in msg, (st, msg)

@@ -1114,6 +1114,12 @@ extern "C" qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* pa
              QG_ERR_UNSUPPORTED_SHAPE, "%s: num_pages=%d: the pool is too large", who,
              kv->num_pages);
   if (B == 0 || T == 0) return QG_OK;
+  const bool exact = q_dtype == QG_F32 || out_dtype == QG_F32;
+  const pa::Plan plan =
+      pa::plan(B, T, H, Hkv, D, kv->dtype == QG_KV_INT8, (long long)max_pages * kv->page_size, exact);
+  QG_REQUIRE(plan.pieces >= 0, QG_ERR_UNSUPPORTED_SHAPE,
+             "%s: T=%d rows of H=%d heads over max_pages=%d pages are too many for one call", who,
+             T, H, max_pages);
   if (qg_status s = pk::check_pool_pointers(who, kv)) return s;
   QG_REQUIRE(page_table && kv_len && q && out, QG_ERR_INVALID_ARGUMENT,
              "%s: null page_table, kv_len, q or out", who);
@@ -1125,12 +1131,6 @@ extern "C" qg_status qg_paged_attention(const qg_paged_kv* kv, const int32_t* pa
   QG_REQUIRE(ws && ws_bytes >= need, QG_ERR_WORKSPACE_TOO_SMALL,
              "%s: workspace of %zu bytes given, %zu needed", who, ws_bytes, need);
   QG_REQUIRE(aligned(ws, 256), QG_ERR_MISALIGNED, "%s: ws not 256-byte aligned", who);
-  const bool exact = q_dtype == QG_F32 || out_dtype == QG_F32;
-  const pa::Plan plan =
-      pa::plan(B, T, H, Hkv, D, kv->dtype == QG_KV_INT8, (long long)max_pages * kv->page_size, exact);
-  QG_REQUIRE(plan.pieces >= 0, QG_ERR_UNSUPPORTED_SHAPE,
-             "%s: T=%d rows of H=%d heads over max_pages=%d pages are too many for one call", who,
-             T, H, max_pages);
   pa::Params P = {};
   P.q = q;
   P.out = out;
