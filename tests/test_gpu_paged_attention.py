@@ -492,3 +492,51 @@ def test_bad_pages_and_lengths_among_prompt_rows(kind):
                               True)
         m = rows.stop - rows.start
         assert np.all(np.abs(got[rows] - want[:m]) <= tol[:m])
+
+
+@pytest.mark.parametrize("room", [0, 20000])
+@pytest.mark.parametrize("xt,ot", [(BF, BF), (F32, F32), (F32, BF), (BF, F32)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinite_keys_and_values_that_a_row_sees(D, xt, ot, room):
+    """bf16 pages, one row: an infinite V value makes that dim infinite (NaN
+    where both signs meet), whatever terms the weights are carried in; a K row
+    with a score of -inf is as if it were not there, one with +inf gives NaN."""
+    H, Hkv, L = 4, 2, 300
+    cache = Cache("bf16", 2, Hkv, D, 64, room or L, [L, L], 1200)
+    v_bad = {5: (0x7F80, [0, 3]), 130: (0xFF80, [1, 3]), 299: (0x7F80, [D - 1])}
+    for t, (bits, dims) in v_bad.items():
+        p, r = cache.place(0, t)
+        cache.v[p, 0, r, dims] = bits
+    q = qg_synth.gaussian((2, H * D), 1.0, 1201)
+    qv = q if xt == F32 else O.bf16_bits_to_f64(bf16_bits(q))
+    # sequence 1: token 77's score is -inf for KV head 0's first query head (and
+    # the second one, by the sign it gets), token 200's NaN for KV head 1's
+    sign = qv[1].reshape(H, D)
+    qv = np.asarray(qv, np.float64).copy()
+    qv[1].reshape(H, D)[1, 9] = abs(sign[1, 9]) * np.sign(sign[0, 9])
+    p, r = cache.place(1, 77)
+    cache.k[p, 0, r, 9] = 0xFF80 if sign[0, 9] > 0 else 0x7F80
+    p, r = cache.place(1, 200)
+    cache.k[p, 1, r, 9] = 0x7F80 if sign[2, 9] > 0 else 0xFF80
+    kv, table = cache.upload(qg)
+    qd = torch.from_numpy(qv).to(xt).cuda()
+    out = torch.full((2, H * D), 55.0, dtype=ot, device="cuda")
+    ws = torch.empty(qg.qg_paged_attention_workspace_size(D), dtype=torch.uint8, device="cuda")
+    qg.qg_paged_attention(kv, table, dev(np.array([L, L], np.int32)), qd, out, H, 1 / math.sqrt(D),
+                          ws)
+    got, exact = host64(out).reshape(2, H, D), F32 in (xt, ot)
+    args = (H, Hkv, D, 1 / math.sqrt(D), "bf16", exact, ot == BF)
+    with np.errstate(invalid="ignore"):
+        k, v = cache.values(0, L)
+    hit = sorted({d for _, dims in v_bad.values() for d in dims})
+    want, tol = reference(qv[:1], k, np.where(np.isfinite(v), v, 0.0), *args)
+    keep = np.ones((H, D), bool)
+    keep[:2, hit] = False
+    assert np.all(np.abs(got[0] - want.reshape(H, D))[keep] <= tol.reshape(H, D)[keep])
+    assert np.isposinf(got[0, :2, [0, D - 1]]).all() and np.isneginf(got[0, :2, 1]).all()
+    assert np.isnan(got[0, :2, 3]).all()
+    k, v = (np.delete(a, 77, 1) for a in cache.values(1, L))
+    k[1] = np.where(np.isfinite(k[1]), k[1], 0.0)
+    want, tol = reference(qv[1:], k, v, *args)
+    assert np.all(np.abs(got[1] - want.reshape(H, D))[:2] <= tol.reshape(H, D)[:2])
+    assert np.isnan(got[1, 2]).all()

@@ -280,14 +280,17 @@ struct Walk {
         }
       }
     }
+    // (bf16 pages: an infinite K value makes its term of q infinite in s, which
+    // says it all; times a lower term of 0 or the other sign it is noise)
     if constexpr (QS > 1) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += rest[e];
+      for (int e = 0; e < 4; ++e) s[e] += I8 ? rest[e] : fminf(fmaxf(rest[e], -FLT_MAX), FLT_MAX);
     }
   }
 
-  // bf16 pages, a tile that some columns see in part, with V values that are
-  // not finite: 0 * NaN must not reach the columns that do not see them, so
+  // bf16 pages, V values that are not finite in a tile that some columns see in
+  // part, or whose weights have several terms: 0 * inf must reach neither the
+  // columns that do not see them nor an infinite sum by way of a lower term, so
   // the products are formed one by one (never taken with finite values).
   static __device__ __forceinline__ void accumulate_seen(State<D>& S, const float (&p)[4],
                                                       const uint4 (&vr)[4][VC], int lane) {
@@ -318,17 +321,20 @@ struct Walk {
 
   __device__ __forceinline__ void weigh(State<D>& S, float (&p)[4], bool part) {
     if constexpr (!I8) {
-      if (part) {
-        bool odd = false;
+      if (PS > 1 || part) {
+        // (0 * x is NaN for these alone: one instruction for two values)
+        __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+        const __nv_bfloat162 zero = z;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < VC; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < (VB >= 16 ? 4 : 2); ++e) {
               const uint32_t x = word(vr[i][c], e);
-              odd |= (x & 0x7F800000u) == 0x7F800000u || (x & 0x7F80u) == 0x7F80u;
+              z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), zero, z);
             }
+        const bool odd = (*reinterpret_cast<const uint32_t*>(&z) & 0x7FFF7FFFu) != 0;
         if (__any_sync(0xffffffffu, odd)) {
           accumulate_seen(S, p, vr, lane);
           return;
