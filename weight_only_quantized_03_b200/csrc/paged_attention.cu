@@ -104,6 +104,33 @@ __device__ __forceinline__ uint32_t take16(float& lo, float& hi) {
   }
 }
 
+// Four weights in PS bf16 terms, each but the last one cut off, not rounded, and
+// at least 2^-126 where the weight is not 0: so a lower term is never 0 or of
+// the other sign beside an infinite V value, whose sum would be NaN.
+template <int PS>
+__device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&b)[PS][2]) {
+  float rest[4], least[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    rest[i] = p[i];
+    least[i] = fminf(p[i], FLT_MIN);
+  }
+#pragma unroll
+  for (int e = 0; e < PS; ++e) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = e + 1 < PS ? __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u) : rest[i];
+      if (e > 0) h[i] = fmaxf(h[i], least[i]);
+      rest[i] -= h[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      b[e][i] = e + 1 < PS ? __byte_perm(__float_as_uint(h[2 * i]), __float_as_uint(h[2 * i + 1]), 0x7632u)
+                           : mm::pack_bf16(h[2 * i], h[2 * i + 1]);
+  }
+}
+
 // Visible tokens of column c of the item's sequence. Columns past the last
 // one (their q is zero, nothing is stored for them) see everything, so that
 // they do not make a tile partly masked.
@@ -288,9 +315,8 @@ struct Walk {
     }
   }
 
-  // bf16 pages, V values that are not finite in a tile that some columns see in
-  // part, or whose weights have several terms: 0 * inf must reach neither the
-  // columns that do not see them nor an infinite sum by way of a lower term, so
+  // bf16 pages, a tile that some columns see in part, with V values that are
+  // not finite: 0 * NaN must not reach the columns that do not see them, so
   // the products are formed one by one (never taken with finite values).
   static __device__ __forceinline__ void accumulate_seen(State<D>& S, const float (&p)[4],
                                                       const uint4 (&vr)[4][VC], int lane) {
@@ -321,7 +347,7 @@ struct Walk {
 
   __device__ __forceinline__ void weigh(State<D>& S, float (&p)[4], bool part) {
     if constexpr (!I8) {
-      if (PS > 1 || part) {
+      if (part) {
         // (0 * x is NaN for these alone: one instruction for two values)
         __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
         const __nv_bfloat162 zero = z;
@@ -342,10 +368,19 @@ struct Walk {
       }
     }
     uint32_t b[PS][2];
+    if constexpr (I8 || PS == 1) {
+#pragma unroll
+      for (int e = 0; e < PS; ++e) {
+        b[e][0] = take16<I8>(p[0], p[1]);
+        b[e][1] = take16<I8>(p[2], p[3]);
+      }
+    } else {
+      split_weights<PS>(p, b);
+    }
 #pragma unroll
     for (int e = 0; e < PS; ++e) {
-      b[e][0] = transpose8x8(take16<I8>(p[0], p[1]));
-      b[e][1] = transpose8x8(take16<I8>(p[2], p[3]));
+      b[e][0] = transpose8x8(b[e][0]);
+      b[e][1] = transpose8x8(b[e][1]);
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
