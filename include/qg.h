@@ -546,9 +546,10 @@ qg_status qg_paged_kv_gather(const qg_paged_kv* kv, const int32_t* page_table, i
  *            serves calls that run one after another (one stream), not
  *            calls that may overlap.
  * Precision: bf16 q and out: operands of the tensor cores are exact (codes,
- * bf16 values, q) but for the softmax weights (fp16 with int8 pages, bf16
- * with bf16 pages); sums, maxima and scales in fp32. With an fp32 q or out,
- * q and the weights are carried in several 16-bit terms (22 bits or more).
+ * bf16 values, q) but for the softmax weights (fp16 with int8 pages; with
+ * bf16 pages two bf16 terms, 16 bits, and one, 8 bits, on tcgen05); sums,
+ * maxima and scales in fp32. With an fp32 q or out, q and the weights are
+ * carried in several 16-bit terms (22 bits or more).
  * Larger calls with head_dim <= 128, bf16 q and out and more than 8 row-head
  * pairs of a KV head per sequence (prompts, mostly) run on tcgen05; the waits
  * inside that kernel are bounded in time (1 s), and one that gives up makes its

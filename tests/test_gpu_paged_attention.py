@@ -540,3 +540,28 @@ def test_infinite_keys_and_values_that_a_row_sees(D, xt, ot, room):
     want, tol = reference(qv[1:], k, v, *args)
     assert np.all(np.abs(got[1] - want.reshape(H, D))[:2] <= tol.reshape(H, D)[:2])
     assert np.isnan(got[1, 2]).all()
+
+
+@pytest.mark.parametrize("D,H,Hkv,n,lens,cap", [
+    (64, 16, 16, [1, 1, 1], [1500, 300, 7], 0), (128, 16, 8, [1, 1], [700, 33], 0),
+    (128, 8, 2, [1, 1], [700, 33], 20000), (256, 4, 2, [1, 2], [300, 40], 0),
+    (64, 6, 2, [1, 2, 0, 1], [1000, 15, 0, 129], 20000),
+])
+def test_weights_of_bf16_pages_keep_16_bits(D, H, Hkv, n, lens, cap):
+    """Single tokens and a few rows with bf16 q and out: a weight is cut to
+    bf16 (2^-7) and its rest rounded to bf16 (2^-8 of that, at most): within
+    2^-15 of it. The tolerance is that of exact weights, with sum p |v| taken from
+    its difference to the one with 8 bits."""
+    cache = Cache("bf16", len(n), Hkv, D, 64, cap or max(lens), lens, 1210)
+    got, q = run(cache, n, lens, H, BF, BF, 1211)
+    r0 = starts(n)
+    for b in range(len(n)):
+        if not n[b]:
+            continue
+        rows = slice(r0[b], r0[b + 1])
+        k, v = cache.values(b, lens[b])
+        args = (q[rows], k, v, H, Hkv, D, 1 / math.sqrt(D), "bf16")
+        want, tol = reference(*args, True, True)
+        pv = (reference(*args, False, True)[1] - tol) / (1.01 * (2.0 ** -8 - 2.0 ** -22))
+        err = np.abs(got[rows] - want)
+        assert np.all(err <= tol + 2.0 ** -15 * pv), (b, float((err - tol).max()))

@@ -26,9 +26,11 @@
 // largest, fp32 q takes two fp16 terms (22 bits). Weights times V's scale
 // are brought into fp16's range by a running power of two r >= |scale| and
 // 2^11: they keep 11 bits down to 2^-25 of the largest, where bf16 would
-// keep 8. bf16 pages: bf16 operands, fp32 q and weights in three bf16 terms.
-// With a bf16 output the weights take one term, with an fp32 output two
-// (int8 pages) or three (bf16 pages); the denominator sums them unrounded.
+// keep 8. bf16 pages: bf16 operands, fp32 q in three bf16 terms, the weights in two
+// (16 bits). With an fp32 output the weights take two terms (int8 pages) or three
+// (bf16 pages); the denominator sums them unrounded. (One term for bf16 pages with a
+// bf16 output: 7 x 1500 of 64 11.3 in place of 11.5 us, 32 x 2048 54.5 and 54.8, and
+// errors of 2.3e-3 of the largest value in place of its rounding's 1.7e-3.)
 //
 // The softmax is online per column in fp32, with a lazy maximum: the
 // reference only moves (and the accumulators are only rescaled) when a score
@@ -404,13 +406,14 @@ struct Walk {
         a2 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x5410u);
         a3 = __byte_perm(word(vr[2][c], e), word(vr[3][c], e), 0x7632u);
       }
-      // The tensor core's adds truncate. One term: 16 tokens an add, and what a
-      // bf16 result shows of it is nothing. Several: the tile's sum is formed
-      // by itself, smallest term first, and added to the running one with
-      // rounding, which keeps a long cache's sum at fp32's accuracy (32749
+      // The tensor core's adds truncate. Terms added to the running sum, 16 tokens an
+      // add: what a bf16 result shows of that is nothing. For an fp32 one the tile's
+      // sum is formed by itself, smallest term first, and added to the running one
+      // with rounding, which keeps a long cache's sum at fp32's accuracy (32749
       // tokens: 1.3e-6 off with the terms added to the running sum).
-      if constexpr (PS == 1) {
-        mma<I8>(S.o[i], a0, a1, a2, a3, b[0][0], b[0][1]);
+      if constexpr (QS == 1) {
+#pragma unroll
+        for (int e = PS - 1; e >= 0; --e) mma<I8>(S.o[i], a0, a1, a2, a3, b[e][0], b[e][1]);
       } else {
         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1106,11 +1109,11 @@ inline Plan plan(int B, int T, int H, int Hkv, int D, bool i8, long long cap, bo
 
 template <int D, bool I8>
 cudaError_t launch(const Params& P, const Plan& p, bool exact, cudaStream_t st) {
-  constexpr int E = I8 ? 2 : 3;  // terms of fp32 q and weights
+  constexpr int E = I8 ? 2 : 3, W = I8 ? 1 : 2;  // terms of fp32 q and weights; of the weights
   if (p.prompt) return launch_prompt(P, D, I8, st);
   if (exact)
     return p.z ? launch_cluster<D, I8, E, E>(P, p.z, st) : launch_split<D, I8, E, E>(P, st);
-  return p.z ? launch_cluster<D, I8, 1, 1>(P, p.z, st) : launch_split<D, I8, 1, 1>(P, st);
+  return p.z ? launch_cluster<D, I8, 1, W>(P, p.z, st) : launch_split<D, I8, 1, W>(P, st);
 }
 
 // The largest number of pieces times columns any call of the head size uses.
