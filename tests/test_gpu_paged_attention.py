@@ -565,3 +565,33 @@ def test_weights_of_bf16_pages_keep_16_bits(D, H, Hkv, n, lens, cap):
         pv = (reference(*args, False, True)[1] - tol) / (1.01 * (2.0 ** -8 - 2.0 ** -22))
         err = np.abs(got[rows] - want)
         assert np.all(err <= tol + 2.0 ** -15 * pv), (b, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("case", [
+    ("int8", 128, 64, 16, 8, [100, 37, 1, 0, 250], [400, 37, 290, 5, 250], F32, F32, 0),
+    ("bf16", 128, 64, 16, 8, [100, 37, 1, 0, 250], [400, 37, 290, 5, 250], F32, F32, 0),
+    ("int8", 64, 32, 12, 4, [130, 7, 300], [500, 900, 300], F32, BF, 0),
+    ("bf16", 64, 16, 6, 2, [200, 150], [200, 620], BF, F32, 0),
+    ("int8", 256, 32, 8, 2, [90, 3, 110], [200, 333, 110], BF, BF, 0),
+    ("bf16", 256, 64, 4, 2, [70, 140], [300, 140], F32, F32, 0),
+    ("int8", 128, 64, 4, 1, [60] * 5, [60 + 75 * i for i in range(5)], F32, F32, 20000),
+    ("bf16", 128, 128, 4, 2, [45, 0, 210], [700, 3, 210], F32, BF, 20000),
+], ids=lambda c: f"{c[0]}-d{c[1]}-h{c[3]}.{c[4]}-n{c[5][:3]}-room{c[9]}")
+def test_hundreds_of_rows_in_fp32_or_with_wide_heads(case):
+    """What the prompt kernel does not take, in hundreds of rows: many items a
+    piece of the line, cuts inside items and before their first chunk."""
+    kind, D, page, H, Hkv, n, lens, xt, ot, room = case
+    check(kind, D, page, H, Hkv, n, lens, xt, ot, 1220, cap=room or max(lens), pad=3)
+
+
+@pytest.mark.parametrize("xt,ot", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("lens", [[1], [16], [128], [129], [1, 128, 1, 129, 2, 127],
+                                  [46 + i for i in range(25)], [257] * 40, [3000, 1, 1, 1]],
+                         ids=lambda l: f"{len(l)}x{l[0]}")
+def test_cuts_of_the_line(lens, xt, ot):
+    """Room for 20000 tokens, so that the line is cut: items of one chunk and
+    of the least and the most tokens of one, pieces of a single unit, pieces
+    that begin or end in an item's part that stands for no chunk."""
+    for n in (1, 2):
+        rows = [min(n, x) for x in lens]
+        check("int8", 64, 64, 4, 2, rows, lens, xt, ot, 1230, cap=20000)
