@@ -194,3 +194,73 @@ def test_the_loop_from_a_graph_gives_the_same_bits(kind):
     for a, b in zip(runs[0][2], runs[1][2]):
         for x, y in zip(a, b):
             np.testing.assert_array_equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("n", [[1, 1, 2], [40, 1, 70]])
+def test_rows_before_the_first_and_behind_the_last_sequence_stay(kind, n):
+    """row_start begins past 0 and ends before T: append, attention and
+    gather leave the rows outside alone (and do not read them: they are NaN),
+    the rows inside are those of the same call without them."""
+    dtype = torch.int8 if kind == "int8" else torch.bfloat16
+    lens = [x + 13 * i for i, x in enumerate(n)]
+    g = torch.Generator(device="cuda").manual_seed(31)
+    B, T, lead, tail = len(n), sum(n), 21, 5
+    most = max(lens) // PAGE + 1
+    table = torch.randperm(B * most, generator=g, device="cuda").view(B, most).int()
+    x = torch.randn((T, (H + 2 * HKV) * D), generator=g, device="cuda").bfloat16()
+    ws = torch.empty(qg.qg_paged_attention_workspace_size(D), dtype=torch.uint8, device="cuda")
+    ld, runs = dev(np.array(lens, np.int32)), []
+    for before, behind in ((0, 0), (lead, tail)):
+        kv = qg.PagedKV.empty(B * most, PAGE, HKV, D, dtype)
+        for t in (kv.k_pages, kv.v_pages, kv.k_scales, kv.v_scales):
+            if t is not None:
+                t.zero_()
+        all_rows = before + T + behind
+        rows = slice(before, before + T)
+        wide = torch.full((all_rows, x.shape[1]), math.nan, dtype=torch.bfloat16, device="cuda")
+        wide[rows] = x
+        rs = dev(starts(n) + before)
+        full = lambda w, dt=torch.bfloat16: torch.full((all_rows, w), 55.0, dtype=dt, device="cuda")
+        q, out, k, v = full(H * D), full(H * D), full(HKV * D), full(HKV * D)
+        a, b, c = wide.split((H * D, HKV * D, HKV * D), 1)
+        qg.qg_paged_kv_append(kv, table, ld, b, c, row_start=rs, q=a, q_out=q)
+        qg.qg_paged_attention(kv, table, ld, q, out, H, SCALE, ws, row_start=rs)
+        qg.qg_paged_kv_gather(kv, table, ld - torch.tensor(n, device="cuda").int(), rs, k, v)
+        torch.cuda.synchronize()
+        for t in (q, out, k, v):
+            assert bool((t[:before] == 55.0).all()) and bool((t[before + T:] == 55.0).all())
+            assert bool(torch.isfinite(t).all())
+        runs.append([t[rows].clone() for t in (q, out, k, v)] +
+                    [t for t in (kv.k_pages, kv.v_pages) if t is not None])
+    assert all(torch.equal(s, t) for s, t in zip(*runs))
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("heads,rows", [(256, 1), (16, 70), (4, 2), (3, 33)])
+def test_a_row_of_q_that_is_not_finite_stays_alone(kind, heads, rows):
+    """One query head's values NaN or infinite: that head's row is NaN, its
+    neighbours in a tile are as they were."""
+    dtype = torch.int8 if kind == "int8" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(32)
+    L, hkv = 130, 1
+    kv = qg.PagedKV.empty(9, PAGE, hkv, D, dtype)
+    table = torch.arange(9, device="cuda", dtype=torch.int32).view(1, 9)
+    x = torch.randn((L, 2 * hkv * D), generator=g, device="cuda")
+    qg.qg_paged_kv_append(kv, table, dev(np.array([L], np.int32)), x[:, :D], x[:, D:],
+                          row_start=dev(starts([L])))
+    q = torch.randn((rows, heads * D), generator=g, device="cuda").bfloat16()
+    ws = torch.empty(qg.qg_paged_attention_workspace_size(D), dtype=torch.uint8, device="cuda")
+    outs = []
+    for bad in (False, True):
+        if bad:
+            q.view(rows, heads, D)[rows // 2, heads // 2, 3] = math.inf
+            q.view(rows, heads, D)[rows - 1, 0, :] = math.nan
+        out = torch.empty_like(q)
+        qg.qg_paged_attention(kv, table, dev(np.array([L], np.int32)), q, out, heads, SCALE, ws,
+                              row_start=dev(starts([rows])))
+        outs.append(out.view(rows, heads, D))
+    same = torch.ones((rows, heads), dtype=torch.bool, device="cuda")
+    same[rows // 2, heads // 2] = same[rows - 1, 0] = False
+    assert torch.equal(outs[0][same], outs[1][same])
+    assert bool(torch.isnan(outs[1][~same]).all())
