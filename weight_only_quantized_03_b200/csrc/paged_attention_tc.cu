@@ -22,7 +22,7 @@
 // two CTAs on an SM take about 2900 for a step each. The step's products are
 // 640 cycles of tensor core (S reads both operands from shared memory), and a
 // scheduler issues every other cycle. 4096 rows over 4096 tokens (16 query, 8
-// KV heads of 128): 390 TFLOP/s. Measured and slower: eight row warps with
+// KV heads of 128): 113 us, 607 TFLOP/s. Measured and slower: eight row warps with
 // half of a step's keys each (2053 rows of five users: 69 against 60 us), 256
 // pairs a CTA (80), and the line of all steps cut into equal pieces with a
 // merge behind (108: a step's scheduling and the pieces' parts cost more than
@@ -30,8 +30,8 @@
 //
 // Balance: long tiles start first, and where the tiles do not fill the GPU a
 // cluster of up to eight CTAs shares a tile's keys; their results meet through
-// distributed shared memory (128 rows over 32768 tokens: 914 us with one CTA a
-// tile, 131 with eight).
+// distributed shared memory (128 rows over 32768 tokens: 698 us with one CTA a
+// tile, 119 with eight).
 //
 // A value of V that is infinite or NaN at a token that some of the rows do
 // not see must not reach them as 0 * inf: it is left out of the operand, and
@@ -867,9 +867,10 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
 
 // CTAs of a cluster that share a tile's keys: as many as fit the GPU at once
 // (two an SM) with four steps each, should the sequences fill their pages.
-// Measured with 1, 2, 4 and 8 (us): 128 rows over 32768 tokens 914, 456, 235,
-// 137; 512 over 8192 151, 98, 69, 97; 2053 rows of five users 60, 71, 105, 226;
-// 300 rows over themselves 14, 16, 19, 39.
+// Measured with 1, 2, 4 and 8 (us): 128 rows over 32768 tokens 698, 310, 182,
+// 119; 512 over 8192 148, 82, 67, 95; 2053 rows of five users 50, 55, 100, 208;
+// 300 rows over themselves 14, 15, 20, 37. (Page tables far wider than the
+// sequences get the larger ones: 300 rows with room for 32768 tokens 20.)
 static int prompt_cluster(const Params& P) {
   const long long tiles = ((long long)P.T * P.G / kRows + P.B / 2 + 1) * P.Hkv;
   const long long steps = (long long)P.max_pages * P.bpp * kBlock / kKeys;

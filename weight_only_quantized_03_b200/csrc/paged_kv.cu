@@ -15,9 +15,9 @@
 // while the first rows are under way.
 //
 // What bounds it: a few rows, the chain launch, lengths, table, rows, stores
-// (32 sequences of one token, 16 + 2 x 8 heads of 128, with the read-back 6.3
+// (32 sequences of one token, 16 + 2 x 8 heads of 128, with the read-back 6.4
 // us); prompts, latency and issue, a lane's 8 rows in turn (16000 int8 rows of
-// 8 users 88 us with the read-back, 3.7 TB/s).
+// 8 users 90 us with the read-back, 3.6 TB/s).
 //
 // The mapping of CTAs to (sequence, block) needs no host knowledge of the
 // lengths: n rows touch at most n/16 + 2 blocks, so slot ranges
@@ -434,8 +434,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, const NewRows
 
 // CTAs an SM: bf16 rows of 128 take 80 registers with the next item's rows
 // ahead (us with three CTAs so, three without, four: 16000 int8 rows of 8 users
-// 88, 94, 107; 600 rows 11.3, 11.5, 12.6); fp32 rows are faster as four at 64
-// (4099 rows 37.6 against 41.2).
+// 90, 99, 121; 4099 rows 31.6, 32.4, 35.2; 600 rows 11.9, 12.0, 13.6); fp32 rows
+// are a little faster as four at 64 (4099 rows 39.6 against 40.2).
 constexpr int append_ctas(int D, bool xf32) { return D > 128 ? 2 : xf32 ? 4 : 3; }
 
 template <int D, bool I8, bool XF32>

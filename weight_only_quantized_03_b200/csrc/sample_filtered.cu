@@ -23,10 +23,10 @@
 //
 // What bounds it: one row, the chain of phases (151936 values over 16 CTAs, 46
 // thousand cycles: reading 6, weights and histogram 11, its sums through
-// distributed shared memory 7, border bins 5, collection 8, sort and search 6);
-// full batches, four shared-memory atomics and a float64 exp a value (32 rows
-// of 151936 over 128 CTAs, 52 us: 20 of them). 30 us a row, 160 rows of 2048
-// 12.9.
+// distributed shared memory 7, border bins 5, collection 8, sort and search 6,
+// the rest barriers); full batches, four shared-memory atomics and a float64 exp
+// a value (32 rows of 151936 over 128 CTAs, 52 us: 20 of them). 24-29 us a row, by
+// how many members the border bins have, 160 rows of 2048 13.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
