@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
     mbar_arrive(&S.q_full);
 
     const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-    float m = -FLT_MAX, l = 0.f, r = FLT_MIN;
+    // V's unit: 2048 / r is finite from 2^-115 on (at a scale of 2^-126 weights keep
+    // their 11 bits down to 2^-14 of the largest, not 2^-25)
+    float m = -FLT_MAX, l = 0.f, r = 0x1p-115f;
     for (int j = 0; j < steps; ++j) {
       const int b = j & 1;
       if (!wait_bar(&S.s_full[b], (uint32_t)(j >> 1) & 1u, abort)) {
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
           tmem_ld32(sc + 32 * h, s);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float k = ks[2 * h + q], w = I8 ? vs[2 * h + q] * inv * 2048.f : 1.f;
+            const float k = ks[2 * h + q], w = I8 ? vs[2 * h + q] * inv : 1.f;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               float y[2];
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kPThreads, 2) prompt_kernel(const __grid_const
         most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       };
       auto form = [&]() {
-        const float inv = I8 ? 1.f / r : 1.f;  // (finite from the least r, 2^-126, on)
+        const float inv = I8 ? 2048.f / r : 1.f;
         if (part)
           weights(std::true_type(), inv);
         else
